@@ -98,6 +98,7 @@ def lib() -> ctypes.CDLL:
         L.qlinear_forward_ex.restype = ci
         L.qlinear_forward_ex.argtypes = [vp, i64, i64, i64, vp, vp, vp, ci, ci, ci, vp, ci, vp, ci, vp, sz,
                                          ctypes.POINTER(Schedule), vp]
+        ffn8.bind(L)
         _lib = L
     return _lib
 
@@ -596,3 +597,11 @@ def linear_a8(x: torch.Tensor, pw: PackedWeight, bias: torch.Tensor | None = Non
                                     _ptr(out), od, _ptr(workspace), workspace.numel(),
                                     -1 if tile is None else int(tile), _stream(x.device)), "qlinear_forward_a8")
     return out.reshape(*lead, pw.N)
+
+
+# ---- 8-bit feed-forward operators --------------------------------------------------------
+
+from . import ffn8  # noqa: E402
+from .ffn8 import *  # noqa: E402,F401,F403
+
+__all__ += ffn8.__all__

@@ -29,6 +29,11 @@ SOURCES = [   # slowest first, so the parallel build starts them first
     "ql_misc.hip",
     "ql_quant.hip",
     "ql_lora.hip",
+    "ql_i8_gemm.hip",
+    "ql_i8_back.hip",
+    "ql_norm.hip",
+    "ql_i8_pack.hip",
+    "ql_i8_api.hip",
 ]
 
 ARCH = "gfx950"

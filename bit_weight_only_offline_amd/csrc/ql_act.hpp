@@ -1,0 +1,68 @@
+// Gated activations and small store helpers shared by the per-channel INT8 kernels.
+//
+// Both activations have the form  act(g) = g * p,  p = logistic(z):  z = g for SiLU, and
+// z = 2 sqrt(2/pi) (g + 0.044715 g^3) for the tanh form of GELU, since (1 + tanh(z / 2)) / 2
+// is the logistic function of z.  So  act'(g) = p + g p (1 - p) z'.  The argument of z is
+// held to |g| <= 1e4, far past where p is 0 or 1 in float32, so that no cube overflows; a
+// comparison with NaN is false, so NaN stays NaN.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ql_decode.hpp"
+
+namespace ql {
+
+enum : int { GATE_SILU = 0, GATE_GELU = 1 };
+
+constexpr float GELU_A = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+constexpr float GELU_B = 0.044715f;
+
+// 1 / (1 + exp(-z)): the hardware exponential and reciprocal, each within about 1 ulp
+// (the results are rounded to bf16, or compared at float32 tolerances far above that)
+__device__ inline float logistic(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+
+__device__ inline float gate_clamp(float g) { return g > 1e4f ? 1e4f : (g < -1e4f ? -1e4f : g); }
+
+__device__ inline float gate_act(float g, int act) {
+    const float c = gate_clamp(g);
+    return g * logistic(act == GATE_SILU ? c : GELU_A * (c + GELU_B * c * c * c));
+}
+
+// act(g) and act'(g)
+__device__ inline void gate_act_grad(float g, int act, float &a, float &da) {
+    const float c = gate_clamp(g);
+    const float z = act == GATE_SILU ? c : GELU_A * (c + GELU_B * c * c * c);
+    const float dz = act == GATE_SILU ? 1.0f : GELU_A * (1.0f + 3.0f * GELU_B * c * c);
+    const float p = logistic(z);
+    a = g * p;
+    da = p + c * p * logistic(-z) * dz;
+}
+
+__device__ inline uint32_t pack_bf16(float lo, float hi) {
+    return uint32_t(__builtin_bit_cast(uint16_t, (__bf16)lo)) | (uint32_t(__builtin_bit_cast(uint16_t, (__bf16)hi)) << 16);
+}
+
+// Four consecutive values of one row at element index i, of which the first `count` exist.
+// vec: the row starts four-element aligned, so one store serves.
+__device__ inline void store4_bf16(uint16_t *p, int64_t i, const float (&v)[4], int count, bool vec) {
+    if (vec && count >= 4) {
+        *reinterpret_cast<u32x2 *>(p + i) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (r < count) reinterpret_cast<__bf16 *>(p)[i + r] = (__bf16)v[r];
+    }
+}
+__device__ inline void store4_f32(float *p, int64_t i, const float (&v)[4], int count, bool vec) {
+    if (vec && count >= 4) {
+        *reinterpret_cast<f32x4 *>(p + i) = f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (r < count) p[i + r] = v[r];
+    }
+}
+
+}  // namespace ql

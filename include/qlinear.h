@@ -383,6 +383,109 @@ ql_status qlinear_grouped_forward(const void *x, int64_t T, const int32_t *token
                                   void *out, ql_dtype out_dtype, void *workspace,
                                   size_t workspace_bytes, void *stream);
 
+/*
+ * 8-bit feed-forward operators.  Activations are int8 codes [M, K] with one float32 scale a
+ * token (qlinear_quantize_activations() and qlinear_block_norm() make them), weights int8
+ * codes [N, K] with one float32 scale a channel, K a multiple of 32 and at most 131071 (so
+ * that the int32 sums are exact for all codes in -128 .. 127), N at most 2^20.
+ *
+ * qlinear_i8_pack() lays a weight out once for every product below; a gated weight holds
+ * two weights of the same shape, up (codes, scales) and gate (gate_codes, gate_scales),
+ * interleaved.  gate_codes and gate_scales are both NULL for a plain weight.  Canonical
+ * arrays need the alignment of their elements only.  qlinear_i8_unpack() inverts it
+ * bit-exactly.
+ */
+ql_status qlinear_i8_packed_bytes(int64_t N, int64_t K, int gated, size_t *w_bytes, size_t *s_bytes);
+ql_status qlinear_i8_pack(int64_t N, int64_t K, const void *codes, const float *scales, const void *gate_codes,
+                          const float *gate_scales, void *packed_w, void *packed_s, void *stream);
+ql_status qlinear_i8_unpack(int64_t N, int64_t K, const void *packed_w, const void *packed_s, void *codes,
+                            float *scales, void *gate_codes, float *gate_scales, void *stream);
+
+/*
+ * y[m, n] = scales[m] s[n] sum_k codes[m, k] q[n, k] + bias[n]
+ *   codes      int8 [M, K] row-major, 16-byte aligned     scales  float32 [M]
+ *   bias       bf16 [N] or NULL                           out     [M, N] bf16 or float32
+ *   workspace  qlinear_i8_workspace_bytes() bytes, 256-byte aligned (NULL if 0): int32
+ *              partial sums where the input dimension is split over workgroups
+ * The sums are exact integers, so results do not depend on the schedule.  M = 0 is a no-op.
+ */
+ql_status qlinear_i8_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated, size_t *bytes);
+ql_status qlinear_i8_forward(const void *codes, const float *scales, int64_t M, int64_t N, int64_t K,
+                             const void *packed_w, const void *packed_s, const void *bias, void *out,
+                             ql_dtype out_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gated feed-forward projection: up and gate as two such products of the same codes,
+ * h = act(gate) * up, in one kernel.  SiLU, or GELU in its tanh form.
+ *   bias  bf16 [2N] = [up | gate] or NULL
+ *   out   [M, N] bf16 or float32
+ *   raw   NULL, or bf16 [M, 2N] = [up | gate] before the activation, which the backward
+ *         pass reads
+ */
+typedef enum { QL_GATE_SILU = 0, QL_GATE_GELU = 1 } ql_gate_act;
+ql_status qlinear_i8_gated_forward(const void *codes, const float *scales, int64_t M, int64_t N, int64_t K,
+                                   const void *packed_w, const void *packed_s, const void *bias, ql_gate_act act,
+                                   void *out, ql_dtype out_dtype, void *raw, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/*
+ * Backward passes with frozen weights, with respect to the dequantised activations
+ * (scales[m] * codes[m, k]; the quantisation itself is passed straight through).
+ *   linear   dx[m, k] = sum_n dy[m, n] s[n] q[n, k]
+ *   gated    dup = dh act(gate), dgate = dh up act'(gate), draw = [dup | dgate],
+ *            dx = dup . Up + dgate . Gate
+ * The weight enters the bf16 matrix cores as s[n] q[n, k] rounded to bf16, sums are float32.
+ *   dy, dh  bf16 [M, N]; raw, draw bf16 [M, 2N]; dx bf16 [M, K]; all 16-byte aligned
+ *   draw's column sums are the gradient of the biases.
+ *   workspace  qlinear_i8_backward_workspace_bytes() bytes, 256-byte aligned (NULL if 0)
+ */
+ql_status qlinear_i8_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated, size_t *bytes);
+ql_status qlinear_i8_backward(const void *dy, int64_t M, int64_t N, int64_t K, const void *packed_w,
+                              const void *packed_s, void *dx, void *workspace, size_t workspace_bytes, void *stream);
+ql_status qlinear_i8_gated_backward(const void *dh, const void *raw, int64_t M, int64_t N, int64_t K,
+                                    const void *packed_w, const void *packed_s, ql_gate_act act, void *dx, void *draw,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The step between two blocks of a residual stream: norm of the finished block's output y,
+ * its gate, the scaled residual, and the norm that the next block reads.
+ *   t  = y * rsqrt(mean(y^2) + eps) * post_weight     (post_weight NULL: t = y)
+ *   r' = residual_scale * residual + gate * t         (y NULL: no block, r' = scale * residual)
+ *   x  = r' * rsqrt(mean(r'^2) + eps) * pre_weight    (pre_weight NULL: no x)
+ *   residual, residual_out  [R, C] bf16 or float32 (residual_dtype); may be the same buffer
+ *   y            bf16 [R, C]
+ *   post_weight, pre_weight  [C], gate [gates, C]: float32 or bf16 (param_dtype); row r uses
+ *                gate r / (R / gates); gates = 0 and gate NULL for none
+ *   x            bf16 [R, C]; or codes int8 [R, C] and scales float32 [R] in its place:
+ *                s = max|x| / 127, q = clamp(rint(x / s), -127, 127), an all-zero row has
+ *                s = 0 and codes 0, a row with NaN or infinity s = NaN and codes 0
+ *   C at most 32768; eps > 0.  All arithmetic is float32; x is formed from r' before r' is
+ *   rounded.  Rows whose addresses allow it (C a multiple of 8, 16-byte alignment) take
+ *   16-byte accesses.  R = 0 is a no-op.
+ */
+ql_status qlinear_block_norm(const void *residual, ql_dtype residual_dtype, const void *y, const void *post_weight,
+                             const void *pre_weight, const void *gate, ql_dtype param_dtype, int64_t gates,
+                             float residual_scale, float eps, int64_t R, int64_t C, void *residual_out, void *x,
+                             void *codes, float *scales, void *stream);
+
+/*
+ * Its backward pass.
+ *   dx            bf16 [R, C], gradient of x (with pre_weight)
+ *   dresidual     gradient of r' from the rest of the network, or NULL for zero
+ *   residual_out  r' as the forward pass returned it; y as it was given
+ *   out: dresidual_in [R, C] (residual_dtype), dy bf16 [R, C] (with y), dpost, dpre float32
+ *        [C] and dgate float32 [gates, C] for the parameters that are given
+ *   workspace     qlinear_block_norm_backward_workspace_bytes() bytes, 256-byte aligned: the
+ *                 workgroups' column sums, which a second launch adds in a fixed order
+ */
+ql_status qlinear_block_norm_backward_workspace_bytes(int64_t R, int64_t C, int64_t gates, size_t *bytes);
+ql_status qlinear_block_norm_backward(const void *dx, const void *dresidual, const void *residual_out,
+                                      ql_dtype residual_dtype, const void *y, const void *post_weight,
+                                      const void *pre_weight, const void *gate, ql_dtype param_dtype, int64_t gates,
+                                      float residual_scale, float eps, int64_t R, int64_t C, void *dresidual_in,
+                                      void *dy, float *dpost, float *dpre, float *dgate, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
