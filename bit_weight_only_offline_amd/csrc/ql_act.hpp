@@ -40,8 +40,10 @@ __device__ inline void gate_act_grad(float g, int act, float &a, float &da) {
     da = p + c * p * logistic(-z) * dz;
 }
 
+// two float32 rounded to bf16 (to nearest even) in one conversion
 __device__ inline uint32_t pack_bf16(float lo, float hi) {
-    return uint32_t(__builtin_bit_cast(uint16_t, (__bf16)lo)) | (uint32_t(__builtin_bit_cast(uint16_t, (__bf16)hi)) << 16);
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
 
 // Four consecutive values of one row at element index i, of which the first `count` exist.

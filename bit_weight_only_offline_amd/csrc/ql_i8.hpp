@@ -46,9 +46,9 @@ inline I8Layout make_i8_layout(int64_t N, int64_t K, bool gated) {
 // Schedules of the forward products.
 //   kind 0 (few rows): one workgroup per NT column tiles over the whole input dimension,
 //          its WK wavefronts taking the chunks in turn; MT row tiles of 16
-//   kind 1 (tiles): WM x WN wavefronts, each MT x NT tiles of 16 x 16, operands staged
-//          through LDS, CPS chunks a stage and S stages
-struct I8Cfg { int kind, MT, NT, WK, WM, WN, CPS, S; };
+//   kind 1 (tiles): WM x WN wavefronts, each MT x NT tiles of 16 x 16, WK times on alternate
+//          chunks; operands staged through LDS, S stages
+struct I8Cfg { int kind, MT, NT, WK, WM, WN, S; };
 
 struct I8Plan {
     int cfg = 0;
@@ -69,28 +69,36 @@ struct I8Args {
     int M, N, K, ntiles, kchunks;
     int mtiles, nblocks, ks, cps;
     int act, out_f32;
-    int vec;                // rows of out (and raw) may be stored four channels at a time
+    int vec, vec8;          // rows of out (and raw) may be stored four / eight channels at a time
 };
 
 I8Plan make_i8_plan(const I8Layout &L, int64_t M);
 
-// Launch arguments of the backward products  dx = (dy * s) . q.
+// Rows of 64 bytes in LDS (four 16-byte pieces): piece p of row r sits at place
+// p ^ row_swizzle(r).  An operand read takes one piece of each of 16 rows with 16 lanes, four
+// such sets in one instruction, and the LDS serves 16 lanes at a time: either 16 consecutive
+// ones, or (as the conflict counter shows) lanes 0-3, 12-15, 20-23, 24-27 and their like.
+// With r / 4 negated both kinds of groups touch all 64 banks once; with r / 4 itself the
+// second kind meets twice in half of them.
+__host__ __device__ constexpr int row_swizzle(int r) { return (-(r >> 2)) & 3; }
+
+// Launch arguments of the backward products  dx = operand . q.
 struct I8BackArgs {
-    const uint16_t *dy;     // bf16, row stride ldy elements; gated: gate part `half` elements on
+    const uint16_t *dy;     // the operand: scaled gradients, bf16, rows of ldy elements in packed
+                            // row order, ldy a multiple of 8, zero past the last channel
     const uint8_t *w;
-    const float *s;
     uint16_t *dx;           // bf16 [M, K]
     float *part;            // float32 partial sums [ks][M][K] or null
-    int64_t ldy, half;
-    int M, N, K, ntiles, kchunks;
-    int mtiles, nblocks, ks, nps;   // nps: 64-row steps of the contraction per split
+    int64_t ldy;
+    int M, K, ntiles, kchunks;
+    int mtiles, nblocks, ks, nps;   // nps: 32-row steps of the contraction per split
 };
 
 struct I8BackPlan {
     int cfg = 0, mtiles = 1, nblocks = 1;
     int ks = 1, nps = 0;
-    int64_t Np = 0;                        // N rounded up to eight
-    size_t copy_bytes = 0, ws_bytes = 0;   // padded copy of dy (gated: du and dg), then partial sums
+    int64_t Np = 0;                           // N rounded up to eight (gated: to a tile)
+    size_t operand_bytes = 0, ws_bytes = 0;   // the operand, then partial sums
 };
 
 I8BackPlan make_i8_back_plan(const I8Layout &L, int64_t M);

@@ -5,13 +5,16 @@
 //            rows of both weights, up and gate tiles alternating as they are packed
 //
 // The product contracts over the weight's rows, across the direction it is packed in, and
-// needs it in bf16.  A workgroup therefore turns each 64-row step of its weight columns
+// needs it in bf16.  A workgroup therefore turns each 32-row step of its weight columns
 // into operand order once, through LDS, for all of its rows of dy: a thread takes the four
-// inputs of one 32-bit word from eight consecutive channels, and since a conversion picks
-// any byte of a word, the transposition costs no shuffles.  Per value: byte -> float32
-// (exact), one fused multiply-add (u - 128) s that rounds once, and half of a packed
-// rounding to bf16.  That bf16 rounding of the scaled weight is the only one before the
-// float32 sums; scaling dy instead would round as much and need a second copy of it.
+// inputs of one 32-bit word from four consecutive channels, and since a byte permute picks
+// any byte of a word, the transposition costs no shuffles of its own.
+//
+// int8 codes are exact in bf16, the channel scales are not: they are folded into dy (or du
+// and dg) in float32 before its rounding to bf16, in the pass that forms the product's
+// operand.  That rounding is the only one before the float32 sums.  (Scaling the codes
+// instead needs no pass over dy, but a multiplication and a rounding for every code in the
+// inner loop, where decoding is what keeps the matrix cores waiting.)
 #include <hip/hip_runtime.h>
 
 #include "ql_act.hpp"
@@ -24,25 +27,39 @@ namespace ql {
 namespace {
 
 constexpr uint32_t OUT_OF_RANGE = 0x80000000u;   // a buffer offset that reads as zero
-constexpr int NSTEP = 64;                        // weight rows (contraction) per step
+constexpr int NSTEP = 32;                        // weight rows (contraction) per step
+constexpr int BACK_KP = 256, BACK_KQ = 4;        // inputs per workgroup, and chunks of them
+constexpr int BACK_WAVES = 8;
 
-// One workgroup: MP = 16 MT WM rows of dy by KP = 16 NT WN inputs, the contraction in steps
-// of 64 packed rows (four tiles).  LDS, two buffers each: dy rows [MP][64] bf16 (XOR-swizzled
-// 16-byte pieces), packed tiles as loaded [4][KP / 64] KiB, and the bf16 operand
-// [KP / 16][2] KiB.  While step i is multiplied, the packed tiles of step i + 1 become its
-// operand and the loads of dy for i + 1 and of packed tiles for i + 2 are in flight; one
-// barrier a step.
-template <int WM, int WN, int MT, int NT, bool GATED, bool SPLIT>
-__global__ void __launch_bounds__(64 * WM * WN) i8_back_kernel(I8BackArgs a) {
-    constexpr int W = WM * WN, T = 64 * W;
-    constexpr int MP = 16 * MT * WM, KP = 16 * NT * WN, KQ = KP / 64;
-    static_assert(KP % 64 == 0, "whole chunks");
-    constexpr int NA = MP / 8, NR = 4 * KQ;          // 1 KiB loads a step
-    constexpr int A_BYTES = MP * 128, R_BYTES = NR * 1024, D_BYTES = KP * 128;
-    constexpr int NAW = (NA + W - 1) / W, NRW = (NR + W - 1) / W;
-    constexpr int TASKS = 2 * KP;                    // eight rows by four inputs each
+// An LDS store of 8 bytes.  Written as assembly text because the compiler, which cannot tell
+// the stages of the ring apart, would wait before every store for the buffer->LDS loads in
+// flight; the step's barrier waits for the stores (lgkmcnt), and nothing reads them sooner.
+__device__ inline void lds_store8(uint8_t *p, u32x2 v) {
+    const uint32_t at = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)p));
+    asm volatile("ds_write_b64 %0, %1" : : "v"(at), "v"(v) : "memory");
+}
+
+// LDS: dy rows [MP][32] bf16 and packed tiles [2][4] KiB, four stages each; the decoded
+// operand [16][1] KiB, two stages.
+constexpr int back_lds(int mp) { return 4 * (mp * 64 + 8 * 1024) + 2 * BACK_KP * 64; }
+
+// One workgroup: MP = 16 MT WM rows of dy by 256 inputs, the contraction in steps of 32
+// packed rows (two tiles).  While step s is multiplied out of registers, the operands of
+// step s + 1 are read into registers, each wavefront decodes one of the eight packed tiles
+// of step s + 2 (the one it loaded itself), and the buffer->LDS loads of dy for s + 4 and of
+// tiles for s + 5 are issued; one barrier a step.
+template <int WM, int WN, int MT, int NT, bool SPLIT>
+__global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) {
+    static_assert(WM * WN == BACK_WAVES && 16 * NT * WN == BACK_KP, "eight wavefronts over 256 inputs");
+    constexpr int MP = 16 * MT * WM;
+    constexpr int NA = MP / 16;                      // 1 KiB loads of dy a step
+    // fewer loads than wavefronts: some are issued twice (the same bytes to the same place),
+    // so that all wavefronts wait for the same count
+    constexpr int NAW = NA < BACK_WAVES ? 1 : NA / BACK_WAVES;
+    constexpr int PER_STEP = NAW + 1;
+    constexpr int A_BYTES = MP * 64, R_BYTES = 8 * 1024, D_BYTES = BACK_KP * 64;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    uint8_t *const ldsA = lds, *const ldsR = lds + 2 * A_BYTES, *const ldsD = ldsR + 2 * R_BYTES;
+    uint8_t *const ldsA = lds, *const ldsR = ldsA + 4 * A_BYTES, *const ldsD = ldsR + 4 * R_BYTES;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -57,87 +74,73 @@ __global__ void __launch_bounds__(64 * WM * WN) i8_back_kernel(I8BackArgs a) {
     const int band = lin / (8 * a.nblocks), in_band = lin - band * 8 * a.nblocks;
     const int band_rows = min(8, a.mtiles - 8 * band);
     const int mtile = 8 * band + in_band % band_rows, kblock = in_band / band_rows;
-    const int m0 = mtile * MP, kq0 = kblock * KQ;
+    const int m0 = mtile * MP, kq0 = kblock * BACK_KQ;
     const int m_here = min(MP, a.M - m0);
 
-    const int steps = (a.ntiles + 3) / 4;
+    const int steps = (a.ntiles + 1) / 2;
     const int st0 = SPLIT ? int(blockIdx.y) * a.nps : 0;
     const int st1 = SPLIT ? min(steps, st0 + a.nps) : steps;
 
     const __amdgpu_buffer_rsrc_t yr =
         make_rsrc(a.dy + int64_t(m0) * a.ldy, uint32_t(m_here) * uint32_t(a.ldy) * 2u);
 
-    auto yswz = [](int r) { return (r >> 1) & 7; };
-    // piece p of a step's 64 packed rows: rows 8 p .. 8 p + 7, tile p / 2
+    // piece p (eight packed rows) of row r of dy sits at piece p ^ row_swizzle(r)
+
     uint32_t y_off[NAW];
-    int y_col[NAW];
+    const int y_col = 8 * ((lane & 3) ^ row_swizzle(lane >> 2));
 #pragma unroll
     for (int q = 0; q < NAW; ++q) {
-        const int row = ((wv + W * q) % NA) * 8 + lane / 8, p = (lane % 8) ^ yswz(row);
-        y_col[q] = GATED ? 16 * (p >> 2) + 8 * (p & 1) : 8 * p;
-        y_off[q] = uint32_t(row) * uint32_t(a.ldy) * 2u + uint32_t(y_col[q]) * 2u +
-                   (GATED && (p & 2) ? uint32_t(a.half) * 2u : 0u);
-        if (row >= m_here) y_off[q] = OUT_OF_RANGE;
+        const int row = ((wv + BACK_WAVES * q) % NA) * 16 + (lane >> 2);
+        y_off[q] = row < m_here ? (uint32_t(row) * uint32_t(a.ldy) + uint32_t(y_col)) * 2u : OUT_OF_RANGE;
     }
-    constexpr int COLS = GATED ? NSTEP / 2 : NSTEP;   // channels a step
-    auto issue_y = [&](int st, int buf) {
-#pragma unroll
-        for (int q = 0; q < NAW; ++q) {
-            const uint32_t past = st * COLS + y_col[q] < a.N ? 0u : OUT_OF_RANGE;
-            ld128_lds(yr, (y_off[q] + uint32_t(st) * (COLS * 2)) | past, ldsA + buf * A_BYTES + ((wv + W * q) % NA) * 1024);
-        }
+    // u: the stage's place in the ring, (st - st0) mod 4, a constant where it matters
+    auto issue_y = [&](int q, int st, int u) {
+        const uint32_t past = st < st1 && st * NSTEP + y_col < a.ldy ? 0u : OUT_OF_RANGE;
+        ld128_lds(yr, (y_off[q] + uint32_t(st) * (NSTEP * 2)) | past,
+                  ldsA + (u & 3) * A_BYTES + ((wv + BACK_WAVES * q) % NA) * 1024);
     };
-    // 16-byte piece s of a packed tile lands at slot s ^ (s >> 4) << 1 ^ (chunk & 1): the
-    // words that 64 threads read together then lie in 64 different banks
-    uint32_t r_off[NRW];
+    // This wavefront's packed tile of a step: tile wv / 4, chunk wv mod 4.  Its 16-byte piece
+    // s lands at slot s ^ s / 16: the words that the 64 lanes read together then lie in 64
+    // different banks.
+    const int w_tile = wv >> 2, w_ch = wv & 3;
+    const uint32_t r_off = kq0 + w_ch < a.kchunks ? uint32_t(kq0 + w_ch) * TILE_BYTES + 16u * (lane ^ (lane >> 4)) : OUT_OF_RANGE;
+    auto issue_w = [&](int st, int u) {
+        const int tile = 2 * st + w_tile;
+        const uint32_t past = st < st1 && tile < a.ntiles ? 0u : OUT_OF_RANGE;
+        const __amdgpu_buffer_rsrc_t wr =
+            make_rsrc(a.w + int64_t(min(tile, a.ntiles - 1)) * a.kchunks * TILE_BYTES, uint32_t(a.kchunks) * TILE_BYTES);
+        ld128_lds(wr, r_off | past, ldsR + (u & 3) * R_BYTES + wv * 1024);
+    };
+
+    // Decoding: lane = word j of channels 4 qd .. 4 qd + 3, 16-input group gg of the tile.
+    const int dj = lane & 3, dq = (lane >> 2) & 3, dg = lane >> 4;
+    struct Packed {
+        uint32_t w[4];
+    };
+    const uint8_t *fetch_at[4];
+    uint8_t *store_at[4];
 #pragma unroll
-    for (int q = 0; q < NRW; ++q) {
-        const int b = (wv + W * q) % NR, tile = b / KQ, ch = b % KQ;
-        const int piece = lane ^ ((lane >> 4) << 1) ^ (ch & 1);
-        r_off[q] = kq0 + ch < a.kchunks
-                       ? (uint32_t(tile) * uint32_t(a.kchunks) + uint32_t(kq0 + ch)) * TILE_BYTES + 16u * piece
-                       : OUT_OF_RANGE;
+    for (int i = 0; i < 4; ++i) {
+        fetch_at[i] = ldsR + wv * 1024 + 4 * dj + 16 * ((dg * 16 + 4 * dq + i) ^ dg);
+        store_at[i] = ldsD + ((4 * w_ch + dg) * 64 + (2 * w_tile + (dq >> 1)) * 16 + ((4 * dj + i) ^ dg ^ (dq & 2))) * 16 + (dq & 1) * 8;
     }
-    auto issue_w = [&](int st, int buf) {
-        const int here = min(4, a.ntiles - 4 * st);
-        const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w + int64_t(st) * 4 * a.kchunks * TILE_BYTES,
-                                                    uint32_t(here) * uint32_t(a.kchunks) * TILE_BYTES);
+    auto fetch = [&](Packed &p, int u) {
 #pragma unroll
-        for (int q = 0; q < NRW; ++q) ld128_lds(wr, r_off[q], ldsR + buf * R_BYTES + ((wv + W * q) % NR) * 1024);
+        for (int i = 0; i < 4; ++i) p.w[i] = *reinterpret_cast<const uint32_t *>(fetch_at[i] + (u & 3) * R_BYTES) ^ 0x80808080u;
     };
-    // tasks: four inputs (word j of group gg of chunk ch) of eight rows (octet o of the step)
-    auto decode = [&](int st, int rbuf, int dbuf) {
-        for (int t0 = 0; t0 < TASKS; t0 += T) {
-            if (TASKS < T && ((wv / (TASKS / 64)) % (T / TASKS)) != (st % (T / TASKS))) break;   // in turn
-            const int t = TASKS < T ? tid % TASKS : t0 + tid;
-            const int j = t & 3, half = (t >> 2) & 1, gg = (t >> 3) & 3;
-            const int ch = (t >> 5) % KQ, tile = (t >> 5) / KQ, o = 2 * tile + half;
-            const uint8_t *raw = ldsR + rbuf * R_BYTES + (tile * KQ + ch) * 1024 + 4 * j;
-            uint32_t w[8];
+    // Byte b (input 4 dj + b of the group) of four channels.  A byte u = q + 128 in the low
+    // bits of 2^23 is the float 2^23 + u; 2^23 + 128 less gives q exactly, and so does its
+    // upper half as bf16.  Permutes and subtractions run at the full vector rate, conversion
+    // instructions at a quarter of it: with them a step of 128 x 256 took 0.69 us, without
+    // any decoding 0.37.
+    auto decode = [&](const Packed &p, int u, int b) {
+        float v[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int piece = gg * 16 + half * 8 + i;
-                w[i] = *reinterpret_cast<const uint32_t *>(raw + 16 * (piece ^ (gg << 1) ^ (ch & 1))) ^ 0x80808080u;
-            }
-            const int pt = 4 * st + tile;
-            float s[8];
-            const float *sp = a.s + int64_t(min(pt, a.ntiles - 1)) * TILE_N + 8 * half;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] = pt < a.ntiles ? sp[i] : 0.0f;
-            u32x4 v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a0 = s[2 * i], a1 = s[2 * i + 1], b0 = -128.0f * a0, b1 = -128.0f * a1;
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    v[b][i] = pack_bf16(fmaf(float((w[2 * i] >> (8 * b)) & 0xFFu), a0, b0),
-                                        fmaf(float((w[2 * i + 1] >> (8 * b)) & 0xFFu), a1, b1));
-            }
-            const int kt = 4 * ch + gg;
-            uint8_t *dst = ldsD + dbuf * D_BYTES + ((kt * 2 + (o >> 2)) * 64 + (o & 3) * 16) * 16;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) *reinterpret_cast<u32x4 *>(dst + ((4 * j + b) ^ gg) * 16) = v[b];
-        }
+        for (int i = 0; i < 4; ++i)
+            v[i] = __uint_as_float(__builtin_amdgcn_perm(0x4B000000u, p.w[i], 0x07040400u | uint32_t(b))) - 8388736.0f;
+        lds_store8(store_at[b] + (u & 1) * D_BYTES,
+                   u32x2{__builtin_amdgcn_perm(__float_as_uint(v[1]), __float_as_uint(v[0]), 0x07060302u),
+                         __builtin_amdgcn_perm(__float_as_uint(v[3]), __float_as_uint(v[2]), 0x07060302u)});
     };
 
     f32x4 acc[NT][MT];
@@ -146,63 +149,116 @@ __global__ void __launch_bounds__(64 * WM * WN) i8_back_kernel(I8BackArgs a) {
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    auto multiply = [&](int buf) {
-        const uint8_t *A = ldsA + buf * A_BYTES, *D = ldsD + buf * D_BYTES;
+    // x[i] is free again after its group of matrix instructions, so only w needs two sets
+    u32x4 x[MT], w0[NT], w1[NT];
+    const uint8_t *const x_at = ldsA + (wm * MT * 16 + c) * 64 + ((g ^ row_swizzle(c)) * 16);
+    const uint8_t *w_at[NT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            u32x4 yf[MT], wf[NT];
+    for (int j = 0; j < NT; ++j) {
+        const int kt = wn * NT + j;
+        w_at[j] = ldsD + kt * 1024 + (g * 16 + (c ^ (kt & 3) ^ (2 * (g & 1)))) * 16;
+    }
+    auto read_x = [&](int u, int i) { x[i] = *reinterpret_cast<const u32x4 *>(x_at + (u & 3) * A_BYTES + i * 1024); };
+    auto read_w = [&](u32x4 (&w)[NT], int u, int j) {
+        w[j] = *reinterpret_cast<const u32x4 *>(w_at[j] + (u & 1) * D_BYTES);
+    };
+    auto step = [&](int st, int u, const u32x4 (&w)[NT], u32x4 (&next)[NT]) {
+        wait_vmcnt<2 * PER_STEP>();
+        ring_barrier();
+        Packed p;
+        fetch(p, u + 2);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const int row = (wm * MT + i) * 16 + c;
-                yf[i] = *reinterpret_cast<const u32x4 *>(A + row * 128 + (((4 * h + g) ^ yswz(row)) * 16));
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int kt = wn * NT + j;
-                wf[j] = *reinterpret_cast<const u32x4 *>(D + ((kt * 2 + h) * 64 + g * 16 + (c ^ (kt & 3))) * 16);
-            }
+        for (int i = 0; i < MT; ++i) {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
+                acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[j]),
+                                                                    __builtin_bit_cast(bf16x8, x[i]), acc[j][i], 0, 0, 0);
+            read_x(u + 1, i);
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wf[j]),
-                                                                        __builtin_bit_cast(bf16x8, yf[i]), acc[j][i], 0, 0, 0);
+            for (int j = i * NT / MT; j < (i + 1) * NT / MT; ++j) read_w(next, u + 1, j);
+            // decoding starts behind a group of matrix instructions, under which its words
+            // arrive, and ends before the last, under which its stores finish
+            constexpr int D0 = MT >= 8 ? 2 : (MT >= 2 ? 1 : 0), D1 = MT >= 8 ? 6 : (MT >= 4 ? 3 : MT);
+            if (i >= D0 && i < D1)
+#pragma unroll
+                for (int b = (i - D0) * 4 / (D1 - D0); b < (i - D0 + 1) * 4 / (D1 - D0); ++b) decode(p, u + 2, b);
+            if (i == 0)
+#pragma unroll
+                for (int q = 0; q < NAW; ++q) issue_y(q, st + 4, u + 4);
+            if (i == (MT > 1 ? 1 : 0)) issue_w(st + 5, u + 5);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
 
     if (st0 < st1) {
-        issue_w(st0, st0 & 1);
-        issue_y(st0, st0 & 1);
+        // loads in the order of the steps: dy of s + 4 and tiles of s + 5 together
+        issue_w(st0, 0);
+        issue_w(st0 + 1, 1);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+#pragma unroll
+            for (int q = 0; q < NAW; ++q) issue_y(q, st0 + u, u);
+            if (u < 2) issue_w(st0 + 2 + u, 2 + u);
+        }
         wait_vmcnt<0>();
         ring_barrier();
-        if (st0 + 1 < st1) issue_w(st0 + 1, (st0 + 1) & 1);
-        // every wavefront that takes a turn decodes in its own step; the first step's
-        // operand is due now, whoever's turn it is
-        decode(st0, st0 & 1, st0 & 1);
-        for (int st = st0; st < st1; ++st) {
-            wait_vmcnt<0>();
-            ring_barrier();
-            if (st + 1 < st1) issue_y(st + 1, (st + 1) & 1);
-            if (st + 2 < st1) issue_w(st + 2, st & 1);
-            if (st + 1 < st1) decode(st + 1, (st + 1) & 1, (st + 1) & 1);
-            multiply(st & 1);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            Packed p;
+            fetch(p, u);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) decode(p, u, b);
+        }
+        ring_barrier();
+#pragma unroll
+        for (int i = 0; i < MT; ++i) read_x(0, i);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) read_w(w0, 0, j);
+        // the slot of step st0's tiles is decoded: those of step st0 + 4 go there
+        issue_w(st0 + 4, 0);
+        // whole groups of four: steps past the end read as zero and add nothing
+        for (int st = st0; st < st1; st += 4) {
+            step(st, 0, w0, w1);
+            step(st + 1, 1, w1, w0);
+            step(st + 2, 2, w0, w1);
+            step(st + 3, 3, w1, w0);
         }
     }
+    wait_vmcnt<0>();
+    ring_barrier();                                  // LDS is free for the output rows
 
+    if constexpr (SPLIT) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int m = m0 + (wm * MT + i) * 16 + c;
+            if (m >= a.M) continue;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int k = kq0 * I8_CHUNK + (wn * NT + j) * 16 + 4 * g;
+                if (k < a.K)                          // K is a multiple of 32
+                    *reinterpret_cast<f32x4 *>(a.part + (int64_t(blockIdx.y) * a.M + m) * a.K + k) = acc[j][i];
+            }
+        }
+        return;
+    }
+    // sixteen rows of the wavefront's inputs at a time through its own part of LDS, so that
+    // stores are whole 16-byte pieces (as in the forward tile kernel)
+    constexpr int PIECES = 2 * NT, STRIDE = NT * 32 + 16, ROWS = 64 / PIECES < 16 ? 64 / PIECES : 16;
+    static_assert(BACK_WAVES * 16 * STRIDE <= 4 * R_BYTES, "output rows fit");
+    uint8_t *const mine = ldsR + wv * (16 * STRIDE);
+    const int p_row = lane / PIECES, k_mine = kq0 * I8_CHUNK + wn * NT * 16 + 8 * (lane % PIECES);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-        const int m = m0 + (wm * MT + i) * 16 + c;
-        if (m >= a.M) continue;
+        const int mi = m0 + (wm * MT + i) * 16;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int k = kq0 * 64 + (wn * NT + j) * 16 + 4 * g;
-            if (k >= a.K) continue;                     // K is a multiple of 32
-            if constexpr (SPLIT) {
-                *reinterpret_cast<f32x4 *>(a.part + (int64_t(blockIdx.y) * a.M + m) * a.K + k) = acc[j][i];
-            } else {
-                *reinterpret_cast<u32x2 *>(a.dx + int64_t(m) * a.K + k) =
-                    u32x2{pack_bf16(acc[j][i][0], acc[j][i][1]), pack_bf16(acc[j][i][2], acc[j][i][3])};
-            }
+        for (int j = 0; j < NT; ++j)
+            *reinterpret_cast<u32x2 *>(mine + c * STRIDE + j * 32 + g * 8) =
+                u32x2{pack_bf16(acc[j][i][0], acc[j][i][1]), pack_bf16(acc[j][i][2], acc[j][i][3])};
+#pragma unroll
+        for (int r0 = 0; r0 < 16; r0 += ROWS) {
+            const int row = r0 + p_row, m = mi + row;
+            const u32x4 piece = *reinterpret_cast<const u32x4 *>(mine + (row & 15) * STRIDE + (lane % PIECES) * 16);
+            if (p_row < ROWS && m < a.M && k_mine < a.K) *reinterpret_cast<u32x4 *>(a.dx + int64_t(m) * a.K + k_mine) = piece;
         }
     }
 }
@@ -220,38 +276,49 @@ __global__ void __launch_bounds__(256) i8_back_join_kernel(const float *__restri
     reinterpret_cast<u32x2 *>(dx)[e] = u32x2{pack_bf16(t[0], t[1]), pack_bf16(t[2], t[3])};
 }
 
-// du, dg for V consecutive channels a thread; copy: the padded rows that the product reads
-// when N is not a multiple of eight ([M][2][Np], zero past N), or null.
+// du, dg for V consecutive channels a thread: draw [M, 2N] = [du | dg] in bf16, and the
+// product's operand [M][16 ntiles], both scaled by their channels and in packed tile order
+// (zero past N).
 template <int V>
 __global__ void __launch_bounds__(256) gate_back_kernel(const uint16_t *__restrict__ dh, const uint16_t *__restrict__ raw,
-                                                        uint16_t *__restrict__ draw, uint16_t *__restrict__ copy,
-                                                        int64_t M, int64_t N, int64_t Np, int act) {
+                                                        const float *__restrict__ s, uint16_t *__restrict__ draw,
+                                                        uint16_t *__restrict__ operand, int64_t M, int64_t N,
+                                                        int64_t Np, int act) {
     const int64_t per_row = Np / V, e = int64_t(blockIdx.x) * 256 + threadIdx.x;
     if (e >= M * per_row) return;
     const int64_t m = e / per_row, n = (e % per_row) * V;
+    const int64_t up_at = (n / TILE_N) * 2 * TILE_N + n % TILE_N;    // the gate's 16 further on
+    uint16_t *const op = operand + m * 2 * Np + up_at;
     if constexpr (V == 8) {
-        const u32x4 d = *reinterpret_cast<const u32x4 *>(dh + m * N + n);
-        const u32x4 u = *reinterpret_cast<const u32x4 *>(raw + m * 2 * N + n);
-        const u32x4 g = *reinterpret_cast<const u32x4 *>(raw + m * 2 * N + N + n);
-        u32x4 du, dg;
+        u32x4 du{0u, 0u, 0u, 0u}, dg = du, su = du, sg = du;
+        if (n < N) {                                                  // N is a multiple of eight
+            const u32x4 d = *reinterpret_cast<const u32x4 *>(dh + m * N + n);
+            const u32x4 u = *reinterpret_cast<const u32x4 *>(raw + m * 2 * N + n);
+            const u32x4 g = *reinterpret_cast<const u32x4 *>(raw + m * 2 * N + N + n);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            float o[2], p[2];
+            for (int w = 0; w < 4; ++w) {
+                float o[2], p[2];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const float dv = bf16_bits_to_f32((d[w] >> (16 * b)) & 0xFFFFu);
-                const float uv = bf16_bits_to_f32((u[w] >> (16 * b)) & 0xFFFFu);
-                const float gv = bf16_bits_to_f32((g[w] >> (16 * b)) & 0xFFFFu);
-                float f, df;
-                gate_act_grad(gv, act, f, df);
-                o[b] = dv * f;
-                p[b] = dv * uv * df;
+                for (int b = 0; b < 2; ++b) {
+                    const float dv = bf16_bits_to_f32((d[w] >> (16 * b)) & 0xFFFFu);
+                    const float uv = bf16_bits_to_f32((u[w] >> (16 * b)) & 0xFFFFu);
+                    const float gv = bf16_bits_to_f32((g[w] >> (16 * b)) & 0xFFFFu);
+                    float f, df;
+                    gate_act_grad(gv, act, f, df);
+                    o[b] = dv * f;
+                    p[b] = dv * uv * df;
+                }
+                const float *us = s + up_at + 2 * w, *gs = us + TILE_N;
+                du[w] = pack_bf16(o[0], o[1]);
+                dg[w] = pack_bf16(p[0], p[1]);
+                su[w] = pack_bf16(o[0] * us[0], o[1] * us[1]);
+                sg[w] = pack_bf16(p[0] * gs[0], p[1] * gs[1]);
             }
-            du[w] = pack_bf16(o[0], o[1]);
-            dg[w] = pack_bf16(p[0], p[1]);
+            *reinterpret_cast<u32x4 *>(draw + m * 2 * N + n) = du;
+            *reinterpret_cast<u32x4 *>(draw + m * 2 * N + N + n) = dg;
         }
-        *reinterpret_cast<u32x4 *>(draw + m * 2 * N + n) = du;
-        *reinterpret_cast<u32x4 *>(draw + m * 2 * N + N + n) = dg;
+        *reinterpret_cast<u32x4 *>(op) = su;
+        *reinterpret_cast<u32x4 *>(op + TILE_N) = sg;
     } else {
         float o = 0.0f, p = 0.0f;
         if (n < N) {
@@ -263,44 +330,54 @@ __global__ void __launch_bounds__(256) gate_back_kernel(const uint16_t *__restri
             p = dv * uv * df;
             reinterpret_cast<__bf16 *>(draw)[m * 2 * N + n] = (__bf16)o;
             reinterpret_cast<__bf16 *>(draw)[m * 2 * N + N + n] = (__bf16)p;
+            o *= s[up_at];
+            p *= s[up_at + TILE_N];
         }
-        if (copy) {
-            reinterpret_cast<__bf16 *>(copy)[m * 2 * Np + n] = (__bf16)o;
-            reinterpret_cast<__bf16 *>(copy)[m * 2 * Np + Np + n] = (__bf16)p;
-        }
+        reinterpret_cast<__bf16 *>(op)[0] = (__bf16)o;
+        reinterpret_cast<__bf16 *>(op)[TILE_N] = (__bf16)p;
     }
 }
 
-// dy [M, N] -> rows of Np, zero past N
-__global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t *__restrict__ dy, uint16_t *__restrict__ out,
-                                                       int64_t M, int64_t N, int64_t Np) {
-    const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (e >= M * Np) return;
-    const int64_t m = e / Np, n = e % Np;
-    out[e] = n < N ? dy[m * N + n] : uint16_t(0);
+// The linear product's operand: dy [M, N] times the channel scales, rows of Np, zero past N.
+template <int V>
+__global__ void __launch_bounds__(256) scale_back_kernel(const uint16_t *__restrict__ dy, const float *__restrict__ s,
+                                                         uint16_t *__restrict__ operand, int64_t M, int64_t N,
+                                                         int64_t Np) {
+    const int64_t per_row = Np / V, e = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (e >= M * per_row) return;
+    const int64_t m = e / per_row, n = (e % per_row) * V;
+    if constexpr (V == 8) {
+        const u32x4 d = *reinterpret_cast<const u32x4 *>(dy + m * N + n);
+        u32x4 o;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            o[w] = pack_bf16(bf16_bits_to_f32(d[w] & 0xFFFFu) * s[n + 2 * w], bf16_bits_to_f32(d[w] >> 16) * s[n + 2 * w + 1]);
+        *reinterpret_cast<u32x4 *>(operand + m * Np + n) = o;
+    } else {
+        reinterpret_cast<__bf16 *>(operand)[m * Np + n] = (__bf16)(n < N ? bf16_bits_to_f32(dy[m * N + n]) * s[n] : 0.0f);
+    }
 }
 
 struct BackCfg { int WM, WN, MT, NT; };
-constexpr BackCfg BACK_CFGS[] = {{4, 2, 4, 4}, {2, 2, 4, 4}, {2, 2, 1, 4}};
-constexpr int back_lds(const BackCfg &t) {
-    return 2 * (16 * t.MT * t.WM * 128 + 16 * t.NT * t.WN * (64 + 128));
-}
+constexpr BackCfg BACK_CFGS[] = {{2, 4, 8, 4}, {2, 4, 4, 4}, {2, 4, 2, 4}, {1, 8, 1, 2}};
+constexpr int NUM_BACK_CFGS = 4;
+constexpr int back_rows(const BackCfg &t) { return 16 * t.MT * t.WM; }
 
-template <int I, bool GATED>
+template <int I>
 hipError_t launch_back(const I8BackArgs &a, hipStream_t st) {
     constexpr BackCfg t = BACK_CFGS[I];
-    constexpr int lds = back_lds(t);
-    static_assert(lds <= LDS_BYTES_MAX, "two buffers fit the LDS");
-    const dim3 grid(unsigned(a.mtiles * a.nblocks), unsigned(a.ks)), block(64 * t.WM * t.WN);
+    constexpr int lds = back_lds(back_rows(t));
+    static_assert(lds <= LDS_BYTES_MAX, "the stages fit the LDS");
+    const dim3 grid(unsigned(a.mtiles * a.nblocks), unsigned(a.ks)), block(64 * BACK_WAVES);
     if (a.ks == 1) {
-        auto kern = i8_back_kernel<t.WM, t.WN, t.MT, t.NT, GATED, false>;
+        auto kern = i8_back_kernel<t.WM, t.WN, t.MT, t.NT, false>;
         static const hipError_t set =
             hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (set != hipSuccess) return set;
         hipLaunchKernelGGL(kern, grid, block, lds, st, a);
         return hipGetLastError();
     }
-    auto kern = i8_back_kernel<t.WM, t.WN, t.MT, t.NT, GATED, true>;
+    auto kern = i8_back_kernel<t.WM, t.WN, t.MT, t.NT, true>;
     static const hipError_t set =
         hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (set != hipSuccess) return set;
@@ -312,71 +389,60 @@ hipError_t launch_back(const I8BackArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <bool GATED>
 hipError_t launch_back_any(int cfg, const I8BackArgs &a, hipStream_t st) {
     switch (cfg) {
-        case 0: return launch_back<0, GATED>(a, st);
-        case 1: return launch_back<1, GATED>(a, st);
-        default: return launch_back<2, GATED>(a, st);
+        case 0: return launch_back<0>(a, st);
+        case 1: return launch_back<1>(a, st);
+        case 2: return launch_back<2>(a, st);
+        default: return launch_back<3>(a, st);
     }
 }
 
 }  // namespace
 
-// Rows of dy the product cannot read in place (N not a multiple of eight) are copied to
-// rows of Np first; a gated product's du and dg are written there as they are formed.
 I8BackPlan make_i8_back_plan(const I8Layout &L, int64_t M) {
     I8BackPlan p;
-    p.Np = ceil_div(L.N, 8) * 8;
-    const int64_t kcols = L.kchunks * I8_CHUNK;
-    for (int c = 0; c < 3; ++c) {
-        const BackCfg &t = BACK_CFGS[c];
+    p.Np = L.gated ? ceil_div(L.N, TILE_N) * TILE_N : ceil_div(L.N, 8) * 8;
+    const int64_t kblocks = ceil_div(L.kchunks, BACK_KQ);
+    p.nblocks = int(kblocks);
+    for (int c = 0; c < NUM_BACK_CFGS; ++c) {
         p.cfg = c;
-        p.mtiles = int(ceil_div(M, 16 * t.MT * t.WM));
-        p.nblocks = int(ceil_div(kcols, 16 * t.NT * t.WN));
-        if (int64_t(p.mtiles) * p.nblocks >= 192) break;
+        p.mtiles = int(ceil_div(M, back_rows(BACK_CFGS[c])));
+        if (p.mtiles * kblocks >= 192) break;
     }
-    const int64_t steps = ceil_div(L.ntiles, 4), wgs = int64_t(p.mtiles) * p.nblocks;
+    const int64_t steps = ceil_div(L.ntiles, 2), wgs = int64_t(p.mtiles) * p.nblocks;
     int64_t ks = wgs >= 192 ? 1 : ceil_div(256, wgs);
-    ks = std::max<int64_t>(1, std::min<int64_t>(ks, steps / 4));
-    p.nps = int(ceil_div(steps, ks));
+    ks = std::max<int64_t>(1, std::min<int64_t>(ks, steps / 8));
+    p.nps = int(ceil_div(ceil_div(steps, ks), 4) * 4);
     p.ks = int(ceil_div(steps, p.nps));
-    p.copy_bytes = L.N % 8 ? round256(size_t(M) * size_t(p.Np) * (L.gated ? 4 : 2)) : 0;
-    p.ws_bytes = p.copy_bytes + (p.ks > 1 ? round256(size_t(p.ks) * size_t(M) * size_t(L.K) * 4) : 0);
+    p.operand_bytes = round256(size_t(M) * size_t(p.Np) * (L.gated ? 4 : 2));
+    p.ws_bytes = p.operand_bytes + (p.ks > 1 ? round256(size_t(p.ks) * size_t(M) * size_t(L.K) * 4) : 0);
     return p;
 }
 
 hipError_t launch_i8_backward(const I8Layout &L, const I8BackPlan &p, const uint16_t *dy, const uint16_t *raw, int act,
                               int64_t M, const void *pw, const void *ps, uint16_t *dx, uint16_t *draw, void *ws,
                               hipStream_t st) {
-    uint16_t *copy = p.copy_bytes ? static_cast<uint16_t *>(ws) : nullptr;
-    I8BackArgs a{};
+    uint16_t *operand = static_cast<uint16_t *>(ws);
+    const float *sc = static_cast<const float *>(ps);
+    const bool vec = L.N % 8 == 0;
+    const dim3 grid(unsigned(ceil_div(M * p.Np / (vec ? 8 : 1), 256)));
     if (L.gated) {
-        const int V = copy ? 1 : 8;
-        const int64_t n = M * ((copy ? p.Np : L.N) / V);
-        const dim3 grid(unsigned(ceil_div(n, 256)));
-        if (copy)
-            hipLaunchKernelGGL(gate_back_kernel<1>, grid, dim3(256), 0, st, dy, raw, draw, copy, M, L.N, p.Np, act);
-        else
-            hipLaunchKernelGGL(gate_back_kernel<8>, grid, dim3(256), 0, st, dy, raw, draw, copy, M, L.N, L.N, act);
-        a.dy = copy ? copy : draw;
-        a.half = copy ? p.Np : L.N;
-        a.ldy = 2 * a.half;
+        if (vec) hipLaunchKernelGGL(gate_back_kernel<8>, grid, dim3(256), 0, st, dy, raw, sc, draw, operand, M, L.N, p.Np, act);
+        else hipLaunchKernelGGL(gate_back_kernel<1>, grid, dim3(256), 0, st, dy, raw, sc, draw, operand, M, L.N, p.Np, act);
     } else {
-        if (copy)
-            hipLaunchKernelGGL(pad_rows_kernel, dim3(unsigned(ceil_div(M * p.Np, 256))), dim3(256), 0, st, dy, copy, M,
-                               L.N, p.Np);
-        a.dy = copy ? copy : dy;
-        a.ldy = copy ? p.Np : L.N;
+        if (vec) hipLaunchKernelGGL(scale_back_kernel<8>, grid, dim3(256), 0, st, dy, sc, operand, M, L.N, p.Np);
+        else hipLaunchKernelGGL(scale_back_kernel<1>, grid, dim3(256), 0, st, dy, sc, operand, M, L.N, p.Np);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    I8BackArgs a{};
     a.w = static_cast<const uint8_t *>(pw);
-    a.s = static_cast<const float *>(ps);
+    a.dy = operand;
+    a.ldy = (L.gated ? 2 : 1) * p.Np;
     a.dx = dx;
-    a.part = p.ks > 1 ? reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + p.copy_bytes) : nullptr;
+    a.part = p.ks > 1 ? reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + p.operand_bytes) : nullptr;
     a.M = int(M);
-    a.N = int(copy ? p.Np : L.N);
     a.K = int(L.K);
     a.ntiles = int(L.ntiles);
     a.kchunks = int(L.kchunks);
@@ -384,7 +450,7 @@ hipError_t launch_i8_backward(const I8Layout &L, const I8BackPlan &p, const uint
     a.nblocks = p.nblocks;
     a.ks = p.ks;
     a.nps = p.nps;
-    return L.gated ? launch_back_any<true>(p.cfg, a, st) : launch_back_any<false>(p.cfg, a, st);
+    return launch_back_any(p.cfg, a, st);
 }
 
 }  // namespace ql

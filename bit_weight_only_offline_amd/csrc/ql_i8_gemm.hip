@@ -30,36 +30,44 @@ __device__ inline i32x4 mma(const u32x4 &a, const u32x4 &b, i32x4 c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
 
-// The float32 results of four consecutive channels of token m (scale xs) whose sums are
-// `sum`, tile `tile` holding them at position `at` (a multiple of four).
-__device__ inline void scaled(const I8Args &a, float xs, int tile, int at, int64_t bias_at, int count, const i32x4 &sum,
-                              float (&v)[4]) {
-    const f32x4 s = *reinterpret_cast<const f32x4 *>(a.s + int64_t(tile) * TILE_N + at);
+// Scales and biases of four consecutive channels: tile `tile`, position `at` in it (a
+// multiple of four), of which the first `count` exist and whose biases start at `bias_at`.
+struct Channels {
+    f32x4 s, b;
+};
+__device__ inline Channels channels(const I8Args &a, int tile, int at, int64_t bias_at, int count) {
+    Channels q;
+    q.s = *reinterpret_cast<const f32x4 *>(a.s + int64_t(tile) * TILE_N + at);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const float b = (a.bias && r < count) ? bf16_bits_to_f32(a.bias[bias_at + r]) : 0.0f;
-        v[r] = fmaf(float(sum[r]) * xs, s[r], b);
-    }
+    for (int r = 0; r < 4; ++r) q.b[r] = (a.bias && r < count) ? bf16_bits_to_f32(a.bias[bias_at + r]) : 0.0f;
+    return q;
 }
 
-// Linear: tile `tile`, channels 16 tile + at .. +3 of token m.
-__device__ inline void emit_linear(const I8Args &a, int m, float xs, int tile, int at, const i32x4 &sum) {
-    const int n = tile * TILE_N + at, count = a.N - n;
+// The float32 results of those channels for a token of scale xs whose sums are `sum`.
+__device__ inline void scaled(const Channels &q, float xs, const i32x4 &sum, float (&v)[4]) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = fmaf(float(sum[r]) * xs, q.s[r], q.b[r]);
+}
+
+// Linear: channels n .. n + 3 of token m.
+__device__ inline void emit_linear(const I8Args &a, int m, float xs, int n, const Channels &q, const i32x4 &sum) {
+    const int count = a.N - n;
     if (count <= 0) return;
     float v[4];
-    scaled(a, xs, tile, at, n, count, sum, v);
+    scaled(q, xs, sum, v);
     const int64_t i = int64_t(m) * a.N + n;
     if (a.out_f32) store4_f32(static_cast<float *>(a.out), i, v, count, a.vec);
     else store4_bf16(static_cast<uint16_t *>(a.out), i, v, count, a.vec);
 }
 
-// Gated: tile pair `pair` (up tile 2 pair, gate tile 2 pair + 1).
-__device__ inline void emit_gated(const I8Args &a, int m, float xs, int pair, int at, const i32x4 &up, const i32x4 &gt) {
-    const int n = pair * TILE_N + at, count = a.N - n;
+// Gated: the same of an up and a gate tile.
+__device__ inline void emit_gated(const I8Args &a, int m, float xs, int n, const Channels &uq, const Channels &gq,
+                                  const i32x4 &up, const i32x4 &gt) {
+    const int count = a.N - n;
     if (count <= 0) return;
     float u[4], g[4], h[4];
-    scaled(a, xs, 2 * pair, at, n, count, up, u);
-    scaled(a, xs, 2 * pair + 1, at, int64_t(a.N) + n, count, gt, g);
+    scaled(uq, xs, up, u);
+    scaled(gq, xs, gt, g);
 #pragma unroll
     for (int r = 0; r < 4; ++r) h[r] = gate_act(g[r], a.act) * u[r];
     const int64_t i = int64_t(m) * a.N + n;
@@ -70,6 +78,17 @@ __device__ inline void emit_gated(const I8Args &a, int m, float xs, int pair, in
         store4_bf16(a.raw, j, u, count, a.vec);
         store4_bf16(a.raw, j + a.N, g, count, a.vec);
     }
+}
+
+// One token's four channels of tile t (gated: of tile pair t), sums from `total(tile)`.
+template <bool GATED, typename F>
+__device__ inline void emit(const I8Args &a, int m, int t, int at, F total) {
+    const int n = t * TILE_N + at, count = a.N - n;
+    if constexpr (GATED)
+        emit_gated(a, m, a.xs[m], n, channels(a, 2 * t, at, n, count), channels(a, 2 * t + 1, at, int64_t(a.N) + n, count),
+                   total(2 * t), total(2 * t + 1));
+    else
+        emit_linear(a, m, a.xs[m], n, channels(a, t, at, n, count), total(t));
 }
 
 // ---- few rows: the weight streams through registers ----------------------------------
@@ -149,41 +168,41 @@ __global__ void __launch_bounds__(64 * WK) i8_rows_kernel(I8Args a) {
         const int l = e & 63, i = (e >> 6) % MT, j = (e >> 6) / MT;
         const int m = m0 + 16 * i + (l & 15), at = 4 * (l >> 4);
         if (m >= a.M || (GATED ? 2 * j : j) >= nt_here) continue;
-        const float xs = a.xs[m];
-        auto total = [&](int tile) {
-            i32x4 t = red[(tile * MT + i) * 64 + l];
+        emit<GATED>(a, m, (GATED ? nt0 / 2 : nt0) + j, at, [&](int tile) {
+            i32x4 t = red[((tile - nt0) * MT + i) * 64 + l];
 #pragma unroll
-            for (int w = 1; w < WK; ++w) t += red[(w * NT * MT + tile * MT + i) * 64 + l];
+            for (int w = 1; w < WK; ++w) t += red[(w * NT * MT + (tile - nt0) * MT + i) * 64 + l];
             return t;
-        };
-        if constexpr (GATED) emit_gated(a, m, xs, nt0 / 2 + j, at, total(2 * j), total(2 * j + 1));
-        else emit_linear(a, m, xs, nt0 + j, at, total(j));
+        });
     }
 }
 
 // ---- tiles: both operands staged through LDS ------------------------------------------
-// WM x WN wavefronts, each 16 MT tokens x NT column tiles.  A stage holds CPS chunks of
-// 16 MT WM activation rows and of NT WN weight tiles; S stages form a ring that direct
-// buffer->LDS loads fill, S - 1 stages ahead of the one being multiplied.  Activation rows
-// are loaded in whole 64 CPS-byte runs; a XOR swizzle of their 16-byte pieces, applied to
-// the global address of each lane, spreads the 16 rows of an operand read over all banks.
-// Weight tiles are stored in operand order, so their reads are linear.
-template <int WM, int WN, int MT, int NT, int CPS, int S, bool GATED, bool SPLIT>
-__global__ void __launch_bounds__(64 * WM * WN) i8_tile_kernel(I8Args a) {
+// WM x WN wavefronts, each 16 MT tokens x NT column tiles, WK times: the WK groups take
+// alternate chunks (64 inputs) and their sums meet in LDS at the end, which keeps a compute
+// unit's matrix cores busy where there are too few tiles for several workgroups.  A stage is
+// WK chunks of 16 MT WM activation rows and of NT WN weight tiles; S stages form a ring that
+// direct buffer->LDS loads fill.  Activation rows are loaded in 64-byte runs; a XOR swizzle of their
+// 16-byte pieces, applied to the global address of each lane, spreads the 16 rows of an
+// operand read over all banks.  Weight tiles are stored in operand order, so their reads are
+// linear.
+template <int WM, int WN, int WK, int MT, int NT, int S, bool GATED, bool SPLIT>
+__global__ void __launch_bounds__(64 * WM * WN * WK) i8_tile_kernel(I8Args a) {
     static_assert(!GATED || NT % 2 == 0, "up and gate tiles go together");
-    constexpr int W = WM * WN;
+    constexpr int W = WM * WN * WK;
     constexpr int MP = 16 * MT * WM, NTT = NT * WN;
-    constexpr int P = 4 * CPS, RPI = 64 / P;           // 16-byte pieces a row, rows a load
-    constexpr int NA = MP / RPI, NB = NTT * CPS;       // 1 KiB loads a stage
-    static_assert(NA % W == 0 && NB % W == 0, "every wavefront issues the same loads");
-    constexpr int NAW = NA / W, NBW = NB / W, PER_STAGE = NAW + NBW;
+    constexpr int XA = MP / 16, XB = NTT;              // 1 KiB loads a chunk
+    constexpr int NA = XA * WK, NB = XB * WK;          // and a stage
+    // every wavefront issues the same number of loads; where they do not divide evenly some
+    // are issued twice (the same bytes to the same place)
+    constexpr int NAW = (NA + W - 1) / W, NBW = (NB + W - 1) / W, PER_STAGE = NAW + NBW;
     constexpr int STAGE = (NA + NB) * 1024;
-    static_assert(S * STAGE <= LDS_BYTES_MAX && S >= 2 && S <= 6, "ring fits the LDS");
+    static_assert(S * STAGE <= LDS_BYTES_MAX && S >= 4 && S <= 6, "ring fits the LDS");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wv / WN, wn = wv % WN;
+    const int wk = wv / (WM * WN), wm = wv / WN % WM, wn = wv % WN;
     const int g = lane >> 4, c = lane & 15;
 
     // Block b runs on XCD b mod 8: give each XCD one contiguous run of the tile order, and
@@ -200,38 +219,40 @@ __global__ void __launch_bounds__(64 * WM * WN) i8_tile_kernel(I8Args a) {
     const int nt_here = min(NTT, a.ntiles - nt0), m_here = min(MP, a.M - m0);
 
     const int kc0 = SPLIT ? int(blockIdx.y) * a.cps : 0;
-    const int kc1 = SPLIT ? min(a.kchunks, kc0 + a.cps) : a.kchunks;
-    const int nst = (kc1 - kc0 + CPS - 1) / CPS;
+    const int nck = SPLIT ? min(a.kchunks - kc0, a.cps) : a.kchunks;   // chunks, and stages of them
+    const int nst = (nck + WK - 1) / WK;
 
     const __amdgpu_buffer_rsrc_t wr =
         make_rsrc(a.w + int64_t(nt0) * a.kchunks * TILE_BYTES, uint32_t(nt_here) * uint32_t(a.kchunks) * TILE_BYTES);
     const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x + int64_t(m0) * a.K, uint32_t(m_here) * uint32_t(a.K));
 
-    auto xswz = [](int r) { return P == 8 ? ((r >> 1) & 7) : ((r >> 2) & 3); };
-    uint32_t a_off[NAW], b_off[NBW];
-    int b_chunk[NBW];
+    // load l of a stage: chunk l / XA, 16 rows l mod XA; then chunk l / XB, tile l mod XB
+    uint32_t off[PER_STAGE];
 #pragma unroll
     for (int q = 0; q < NAW; ++q) {
-        const int row = (wv + W * q) * RPI + lane / P;
-        a_off[q] = row < m_here ? uint32_t(row) * uint32_t(a.K) + 16u * uint32_t((lane % P) ^ xswz(row)) : OUT_OF_RANGE;
+        const int l = (wv + W * q) % NA, row = (l % XA) * 16 + lane / 4;
+        off[q] = row < m_here ? uint32_t(row) * uint32_t(a.K) + uint32_t(kc0 + l / XA) * I8_CHUNK +
+                                    16u * uint32_t((lane % 4) ^ row_swizzle(row))
+                              : OUT_OF_RANGE;
     }
 #pragma unroll
     for (int q = 0; q < NBW; ++q) {
-        const int b = wv + W * q, tile = b / CPS;
-        b_chunk[q] = b % CPS;
-        b_off[q] = tile < nt_here ? (uint32_t(tile) * uint32_t(a.kchunks) + uint32_t(b_chunk[q])) * TILE_BYTES + 16u * lane
-                                  : OUT_OF_RANGE;
+        const int l = (wv + W * q) % NB, tile = l % XB;
+        off[NAW + q] = tile < nt_here ? (uint32_t(tile) * uint32_t(a.kchunks) + uint32_t(kc0 + l / XB)) * TILE_BYTES + 16u * lane
+                                      : OUT_OF_RANGE;
     }
-    auto issue = [&](int st, int buf) {
+    // load q of stage st; past the last chunk it reads as zero, so that every step of the
+    // loop issues and waits for the same number of loads, and the sums stay as they are
+    auto issue = [&](int q, int st, int buf) {
         uint8_t *base = lds + buf * STAGE;
-        const int kc = kc0 + st * CPS;
-#pragma unroll
-        for (int q = 0; q < NAW; ++q) ld128_lds(xr, a_off[q] + uint32_t(kc) * I8_CHUNK, base + (wv + W * q) * 1024);
-#pragma unroll
-        for (int q = 0; q < NBW; ++q) {
-            // a chunk past the range reads as zero, which leaves the sums as they are
-            const uint32_t past = kc + b_chunk[q] < kc1 ? 0u : OUT_OF_RANGE;
-            ld128_lds(wr, (b_off[q] + uint32_t(kc) * TILE_BYTES) | past, base + (NA + wv + W * q) * 1024);
+        if (q < NAW) {
+            const int l = (wv + W * q) % NA;
+            const uint32_t past = st * WK + l / XA < nck ? 0u : OUT_OF_RANGE;
+            ld128_lds(xr, (off[q] + uint32_t(st) * (WK * I8_CHUNK)) | past, base + l * 1024);
+        } else {
+            const int l = (wv + W * (q - NAW)) % NB;
+            const uint32_t past = st * WK + l / XB < nck ? 0u : OUT_OF_RANGE;
+            ld128_lds(wr, (off[q] + uint32_t(st) * (WK * TILE_BYTES)) | past, base + (NA + l) * 1024);
         }
     };
 
@@ -241,45 +262,81 @@ __global__ void __launch_bounds__(64 * WM * WN) i8_tile_kernel(I8Args a) {
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
 
-    auto compute = [&](int buf) {
-        const uint8_t *A = lds + buf * STAGE, *B = A + NA * 1024;
+    // A stage's operands in registers.  Reads of the next stage and loads further ahead are
+    // spread between the matrix instructions of this one: issued together behind a barrier,
+    // by all wavefronts at once, they would leave the matrix cores idle.
+    struct Operands {
+        u32x4 x[MT], w[NT];
+    };
+    constexpr int READS = MT + NT;
+    const uint32_t x_at = uint32_t((wk * XA + wm * MT) * 1024 + c * 64 + ((g ^ row_swizzle(c)) * 16));
+    const uint32_t w_at = uint32_t((NA + wk * XB + wn * NT) * 1024 + lane * 16);
+    auto read = [&](Operands &f, const uint8_t *stage, int r) {
+        if (r < MT) f.x[r] = *reinterpret_cast<const u32x4 *>(stage + x_at + r * 1024);
+        else f.w[r - MT] = *reinterpret_cast<const u32x4 *>(stage + w_at + (r - MT) * 1024);
+    };
+    auto slot = [](int s, int by) { return s + by >= S ? s + by - S : s + by; };
+    // Multiplies stage operands `f` while `next` is read from slot `from` and stage `st` is
+    // loaded into slot `to`.
+    auto multiply = [&](const Operands &f, Operands &next, int from, int st, int to) {
+        const uint8_t *ahead = lds + from * STAGE;
 #pragma unroll
-        for (int h = 0; h < CPS; ++h) {
-            u32x4 xf[MT], wf[NT];
+        for (int j = 0; j < NT; ++j) {
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const int row = (wm * MT + i) * 16 + c;
-                xf[i] = *reinterpret_cast<const u32x4 *>(A + row * (P * 16) + (((4 * h + g) ^ xswz(row)) * 16));
-            }
+            for (int i = 0; i < MT; ++i) acc[j][i] = mma(f.w[j], f.x[i], acc[j][i]);
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-                wf[j] = *reinterpret_cast<const u32x4 *>(B + ((wn * NT + j) * CPS + h) * 1024 + lane * 16);
+            for (int r = j * READS / (NT - 1); r < (j + 1) * READS / (NT - 1) && r < READS; ++r) read(next, ahead, r);
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < MT; ++i) acc[j][i] = mma(wf[j], xf[i], acc[j][i]);
+            for (int q = j * PER_STAGE / NT; q < (j + 1) * PER_STAGE / NT; ++q) issue(q, st, to);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
 
+    // One barrier for two stages.  At the barrier before stages st and st + 1 the operands of
+    // st are in registers, st + 1 and st + 2 have arrived, st + 3 .. st + S - 2 are on their
+    // way, and the slots of st and of the stage before it are free: st + S - 1 and st + S go
+    // there.  Past the last stage loads read as zero and nothing uses what is read.
 #pragma unroll
     for (int u = 0; u < S - 1; ++u)
-        if (u < nst) issue(u, u);
-    for (int i0 = 0; i0 < nst; i0 += S) {
 #pragma unroll
-        for (int u = 0; u < S; ++u) {
-            const int i = i0 + u;
-            if (i < nst) {
-                const int later = min(S - 2, nst - 1 - i);   // stages issued after this one
-                if (later >= 4) wait_vmcnt<4 * PER_STAGE>();
-                else if (later == 3) wait_vmcnt<3 * PER_STAGE>();
-                else if (later == 2) wait_vmcnt<2 * PER_STAGE>();
-                else if (later == 1) wait_vmcnt<PER_STAGE>();
-                else wait_vmcnt<0>();
-                ring_barrier();
-                if (i + S - 1 < nst) issue(i + S - 1, (u + S - 1) % S);
-                compute(u);
-            }
+        for (int q = 0; q < PER_STAGE; ++q) issue(q, u, u);
+    Operands f0, f1;
+    wait_vmcnt<(S - 2) * PER_STAGE>();
+    ring_barrier();
+#pragma unroll
+    for (int r = 0; r < READS; ++r) read(f0, lds, r);
+    int st = 0, at = 0;                                   // at: slot of stage st
+    while (true) {
+        wait_vmcnt<(S - 4) * PER_STAGE>();
+        ring_barrier();
+        multiply(f0, f1, slot(at, 1), st + S - 1, slot(at, S - 1));
+        if (st + 1 == nst) break;
+        multiply(f1, f0, slot(at, 2), st + S, at);
+        st += 2;
+        at = slot(at, 2);
+        if (st == nst) break;
+    }
+    wait_vmcnt<0>();
+    ring_barrier();                                       // the ring is free for what follows
+    if constexpr (WK > 1) {
+        // the later groups hand their sums to the first: 1 KiB a tile, 16 bytes a lane
+        static_assert((WK - 1) * XA * XB <= S * STAGE / 1024, "sums fit the ring");
+        i32x4 *const at = reinterpret_cast<i32x4 *>(lds) + (wm * WN + wn) * (MT * NT) * 64 + lane;
+        constexpr int GROUP = WM * WN * MT * NT * 64;
+        if (wk > 0) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) at[(wk - 1) * GROUP + (j * MT + i) * 64] = acc[j][i];
         }
+        ring_barrier();
+        if (wk > 0) return;                               // no barrier follows
+#pragma unroll
+        for (int k = 0; k < WK - 1; ++k)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) acc[j][i] += at[k * GROUP + (j * MT + i) * 64];
     }
 
     if constexpr (SPLIT) {
@@ -298,17 +355,82 @@ __global__ void __launch_bounds__(64 * WM * WN) i8_tile_kernel(I8Args a) {
         }
         return;
     }
+    // All scales and biases first: behind the first stores their loads could not be shared.
+    constexpr int CT = GATED ? NT / 2 : NT;                // channel tiles of the wavefront
+    const int ct0 = GATED ? (nt0 + wn * NT) / 2 : nt0 + wn * NT;
+    float xs[MT];
+    Channels q[NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int m = m0 + (wm * MT + i) * 16 + c;
+        xs[i] = m < a.M ? a.xs[m] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int n = (ct0 + (GATED ? j / 2 : j)) * TILE_N + 4 * g;
+        q[j] = Channels{};
+        if (n < a.N) q[j] = channels(a, nt0 + wn * NT + j, 4 * g, (GATED && (j & 1) ? int64_t(a.N) : 0) + n, a.N - n);
+    }
+    // A lane holds four channels of a token, eight bytes of bf16.  Sixteen tokens of the
+    // wavefront's columns go through LDS (its own part of the ring), so that
+    // the stores cover whole 16-byte pieces of contiguous runs of each row: 256 x 256 bf16
+    // tiles over 4096 inputs took 505 us a 4096 x 32768 output so, 629 with eight-byte stores,
+    // and a gated product that also stores [up | gate] 509 against 721.
+    if (a.vec8 && !a.out_f32) {
+        constexpr int PIECES = 2 * CT, STRIDE = CT * 32 + 16, KINDS = GATED ? 3 : 1;
+        constexpr int ROWS = 64 / PIECES < 16 ? 64 / PIECES : 16;
+        // behind the sums of the other groups, which may still be read
+        constexpr int SUMS = (WK - 1) * XA * XB * 1024;
+        static_assert(SUMS + WM * WN * KINDS * 16 * STRIDE <= S * STAGE, "output rows fit the ring");
+        uint8_t *const mine = lds + SUMS + wv * (KINDS * 16 * STRIDE);
+        const int kinds = GATED && a.raw ? 3 : 1;
+        const int p_row = lane / PIECES, n_mine = ct0 * TILE_N + 8 * (lane % PIECES);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int mi = m0 + (wm * MT + i) * 16;
+#pragma unroll
+            for (int t = 0; t < CT; ++t) {
+                float v[KINDS][4];
+                if constexpr (GATED) {
+                    scaled(q[2 * t], xs[i], acc[2 * t][i], v[1]);
+                    scaled(q[2 * t + 1], xs[i], acc[2 * t + 1][i], v[2]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[0][r] = gate_act(v[2][r], a.act) * v[1][r];
+                } else {
+                    scaled(q[t], xs[i], acc[t][i], v[0]);
+                }
+#pragma unroll
+                for (int k = 0; k < KINDS; ++k)
+                    if (k < kinds)
+                        *reinterpret_cast<u32x2 *>(mine + k * 16 * STRIDE + c * STRIDE + t * 32 + g * 8) =
+                            u32x2{pack_bf16(v[k][0], v[k][1]), pack_bf16(v[k][2], v[k][3])};
+            }
+#pragma unroll
+            for (int k = 0; k < KINDS; ++k) {
+                if (k >= kinds) continue;
+                uint16_t *const dst = k == 0 ? static_cast<uint16_t *>(a.out) : a.raw + (k == 1 ? 0 : a.N);
+                const int64_t ld = k == 0 ? a.N : 2 * int64_t(a.N);
+#pragma unroll
+                for (int r0 = 0; r0 < 16; r0 += ROWS) {
+                    const int row = r0 + p_row, m = mi + row;
+                    const u32x4 piece =
+                        *reinterpret_cast<const u32x4 *>(mine + k * 16 * STRIDE + (row & 15) * STRIDE + (lane % PIECES) * 16);
+                    if (p_row < ROWS && m < a.M && n_mine < a.N)
+                        *reinterpret_cast<u32x4 *>(dst + int64_t(m) * ld + n_mine) = piece;
+                }
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         const int m = m0 + (wm * MT + i) * 16 + c;
         if (m >= a.M) continue;
-        const float xs = a.xs[m];
 #pragma unroll
-        for (int j = 0; j < NT; j += (GATED ? 2 : 1)) {
-            const int tile = wn * NT + j;
-            if (tile >= nt_here) continue;
-            if constexpr (GATED) emit_gated(a, m, xs, (nt0 + tile) / 2, 4 * g, acc[j][i], acc[j + 1][i]);
-            else emit_linear(a, m, xs, nt0 + tile, 4 * g, acc[j][i]);
+        for (int t = 0; t < CT; ++t) {
+            const int n = (ct0 + t) * TILE_N + 4 * g;
+            if constexpr (GATED) emit_gated(a, m, xs[i], n, q[2 * t], q[2 * t + 1], acc[2 * t][i], acc[2 * t + 1][i]);
+            else emit_linear(a, m, xs[i], n, q[t], acc[t][i]);
         }
     }
 }
@@ -321,20 +443,29 @@ __global__ void __launch_bounds__(256) i8_join_kernel(I8Args a) {
     if (e >= int64_t(a.M) * per_row) return;
     const int m = int(e / per_row), q = int(e % per_row), tile = q >> 2, at = 4 * (q & 3);
     const int64_t width = int64_t(a.ntiles) * TILE_N;
-    auto total = [&](int t) {
+    emit<GATED>(a, m, tile, at, [&](int t) {
         i32x4 s{0, 0, 0, 0};
         for (int k = 0; k < a.ks; ++k)
             s += *reinterpret_cast<const i32x4 *>(a.part + (int64_t(k) * a.M + m) * width + int64_t(t) * TILE_N + at);
         return s;
-    };
-    if constexpr (GATED) emit_gated(a, m, a.xs[m], tile, at, total(2 * tile), total(2 * tile + 1));
-    else emit_linear(a, m, a.xs[m], tile, at, total(tile));
+    });
 }
 
 constexpr I8Cfg CFGS[] = {
-    {0, 1, 2, 8, 1, 1, 1, 0}, {0, 2, 2, 8, 1, 1, 1, 0}, {0, 4, 2, 8, 1, 1, 1, 0},
-    {1, 2, 2, 1, 2, 2, 2, 4}, {1, 4, 4, 1, 2, 2, 2, 4}, {1, 8, 4, 1, 2, 4, 2, 2},
+    {0, 1, 2, 8, 1, 1, 0}, {0, 2, 2, 8, 1, 1, 0}, {0, 4, 2, 8, 1, 1, 0},
+    {1, 8, 4, 1, 2, 4, 5},      // 256 x 256
+    {1, 4, 4, 1, 2, 4, 5},      // 128 x 256
+    {1, 4, 2, 1, 2, 4, 5},      // 128 x 128
+    {1, 2, 2, 1, 2, 4, 6},      // 64 x 128
+    {1, 2, 2, 4, 2, 2, 5},      // 64 x 64, four groups
 };
+constexpr int FIRST_TILE = 3, NUM_CFGS = 8;
+// Microseconds that a compute unit takes for one chunk of a workgroup's tile, and for the
+// tile besides (start, first loads, stores): from runs with one workgroup a unit over 4096 to
+// 14336 inputs.  128 x 128 and 64 x 128 with twice the groups on twice the wavefronts, and
+// 64 x 128 tiles of four wavefronts, were slower wherever they were tried.
+constexpr float CHUNK_US[NUM_CFGS] = {0, 0, 0, 0.75f, 0.43f, 0.28f, 0.15f, 0.09f};
+constexpr float TILE_US = 4.0f, JOIN_US = 5.0f, JOIN_BYTES_PER_US = 4.0e6f;
 constexpr int ROWS_U = 4;
 
 template <typename F>
@@ -356,17 +487,17 @@ hipError_t launch_rows(const I8Args &a, hipStream_t st) {
 template <int I, bool GATED>
 hipError_t launch_tiles(const I8Args &a, hipStream_t st) {
     constexpr I8Cfg t = CFGS[I];
-    constexpr size_t lds = size_t(t.S) * (16 * t.MT * t.WM + 16 * t.NT * t.WN) * t.CPS * I8_CHUNK;
+    constexpr size_t lds = size_t(t.S) * t.WK * (t.MT * t.WM + t.NT * t.WN) * TILE_BYTES;
     const dim3 grid(unsigned(a.mtiles * a.nblocks), unsigned(a.ks));
-    const dim3 block(64 * t.WM * t.WN);
+    const dim3 block(64 * t.WM * t.WN * t.WK);
     if (a.ks == 1) {
-        auto kern = i8_tile_kernel<t.WM, t.WN, t.MT, t.NT, t.CPS, t.S, GATED, false>;
+        auto kern = i8_tile_kernel<t.WM, t.WN, t.WK, t.MT, t.NT, t.S, GATED, false>;
         static const hipError_t set = allow_lds(kern, lds);
         if (set != hipSuccess) return set;
         hipLaunchKernelGGL(kern, grid, block, lds, st, a);
         return hipGetLastError();
     }
-    auto kern = i8_tile_kernel<t.WM, t.WN, t.MT, t.NT, t.CPS, t.S, GATED, true>;
+    auto kern = i8_tile_kernel<t.WM, t.WN, t.WK, t.MT, t.NT, t.S, GATED, true>;
     static const hipError_t set = allow_lds(kern, lds);
     if (set != hipSuccess) return set;
     hipLaunchKernelGGL(kern, grid, block, lds, st, a);
@@ -385,35 +516,52 @@ hipError_t launch_any(int cfg, const I8Args &a, hipStream_t st) {
         case 2: return launch_rows<2, GATED>(a, st);
         case 3: return launch_tiles<3, GATED>(a, st);
         case 4: return launch_tiles<4, GATED>(a, st);
-        default: return launch_tiles<5, GATED>(a, st);
+        case 5: return launch_tiles<5, GATED>(a, st);
+        case 6: return launch_tiles<6, GATED>(a, st);
+        default: return launch_tiles<7, GATED>(a, st);
     }
 }
 
 }  // namespace
 
+// Few rows stream the weight through registers.  More take the tile and the split of the
+// input dimension whose time is least by the measured rates: rounds of workgroups over 256
+// compute units, and for a split the partial sums' way to memory and back and a launch.
+// Measured against every other tile at 128, 256, 512 and 1024 x 4096 x 4096 and 14336, 333 x
+// 5001 x 4128 and 77 x 5003 x 2080 gated, its choice was the fastest or within 4% of it.
 I8Plan make_i8_plan(const I8Layout &L, int64_t M) {
     I8Plan p;
-    if (M <= 64) p.cfg = M <= 16 ? 0 : (M <= 32 ? 1 : 2);
-    else {
-        p.cfg = 5;
-        for (int c : {5, 4, 3}) {
-            p.cfg = c;
-            const I8Cfg &t = CFGS[c];
-            if (ceil_div(M, 16 * t.MT * t.WM) * ceil_div(L.ntiles, t.NT * t.WN) >= 192) break;
+    p.cps = int(L.kchunks);
+    auto blocks = [&](int c, int64_t &mt, int64_t &nb) {
+        const I8Cfg &t = CFGS[c];
+        mt = ceil_div(M, 16 * t.MT * t.WM);
+        nb = ceil_div(L.ntiles, t.NT * t.WN);
+    };
+    int64_t mt, nb;
+    if (M <= 64) {
+        p.cfg = M <= 16 ? 0 : (M <= 32 ? 1 : 2);
+    } else {
+        float best = 0.0f;
+        for (int c = FIRST_TILE; c < NUM_CFGS; ++c) {
+            blocks(c, mt, nb);
+            for (int ks : {1, 2, 3, 4, 6, 8}) {
+                const int64_t cps = ceil_div(ceil_div(L.kchunks, ks), CFGS[c].WK) * CFGS[c].WK;
+                if (ks > 1 && (cps < 8 * CFGS[c].WK || ceil_div(L.kchunks, cps) < ks)) break;
+                float us = float(ceil_div(mt * nb * ks, 256)) * (float(cps) * CHUNK_US[c] + TILE_US);
+                if (ks > 1) us += JOIN_US + float(ks) * float(M) * float(L.ntiles) * TILE_N * 8.0f / JOIN_BYTES_PER_US;
+                if ((c == FIRST_TILE && ks == 1) || us < best) {
+                    best = us;
+                    p.cfg = c;
+                    p.ks = ks;
+                    p.cps = int(cps);
+                }
+            }
         }
     }
-    const I8Cfg &t = CFGS[p.cfg];
-    p.mtiles = int(ceil_div(M, 16 * t.MT * t.WM));
-    p.nblocks = int(ceil_div(L.ntiles, t.NT * t.WN));
-    p.cps = int(L.kchunks);
-    if (t.kind == 1) {
-        const int64_t wgs = int64_t(p.mtiles) * p.nblocks;
-        int64_t ks = wgs >= 192 ? 1 : ceil_div(256, wgs);
-        ks = std::max<int64_t>(1, std::min<int64_t>(ks, L.kchunks / (4 * t.CPS)));
-        p.cps = int(ceil_div(ceil_div(L.kchunks, ks), t.CPS) * t.CPS);
-        p.ks = int(ceil_div(L.kchunks, p.cps));
-        if (p.ks > 1) p.ws_bytes = round256(size_t(p.ks) * size_t(M) * size_t(L.ntiles) * TILE_N * 4);
-    }
+    blocks(p.cfg, mt, nb);
+    p.mtiles = int(mt);
+    p.nblocks = int(nb);
+    if (p.ks > 1) p.ws_bytes = round256(size_t(p.ks) * size_t(M) * size_t(L.ntiles) * TILE_N * 4);
     return p;
 }
 

@@ -28,26 +28,37 @@
 namespace ql {
 namespace {
 
+// Rows are read and written through ranged buffers of exactly their own bytes: what lies past
+// the row's end, or belongs to an absent tensor (no bytes at all), reads as zero and is not
+// written, so no access is predicated.  (The whole offset stands in the lane's part of the
+// address: the scalar part takes no part in the range check.)
+// Zeros past the end add nothing to any sum, and whatever is formed from them stays there.
 template <int V>
 struct Raw { uint32_t w[V == 8 ? 8 : 1]; };   // V values as stored: bf16 (half used) or float32
 
-// V values at element i of a bf16 or float32 array; V = 8 needs 16-byte aligned addresses
+__device__ inline __amdgpu_buffer_rsrc_t row_of(const void *p, int64_t row, int C, bool f32) {
+    const int64_t es = f32 ? 4 : 2;
+    return make_rsrc(static_cast<const uint8_t *>(p) + row * C * es, p ? uint32_t(C) * uint32_t(es) : 0u);
+}
+
+// V values at element `lane + skip` of a row; V = 8 needs 16-byte aligned rows
 template <int V>
-__device__ inline Raw<V> load_raw(const void *p, int64_t i, bool f32) {
+__device__ inline Raw<V> load_raw(__amdgpu_buffer_rsrc_t p, int lane, int skip, bool f32) {
     Raw<V> r;
     if constexpr (V == 8) {
         if (f32) {
-            const u32x4 a = *reinterpret_cast<const u32x4 *>(static_cast<const float *>(p) + i);
-            const u32x4 b = *reinterpret_cast<const u32x4 *>(static_cast<const float *>(p) + i + 4);
+            const u32x4 a = __builtin_amdgcn_raw_buffer_load_b128(p, (lane + skip) * 4, 0, 0);
+            const u32x4 b = __builtin_amdgcn_raw_buffer_load_b128(p, (lane + skip) * 4 + 16, 0, 0);
 #pragma unroll
             for (int j = 0; j < 4; ++j) { r.w[j] = a[j]; r.w[4 + j] = b[j]; }
         } else {
-            const u32x4 a = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p) + i);
+            const u32x4 a = __builtin_amdgcn_raw_buffer_load_b128(p, (lane + skip) * 2, 0, 0);
 #pragma unroll
             for (int j = 0; j < 4; ++j) r.w[j] = a[j];
         }
     } else {
-        r.w[0] = f32 ? static_cast<const uint32_t *>(p)[i] : uint32_t(static_cast<const uint16_t *>(p)[i]);
+        r.w[0] = f32 ? __builtin_amdgcn_raw_buffer_load_b32(p, (lane + skip) * 4, 0, 0)
+                     : uint32_t(__builtin_amdgcn_raw_buffer_load_b16(p, (lane + skip) * 2, 0, 0));
     }
     return r;
 }
@@ -62,19 +73,21 @@ __device__ inline void widen(const Raw<V> &r, bool f32, float *v) {
     }
 }
 template <int V>
-__device__ inline void store_row(void *p, int64_t i, bool f32, const float *v) {
+__device__ inline void store_row(__amdgpu_buffer_rsrc_t p, int lane, int skip, bool f32, const float *v) {
     if constexpr (V == 8) {
         if (f32) {
-            float *q = static_cast<float *>(p) + i;
-            *reinterpret_cast<f32x4 *>(q) = f32x4{v[0], v[1], v[2], v[3]};
-            *reinterpret_cast<f32x4 *>(q + 4) = f32x4{v[4], v[5], v[6], v[7]};
+            const u32x4 a{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+            const u32x4 b{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+            __builtin_amdgcn_raw_buffer_store_b128(a, p, (lane + skip) * 4, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(b, p, (lane + skip) * 4 + 16, 0, 0);
         } else {
-            *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p) + i) =
-                u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+            const u32x4 a{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+            __builtin_amdgcn_raw_buffer_store_b128(a, p, (lane + skip) * 2, 0, 0);
         }
     } else {
-        if (f32) static_cast<float *>(p)[i] = v[0];
-        else static_cast<__bf16 *>(p)[i] = (__bf16)v[0];
+        if (f32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), p, (lane + skip) * 4, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (__bf16)v[0]), p, (lane + skip) * 2, 0, 0);
     }
 }
 
@@ -106,62 +119,57 @@ __device__ inline void reduce(float (&v)[N], float *red, int &turn, int waves) {
 }
 
 // ---- forward ---------------------------------------------------------------------------
-// V values per load, NV loads per thread and row; KEEP: weight vectors stay in registers.
+// V values per load, NV loads per thread and row: load v covers values (v T + t) V ..; rows
+// of up to 8 values a thread keep their weight vectors in registers and fetch a row ahead,
+// longer ones read the vectors again for each row.
 template <int V, int NV, int TMAX, bool RF32>
 __global__ void __launch_bounds__(TMAX) block_norm_kernel(NormArgs a) {
-    constexpr bool KEEP = V * NV <= 16;
     constexpr int E = V * NV;
+    constexpr bool KEEP = E <= 8;
     __shared__ float red[2 * 16 * 4];
-    const int t = threadIdx.x, T = blockDim.x, waves = T >> 6;
+    const int T = blockDim.x, waves = T >> 6, t = threadIdx.x * V;
     int turn = 0;
     const int row0 = blockIdx.x * a.rows_per_wg, row1 = min(a.R, row0 + a.rows_per_wg);
     const float inv_c = 1.0f / float(a.C);
     const bool pf32 = !a.p_bf16;
 
-    int at[NV];
-    bool in[NV];
+    const int step = T * V;
+    // vector `index` of a parameter, ones where it is absent
+    auto param = [&](const void *p, int64_t index, int v, float *out) {
+        if (p) widen<V>(load_raw<V>(row_of(p, index, a.C, pf32), t, v * step, pf32), pf32, out);
+        else
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        at[v] = (v * T + t) * V;
-        in[v] = at[v] < a.C;
-    }
-    auto params = [&](const void *p, int64_t base, float one, float *out) {
+            for (int j = 0; j < V; ++j) out[j] = 1.0f;
+    };
+    float post[KEEP ? E : V], pre[KEEP ? E : V], gate[KEEP ? E : V];
+    if constexpr (KEEP) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            if (p && in[v]) widen<V>(load_raw<V>(p, base + at[v], pf32), pf32, out + v * V);
-            else
-#pragma unroll
-                for (int j = 0; j < V; ++j) out[v * V + j] = one;
+            param(a.post, 0, v, post + v * V);
+            param(a.pre, 0, v, pre + v * V);
         }
-    };
-    float post[KEEP ? E : 1], pre[KEEP ? E : 1], gate[KEEP ? E : 1];
-    if constexpr (KEEP) {
-        params(a.post, 0, 1.0f, post);
-        params(a.pre, 0, 1.0f, pre);
     }
     int64_t gate_of = -1;
 
     Raw<V> ny[NV], nr[NV];
     auto fetch = [&](int row) {
+        const __amdgpu_buffer_rsrc_t py = row_of(a.y, row, a.C, false), pr = row_of(a.r, row, a.C, RF32);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            ny[v] = Raw<V>{};
-            nr[v] = Raw<V>{};
-            if (in[v]) {
-                if (a.y) ny[v] = load_raw<V>(a.y, int64_t(row) * a.C + at[v], false);
-                nr[v] = load_raw<V>(a.r, int64_t(row) * a.C + at[v], RF32);
-            }
+            ny[v] = load_raw<V>(py, t, v * step, false);
+            nr[v] = load_raw<V>(pr, t, v * step, RF32);
         }
     };
-    if (row0 < row1) fetch(row0);
+    if (KEEP && row0 < row1) fetch(row0);
     for (int row = row0; row < row1; ++row) {
         float y[E], r[E];
+        if (!KEEP) fetch(row);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             widen<V>(ny[v], false, y + v * V);
             widen<V>(nr[v], RF32, r + v * V);
         }
-        if (row + 1 < row1) fetch(row + 1);
+        if (KEEP && row + 1 < row1) fetch(row + 1);
 
         if (a.y) {
             float ip = 1.0f;
@@ -173,73 +181,67 @@ __global__ void __launch_bounds__(TMAX) block_norm_kernel(NormArgs a) {
                 ip = rsqrtf(fmaf(ss[0], inv_c, a.eps));
             }
             const int64_t gb = a.gate_rows ? row / a.gate_rows : 0;
-            float gl[KEEP ? 1 : E], pl[KEEP ? 1 : E];
-            if constexpr (KEEP) {
-                if (gb != gate_of) params(a.gate, gb * a.C, 1.0f, gate);
-                gate_of = gb;
-            } else {
-                params(a.gate, gb * a.C, 1.0f, gl);
-                params(a.post, 0, 1.0f, pl);
-            }
+            const bool new_gate = gb != gate_of;
+            gate_of = gb;
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float w = KEEP ? post[KEEP ? e : 0] : pl[KEEP ? 0 : e];
-                const float gv = KEEP ? gate[KEEP ? e : 0] : gl[KEEP ? 0 : e];
-                r[e] = fmaf(gv, y[e] * ip * w, a.alpha * r[e]);
+            for (int v = 0; v < NV; ++v) {
+                float *w = KEEP ? post + v * V : post, *g = KEEP ? gate + v * V : gate;
+                if (!KEEP) param(a.post, 0, v, w);
+                if (!KEEP || new_gate) param(a.gate, gb, v, g);
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    r[v * V + j] = fmaf(g[j], y[v * V + j] * ip * w[j], a.alpha * r[v * V + j]);
             }
         } else {
 #pragma unroll
             for (int e = 0; e < E; ++e) r[e] *= a.alpha;
         }
+        const __amdgpu_buffer_rsrc_t po = row_of(a.r_out, row, a.C, RF32);
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (in[v]) store_row<V>(a.r_out, int64_t(row) * a.C + at[v], RF32, r + v * V);
+        for (int v = 0; v < NV; ++v) store_row<V>(po, t, v * step, RF32, r + v * V);
         if (!a.pre) continue;
 
         float ss[1] = {0.0f};
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int j = 0; j < V; ++j) ss[0] = in[v] ? fmaf(r[v * V + j], r[v * V + j], ss[0]) : ss[0];
+        for (int e = 0; e < E; ++e) ss[0] = fmaf(r[e], r[e], ss[0]);
         reduce<1, false>(ss, red, turn, waves);
         const float iq = rsqrtf(fmaf(ss[0], inv_c, a.eps));
-        float ql[KEEP ? 1 : E];
-        if constexpr (!KEEP) params(a.pre, 0, 1.0f, ql);
 #pragma unroll
-        for (int e = 0; e < E; ++e) r[e] = r[e] * iq * (KEEP ? pre[KEEP ? e : 0] : ql[KEEP ? 0 : e]);
+        for (int v = 0; v < NV; ++v) {
+            float *w = KEEP ? pre + v * V : pre;
+            if (!KEEP) param(a.pre, 0, v, w);
+#pragma unroll
+            for (int j = 0; j < V; ++j) r[v * V + j] = r[v * V + j] * iq * w[j];
+        }
         if (a.x) {
+            const __amdgpu_buffer_rsrc_t px = row_of(a.x, row, a.C, false);
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
-                if (in[v]) store_row<V>(a.x, int64_t(row) * a.C + at[v], false, r + v * V);
+            for (int v = 0; v < NV; ++v) store_row<V>(px, t, v * step, false, r + v * V);
             continue;
         }
         float am[1] = {0.0f};
         bool bad = false;                               // a maximum would drop NaN
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (in[v]) {
-                    am[0] = fmaxf(am[0], fabsf(r[v * V + j]));
-                    bad |= r[v * V + j] != r[v * V + j];
-                }
+        for (int e = 0; e < E; ++e) {
+            am[0] = fmaxf(am[0], fabsf(r[e]));
+            bad |= r[e] != r[e];
+        }
         if (bad) am[0] = INFINITY;
         reduce<1, true>(am, red, turn, waves);
         // a row with NaN or infinity has the scale NaN and codes 0, so its products are NaN
         const float s = am[0] < INFINITY ? __fdiv_rn(am[0], 127.0f) : __uint_as_float(0x7FC00000u);
-        if (t == 0) a.scales[row] = s;
+        if (threadIdx.x == 0) a.scales[row] = s;
+        const __amdgpu_buffer_rsrc_t pq = make_rsrc(a.codes + int64_t(row) * a.C, uint32_t(a.C));
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            if (!in[v]) continue;
             uint32_t q[2] = {0u, 0u};
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float f = s > 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(r[v * V + j], s)), -127.0f), 127.0f) : 0.0f;
                 q[j >> 2] |= (uint32_t(int(f)) & 0xFFu) << (8 * (j & 3));
             }
-            int8_t *dst = a.codes + int64_t(row) * a.C + at[v];
-            if constexpr (V == 8) *reinterpret_cast<u32x2 *>(dst) = u32x2{q[0], q[1]};
-            else dst[0] = int8_t(q[0]);
+            if constexpr (V == 8) __builtin_amdgcn_raw_buffer_store_b64(u32x2{q[0], q[1]}, pq, t + v * step, 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b8((unsigned char)q[0], pq, t + v * step, 0, 0);
         }
     }
 }
@@ -249,11 +251,11 @@ __global__ void __launch_bounds__(TMAX) block_norm_kernel(NormArgs a) {
 // more gates than workgroups (cpb = 1), all rows of gpw gates.  The column sums stay in
 // registers and leave once a workgroup (dgate: once a gate where cpb = 1).
 template <int V, int NV, int TMAX, bool RF32>
-__global__ void __launch_bounds__(TMAX) block_norm_back_kernel(NormBackArgs a) {
-    constexpr bool KEEP = V * NV <= 8;
+__global__ void __launch_bounds__(TMAX, NV <= (V == 8 ? 1 : 4) ? 4 : 1) block_norm_back_kernel(NormBackArgs a) {
     constexpr int E = V * NV;
+    constexpr bool KEEP = E <= 8;
     __shared__ float red[2 * 16 * 4];
-    const int t = threadIdx.x, T = blockDim.x, waves = T >> 6;
+    const int T = blockDim.x, waves = T >> 6, t = threadIdx.x * V;
     int turn = 0;
     const float inv_c = 1.0f / float(a.C);
     const bool pf32 = !a.p_bf16;
@@ -267,31 +269,25 @@ __global__ void __launch_bounds__(TMAX) block_norm_back_kernel(NormBackArgs a) {
         row1 = min(int64_t(a.R), row0 + a.rows_per_wg);
     }
 
-    int at[NV];
-    bool in[NV];
+    const int step = T * V;
+    auto param = [&](const void *p, int64_t index, int v, float *out) {
+        if (p) widen<V>(load_raw<V>(row_of(p, index, a.C, pf32), t, v * step, pf32), pf32, out);
+        else
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        at[v] = (v * T + t) * V;
-        in[v] = at[v] < a.C;
-    }
-    auto params = [&](const void *p, int64_t base, float *out) {
+            for (int j = 0; j < V; ++j) out[j] = 1.0f;
+    };
+    auto sums_out = [&](float *dst, int64_t index, const float *v0) {
+        const __amdgpu_buffer_rsrc_t p = row_of(dst, index, a.C, true);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) store_row<V>(p, t, v * step, true, v0 + v * V);
+    };
+    float post[KEEP ? E : V], pre[KEEP ? E : V], gate[KEEP ? E : V];
+    if constexpr (KEEP) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            if (p && in[v]) widen<V>(load_raw<V>(p, base + at[v], pf32), pf32, out + v * V);
-            else
-#pragma unroll
-                for (int j = 0; j < V; ++j) out[v * V + j] = 1.0f;
+            param(a.post, 0, v, post + v * V);
+            param(a.pre, 0, v, pre + v * V);
         }
-    };
-    auto sums_out = [&](float *dst, const float *v0) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (in[v]) store_row<V>(dst, at[v], true, v0 + v * V);
-    };
-    float post[KEEP ? E : 1], pre[KEEP ? E : 1], gate[KEEP ? E : 1];
-    if constexpr (KEEP) {
-        params(a.post, 0, post);
-        params(a.pre, 0, pre);
     }
     int64_t gate_of = -1;
     float s_post[E], s_pre[E], s_gate[E];
@@ -300,23 +296,20 @@ __global__ void __launch_bounds__(TMAX) block_norm_back_kernel(NormBackArgs a) {
 
     Raw<V> ny[NV], nr[NV], nx[NV], nd[NV];
     auto fetch = [&](int64_t row) {
+        const __amdgpu_buffer_rsrc_t py = row_of(a.y, row, a.C, false), pr = row_of(a.pre ? a.r : nullptr, row, a.C, RF32),
+                                     px = row_of(a.dx, row, a.C, false), pd = row_of(a.dres, row, a.C, RF32);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            ny[v] = nr[v] = nx[v] = nd[v] = Raw<V>{};
-            if (in[v]) {
-                const int64_t j = row * a.C + at[v];
-                if (a.y) ny[v] = load_raw<V>(a.y, j, false);
-                if (a.pre) {
-                    nr[v] = load_raw<V>(a.r, j, RF32);
-                    nx[v] = load_raw<V>(a.dx, j, false);
-                }
-                if (a.dres) nd[v] = load_raw<V>(a.dres, j, RF32);
-            }
+            ny[v] = load_raw<V>(py, t, v * step, false);
+            nr[v] = load_raw<V>(pr, t, v * step, RF32);
+            nx[v] = load_raw<V>(px, t, v * step, false);
+            nd[v] = load_raw<V>(pd, t, v * step, RF32);
         }
     };
-    if (row0 < row1) fetch(row0);
+    if (KEEP && row0 < row1) fetch(row0);
     for (int64_t row = row0; row < row1; ++row) {
         float y[E], r[E], x[E], d[E];
+        if (!KEEP) fetch(row);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             widen<V>(ny[v], false, y + v * V);
@@ -324,17 +317,21 @@ __global__ void __launch_bounds__(TMAX) block_norm_back_kernel(NormBackArgs a) {
             widen<V>(nx[v], false, x + v * V);
             widen<V>(nd[v], RF32, d + v * V);
         }
-        if (row + 1 < row1) fetch(row + 1);
+        if (KEEP && row + 1 < row1) fetch(row + 1);
 
-        float ql[KEEP ? 1 : E];
-        if constexpr (!KEEP) params(a.pre, 0, ql);
-        auto pre_of = [&](int e) { return KEEP ? pre[KEEP ? e : 0] : ql[KEEP ? 0 : e]; };
+        // n = dx w_pre replaces x in the second half: x itself is needed for dw_pre
         float ss[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            ss[0] = fmaf(y[e], y[e], ss[0]);
-            ss[1] = fmaf(r[e], r[e], ss[1]);
-            ss[2] = fmaf(x[e] * pre_of(e), r[e], ss[2]);
+        for (int v = 0; v < NV; ++v) {
+            float *w = KEEP ? pre + v * V : pre;
+            if (!KEEP) param(a.pre, 0, v, w);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int e = v * V + j;
+                ss[0] = fmaf(y[e], y[e], ss[0]);
+                ss[1] = fmaf(r[e], r[e], ss[1]);
+                ss[2] = fmaf(x[e] * w[j], r[e], ss[2]);
+            }
         }
         reduce<3, false>(ss, red, turn, waves);
         const float ip = a.post ? rsqrtf(fmaf(ss[0], inv_c, a.eps)) : 1.0f;
@@ -342,39 +339,44 @@ __global__ void __launch_bounds__(TMAX) block_norm_back_kernel(NormBackArgs a) {
             const float iq = rsqrtf(fmaf(ss[1], inv_c, a.eps));
             const float along = ss[2] * iq * inv_c;          // mean(n u)
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float u = r[e] * iq;
-                d[e] = fmaf(iq, x[e] * pre_of(e) - u * along, d[e]);
-                s_pre[e] = fmaf(x[e], u, s_pre[e]);
+            for (int v = 0; v < NV; ++v) {
+                float *w = KEEP ? pre + v * V : pre;
+                if (!KEEP) param(a.pre, 0, v, w);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const int e = v * V + j;
+                    const float u = r[e] * iq;
+                    d[e] = fmaf(iq, x[e] * w[j] - u * along, d[e]);
+                    s_pre[e] = fmaf(x[e], u, s_pre[e]);
+                }
             }
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) r[e] = a.alpha * d[e];
+        const __amdgpu_buffer_rsrc_t po = row_of(a.dr, row, a.C, RF32);
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (in[v]) store_row<V>(a.dr, row * a.C + at[v], RF32, r + v * V);
+        for (int v = 0; v < NV; ++v) store_row<V>(po, t, v * step, RF32, r + v * V);
         if (!a.y) continue;
 
         const int64_t gb = a.gate_rows ? row / a.gate_rows : 0;
-        float gl[KEEP ? 1 : E], pl[KEEP ? 1 : E];
-        if constexpr (KEEP) {
-            if (gb != gate_of) params(a.gate, gb * a.C, gate);
-            gate_of = gb;
-        } else {
-            params(a.gate, gb * a.C, gl);
-            params(a.post, 0, pl);
-        }
+        const bool new_gate = gb != gate_of;
+        gate_of = gb;
         float dot[1] = {0.0f};
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float w = KEEP ? post[KEEP ? e : 0] : pl[KEEP ? 0 : e];
-            const float gv = KEEP ? gate[KEEP ? e : 0] : gl[KEEP ? 0 : e];
-            const float v = y[e] * ip;
-            s_gate[e] = fmaf(d[e] * w, v, s_gate[e]);
-            const float dt = d[e] * gv;
-            s_post[e] = fmaf(dt, v, s_post[e]);
-            d[e] = dt * w;
-            dot[0] = fmaf(d[e], v, dot[0]);
+        for (int v = 0; v < NV; ++v) {
+            float *w = KEEP ? post + v * V : post, *g = KEEP ? gate + v * V : gate;
+            if (!KEEP) param(a.post, 0, v, w);
+            if (!KEEP || new_gate) param(a.gate, gb, v, g);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int e = v * V + j;
+                const float u = y[e] * ip;
+                s_gate[e] = fmaf(d[e] * w[j], u, s_gate[e]);
+                const float dt = d[e] * g[j];
+                s_post[e] = fmaf(dt, u, s_post[e]);
+                d[e] = dt * w[j];
+                dot[0] = fmaf(d[e], u, dot[0]);
+            }
         }
         if (a.post) {
             reduce<1, false>(dot, red, turn, waves);
@@ -382,19 +384,18 @@ __global__ void __launch_bounds__(TMAX) block_norm_back_kernel(NormBackArgs a) {
 #pragma unroll
             for (int e = 0; e < E; ++e) d[e] = ip * (d[e] - y[e] * ip * along);
         }
+        const __amdgpu_buffer_rsrc_t pz = row_of(a.dy, row, a.C, false);
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (in[v]) store_row<V>(a.dy, row * a.C + at[v], false, d + v * V);
-        if (a.dgate && a.cpb == 1 && (row + 1) % a.gate_rows == 0) {   // this gate is complete
-            sums_out(a.dgate + gb * a.C, s_gate);
+        for (int v = 0; v < NV; ++v) store_row<V>(pz, t, v * step, false, d + v * V);
+        if (a.dgate && (row + 1) % a.gate_rows == 0) {        // this gate is complete
+            sums_out(a.dgate, gb, s_gate);
 #pragma unroll
             for (int e = 0; e < E; ++e) s_gate[e] = 0.0f;
         }
     }
-    const int64_t slot = int64_t(i) * a.C;
-    if (a.part_post) sums_out(a.part_post + slot, s_post);
-    if (a.part_pre) sums_out(a.part_pre + slot, s_pre);
-    if (a.part_gate) sums_out(a.part_gate + slot, s_gate);
+    if (a.part_post) sums_out(a.part_post, i, s_post);
+    if (a.part_pre) sums_out(a.part_pre, i, s_pre);
+    if (a.part_gate) sums_out(a.part_gate, i, s_gate);
 }
 
 // out[b][c] = sum over `count` consecutive rows of part, in a fixed order: 16 row groups of
@@ -419,9 +420,15 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(ColumnSums a) {
     }
 }
 
-int threads_for(int64_t C, int V, int NV, int most) {
-    const int64_t t = ceil_div(ceil_div(C, int64_t(V) * NV), 64) * 64;
-    return int(std::min<int64_t>(t, most));
+// The least number of loads per thread among those compiled with which `most` threads cover
+// a row, and that many threads in whole wavefronts.
+template <int N>
+int loads_per_thread(int64_t C, int V, int most, const int (&choices)[N], int &T) {
+    int nv = choices[N - 1];
+    for (int i = N - 1; i >= 0; --i)
+        if (int64_t(choices[i]) * V * most >= C) nv = choices[i];
+    T = int(ceil_div(ceil_div(C, int64_t(V) * nv), 64) * 64);
+    return nv;
 }
 
 template <int V, int NV, int TMAX>
@@ -441,23 +448,21 @@ hipError_t launch_bwd(const NormBackArgs &a, int T, int wgs, hipStream_t st) {
 
 hipError_t launch_block_norm(const NormArgs &args, bool vec, hipStream_t st) {
     NormArgs a = args;
-    const int V = vec ? 8 : 1;
-    // loads per thread: as few as 512 threads allow, so that a row's latency is short
-    int NV = 1;
-    const int64_t pieces = ceil_div(a.C, V);
-    const int most = pieces > 512 * 4 * (vec ? 1 : 8) ? 1024 : 512;
-    if (vec) while (int64_t(most) * NV < pieces) NV *= 2;
-    else NV = int64_t(most) * 8 >= pieces ? 8 : 32;
-    const int T = threads_for(a.C, V, NV, most);
+    int T, NV;
+    // as few values a thread as 512 threads allow (a short row's latency), then 1024 threads
+    if (vec) NV = loads_per_thread(a.C, 8, a.C > 512 * 16 ? 1024 : 512, {1, 2, 4}, T);
+    else NV = loads_per_thread(a.C, 1, a.C > 512 * 16 ? 1024 : 512, {4, 8, 16, 32}, T);
     const int64_t wgs = std::min<int64_t>(a.R, 256 * (2048 / std::max(T, 256)));
     a.rows_per_wg = int(ceil_div(a.R, wgs));
     const int grid = int(ceil_div(a.R, a.rows_per_wg));
     if (vec) {
-        if (NV == 1) return launch_fwd<8, 1, 512>(a, T, grid, st);
-        if (NV == 2) return launch_fwd<8, 2, 512>(a, T, grid, st);
+        if (NV == 1) return launch_fwd<8, 1, 1024>(a, T, grid, st);
+        if (NV == 2) return launch_fwd<8, 2, 1024>(a, T, grid, st);
         return launch_fwd<8, 4, 1024>(a, T, grid, st);
     }
-    if (NV == 8) return launch_fwd<1, 8, 512>(a, T, grid, st);
+    if (NV == 4) return launch_fwd<1, 4, 512>(a, T, grid, st);
+    if (NV == 8) return launch_fwd<1, 8, 1024>(a, T, grid, st);
+    if (NV == 16) return launch_fwd<1, 16, 1024>(a, T, grid, st);
     return launch_fwd<1, 32, 1024>(a, T, grid, st);
 }
 
@@ -497,21 +502,24 @@ hipError_t launch_block_norm_back(const NormBackArgs &args, const NormBackPlan &
     a.part_gate = has_gate && p.cpb != 1 ? reinterpret_cast<float *>(w + p.off_gate) : nullptr;
     a.dgate = has_gate && p.cpb == 1 ? dgate : nullptr;
 
-    const int V = vec ? 8 : 1;
-    const int64_t pieces = ceil_div(a.C, V);
-    const int most = pieces > 512 * 4 * (vec ? 1 : 8) ? 1024 : 512;
-    int NV = 1;
-    if (vec) while (int64_t(most) * NV < pieces) NV *= 2;
-    else NV = int64_t(most) * 8 >= pieces ? 8 : 32;
-    const int T = threads_for(a.C, V, NV, most), grid = int(p.wgs);
+    // 512 threads leave 256 registers each; only rows past 16384 need 1024
+    int T, NV;
+    const int most = a.C > 512 * 32 ? 1024 : 512;
+    if (vec) NV = loads_per_thread(a.C, 8, most, {1, 2, 4}, T);
+    else NV = loads_per_thread(a.C, 1, most, {4, 8, 16, 32}, T);
+    const int grid = int(p.wgs);
     hipError_t e = hipSuccess;
     if (grid == 0) {
         // no rows: the sums below are empty and write zeros
     } else if (vec) {
         if (NV == 1) e = launch_bwd<8, 1, 512>(a, T, grid, st);
         else if (NV == 2) e = launch_bwd<8, 2, 512>(a, T, grid, st);
+        else if (most == 512) e = launch_bwd<8, 4, 512>(a, T, grid, st);
         else e = launch_bwd<8, 4, 1024>(a, T, grid, st);
-    } else if (NV == 8) e = launch_bwd<1, 8, 512>(a, T, grid, st);
+    } else if (NV == 4) e = launch_bwd<1, 4, 512>(a, T, grid, st);
+    else if (NV == 8) e = launch_bwd<1, 8, 512>(a, T, grid, st);
+    else if (NV == 16) e = launch_bwd<1, 16, 512>(a, T, grid, st);
+    else if (most == 512) e = launch_bwd<1, 32, 512>(a, T, grid, st);
     else e = launch_bwd<1, 32, 1024>(a, T, grid, st);
     if (e != hipSuccess) return e;
 

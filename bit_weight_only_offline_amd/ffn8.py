@@ -56,14 +56,23 @@ def bind(L: ctypes.CDLL) -> None:
         f.argtypes = args
 
 
+# A decoded token's product takes a few microseconds on the GPU, so the wrappers are written
+# for few Python operations: messages are built only when a check fails, and the stream and
+# the current device are read without building objects.
+
 def _call(name: str, device: torch.device, *args) -> None:
     """One entry point on the device's current stream, with that device current."""
-    if device.index != torch.cuda.current_device():
+    index = device.index
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return _call(name, device, *args)
-    status = getattr(_Q.lib(), name)(*args, _Q._stream(device))
+    status = getattr(_Q._lib or _Q.lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
     if status:
         _Q._check(status, name)
+
+
+def _fail(message: str):
+    raise _Q.QLinearError(message)
 
 
 def _need(ok: bool, message: str) -> None:
@@ -72,19 +81,22 @@ def _need(ok: bool, message: str) -> None:
 
 
 def _tensor(t, name: str, dtypes, device=None) -> torch.Tensor:
-    _need(isinstance(t, torch.Tensor) and t.dtype in dtypes,
-          f"{name} must be a tensor of {' or '.join(str(d).replace('torch.', '') for d in dtypes)}")
-    _need(not t.requires_grad, f"{name} must not require grad: call the backward functions")
-    _need(t.device.type == "cuda", "the library runs on a HIP device only")
-    _need(device is None or t.device == device, f"{name} must be on {device}")
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        _fail(f"{name} must be a tensor of {' or '.join(str(d).replace('torch.', '') for d in dtypes)}")
+    if t.requires_grad:
+        _fail(f"{name} must not require grad: call the backward functions")
+    if not t.is_cuda:
+        _fail("the library runs on a HIP device only")
+    if device is not None and t.device != device:
+        _fail(f"{name} must be on {device}")
     return t
 
 
 def _out(out, shape, dtype, device, name="out") -> torch.Tensor:
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _need(out.dtype == dtype and tuple(out.shape) == tuple(shape) and out.is_contiguous() and out.device == device,
-          f"{name} must be a contiguous {tuple(shape)} tensor of {dtype} on {device}")
+    if out.dtype != dtype or out.shape != shape or not out.is_contiguous() or out.device != device:
+        _fail(f"{name} must be a contiguous {tuple(shape)} tensor of {dtype} on {device}")
     return out
 
 
@@ -94,14 +106,15 @@ def _space(workspace, need: int, device) -> tuple:
         return None, 0
     if workspace is None:
         workspace = _Q.workspace(device, need)
-    _need(workspace.numel() * workspace.element_size() >= need and workspace.device == device,
-          f"workspace needs {need} bytes on {device}")
+    if workspace.numel() * workspace.element_size() < need or workspace.device != device:
+        _fail(f"workspace needs {need} bytes on {device}")
     return workspace.data_ptr(), need
 
 
 def _aligned(t: torch.Tensor) -> torch.Tensor:
     """Contiguous, and on a 16-byte boundary (a view may start anywhere)."""
-    t = t.contiguous()
+    if not t.is_contiguous():
+        t = t.contiguous()
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
@@ -141,9 +154,8 @@ class ChannelWeight:
     s: torch.Tensor
     gated = False
 
-    @property
-    def device(self) -> torch.device:
-        return self.w.device
+    def __post_init__(self):
+        self.device = self.w.device
 
 
 @dataclass
@@ -155,9 +167,8 @@ class GatedWeight:
     s: torch.Tensor
     gated = True
 
-    @property
-    def device(self) -> torch.device:
-        return self.w.device
+    def __post_init__(self):
+        self.device = self.w.device
 
 
 def _canonical(codes, scales, name, device=None, shape=None):
@@ -217,18 +228,20 @@ def unpack_gated(pw: GatedWeight):
 def _activations(codes, scales, pw):
     _tensor(codes, "codes", (torch.int8,), pw.device)
     _tensor(scales, "scales", (torch.float32,), pw.device)
-    _need(codes.dim() >= 1 and codes.shape[-1] == pw.K, f"codes must be [..., {pw.K}]")
-    lead = codes.shape[:-1]
+    shape = codes.shape
+    if not shape or shape[-1] != pw.K:
+        _fail(f"codes must be [..., {pw.K}]")
     M = codes.numel() // pw.K
     _need(scales.numel() == M, "scales must hold one value a token")
-    return lead, M, _aligned(codes), scales.contiguous()
+    return shape[:-1], M, _aligned(codes), scales.contiguous()
 
 
 def _bias(bias, n, pw):
     if bias is None:
         return None
     _tensor(bias, "bias", (torch.bfloat16,), pw.device)
-    _need(bias.numel() == n, f"bias must have {n} values")
+    if bias.numel() != n:
+        _fail(f"bias must have {n} values")
     return bias.contiguous()
 
 
@@ -258,7 +271,8 @@ def gated_i8(codes: torch.Tensor, scales: torch.Tensor, pw: GatedWeight, bias: t
     (h, raw) with raw bf16 [..., 2N] = [up | gate] before the activation, which
     gated_i8_backward() reads (`raw` may also be given to be written into)."""
     _need(isinstance(pw, GatedWeight), "pw must be a GatedWeight")
-    _need(act in GATE_ACTS, f"act must be one of {sorted(GATE_ACTS)}")
+    if act not in GATE_ACTS:
+        _fail(f"act must be one of {sorted(GATE_ACTS)}")
     _need(out_dtype in _DTYPES, "out_dtype must be bfloat16 or float32")
     lead, M, codes, scales = _activations(codes, scales, pw)
     bias = _bias(bias, 2 * pw.N, pw)
@@ -278,7 +292,8 @@ def linear_i8_backward(dy: torch.Tensor, pw: ChannelWeight, out: torch.Tensor | 
     dequantised activations.  The gradient of a bias is dy summed over the tokens."""
     _need(isinstance(pw, ChannelWeight), "pw must be a ChannelWeight")
     _tensor(dy, "dy", (torch.bfloat16,), pw.device)
-    _need(dy.dim() >= 1 and dy.shape[-1] == pw.N, f"dy must be [..., {pw.N}]")
+    if not dy.shape or dy.shape[-1] != pw.N:
+        _fail(f"dy must be [..., {pw.N}]")
     dy = _aligned(dy)
     M = dy.numel() // pw.N
     out = _out(out, (*dy.shape[:-1], pw.K), torch.bfloat16, pw.device)
@@ -295,12 +310,15 @@ def gated_i8_backward(dh: torch.Tensor, raw: torch.Tensor, pw: GatedWeight, act:
     that gated_i8(keep_raw=True) returned; draw is the gradient of raw, and its sum over the
     tokens that of the bias."""
     _need(isinstance(pw, GatedWeight), "pw must be a GatedWeight")
-    _need(act in GATE_ACTS, f"act must be one of {sorted(GATE_ACTS)}")
+    if act not in GATE_ACTS:
+        _fail(f"act must be one of {sorted(GATE_ACTS)}")
     _tensor(dh, "dh", (torch.bfloat16,), pw.device)
     _tensor(raw, "raw", (torch.bfloat16,), pw.device)
-    _need(dh.dim() >= 1 and dh.shape[-1] == pw.N, f"dh must be [..., {pw.N}]")
     lead = dh.shape[:-1]
-    _need(raw.shape == (*lead, 2 * pw.N), f"raw must be {(*lead, 2 * pw.N)}")
+    if not dh.shape or dh.shape[-1] != pw.N:
+        _fail(f"dh must be [..., {pw.N}]")
+    if raw.shape != (*lead, 2 * pw.N):
+        _fail(f"raw must be {(*lead, 2 * pw.N)}")
     dh, raw = _aligned(dh), _aligned(raw)
     M = dh.numel() // pw.N
     out = _out(out, (*lead, pw.K), torch.bfloat16, pw.device)

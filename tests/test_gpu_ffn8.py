@@ -684,3 +684,38 @@ def test_refusals():
         with pytest.raises(Q.QLinearError):
             call()
             pytest.fail(f"refusal {i} did not raise")
+
+
+def test_example_stack_learns_its_gates():
+    """The example's stack: gates and norms moved off a teacher's come back towards it, and the
+    gradient of one gate agrees with the change of the loss along it (int8 activations make the
+    loss a step function at the scale of a code, hence the wide step and bound)."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "feed_forward.py")
+    spec = importlib.util.spec_from_file_location("feed_forward_example", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    stack = ex.FeedForwardStack(2, 256, 512, seed=3)
+    g = _gen(4)
+    x = torch.randn((192, 256), generator=g, device="cuda")
+    target = stack.forward(x).float()
+    for name in ("post", "gate"):
+        for p in stack.params[name]:
+            p.mul_(1 + 0.3 * torch.randn(p.shape, generator=g, device="cuda"))
+
+    def loss():
+        return float(0.5 * (stack.forward(x).float() - target).square().sum() / x.shape[0])
+    out, saved = stack.forward(x, keep=True)
+    grads, _ = stack.backward(((out.float() - target) / x.shape[0]).bfloat16(), saved)
+    gate, d = stack.params["gate"][1], torch.sign(grads["gate"][1])
+    kept = gate.clone()
+    gate.add_(0.02 * d)
+    plus = loss()
+    gate.copy_(kept - 0.02 * d)
+    minus = loss()
+    gate.copy_(kept)
+    slope, want = (plus - minus) / 0.04, float((grads["gate"][1] * d).sum())
+    assert abs(slope - want) <= 0.1 * abs(want)
+    losses = [float(stack.tune(x, target, rate=0.3)) for _ in range(12)]
+    assert losses[-1] < losses[0], losses
