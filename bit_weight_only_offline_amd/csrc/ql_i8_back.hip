@@ -362,6 +362,10 @@ struct BackCfg { int WM, WN, MT, NT; };
 constexpr BackCfg BACK_CFGS[] = {{2, 4, 8, 4}, {2, 4, 4, 4}, {2, 4, 2, 4}, {1, 8, 1, 2}};
 constexpr int NUM_BACK_CFGS = 4;
 constexpr int back_rows(const BackCfg &t) { return 16 * t.MT * t.WM; }
+// Microseconds of a compute unit for one 32-row step of a workgroup, and for its start, first
+// operands and stores; of a split's second launch, besides its sums' way to memory and back.
+constexpr float STEP_US[NUM_BACK_CFGS] = {0.86f, 0.53f, 0.45f, 0.33f};
+constexpr float START_US = 5.0f, JOIN_US = 5.0f, JOIN_BYTES_PER_US = 4.0e6f;
 
 template <int I>
 hipError_t launch_back(const I8BackArgs &a, hipStream_t st) {
@@ -400,21 +404,31 @@ hipError_t launch_back_any(int cfg, const I8BackArgs &a, hipStream_t st) {
 
 }  // namespace
 
+// Rows and split whose time is least by the measured rates, as for the forward tiles.
+// Measured against every other choice at 1 to 4096 rows, 2000 to 4096 channels and 3008 to
+// 14336 inputs, and gated 100 x 5000 x 2080 and 2048 x 14336 x 4096.
 I8BackPlan make_i8_back_plan(const I8Layout &L, int64_t M) {
     I8BackPlan p;
     p.Np = L.gated ? ceil_div(L.N, TILE_N) * TILE_N : ceil_div(L.N, 8) * 8;
-    const int64_t kblocks = ceil_div(L.kchunks, BACK_KQ);
+    const int64_t kblocks = ceil_div(L.kchunks, BACK_KQ), steps = ceil_div(L.ntiles, 2);
     p.nblocks = int(kblocks);
+    float best = 0.0f;
     for (int c = 0; c < NUM_BACK_CFGS; ++c) {
-        p.cfg = c;
-        p.mtiles = int(ceil_div(M, back_rows(BACK_CFGS[c])));
-        if (p.mtiles * kblocks >= 192) break;
+        const int64_t mtiles = ceil_div(M, back_rows(BACK_CFGS[c]));
+        for (int ks : {1, 2, 3, 4, 6, 8, 12, 16}) {
+            const int64_t nps = ceil_div(ceil_div(steps, ks), 4) * 4;      // whole groups of four
+            if (ks > 1 && (nps < 8 || ceil_div(steps, nps) < ks)) break;
+            float us = float(ceil_div(mtiles * kblocks * ks, 256)) * (float(nps) * STEP_US[c] + START_US);
+            if (ks > 1) us += JOIN_US + float(ks) * float(M) * float(L.K) * 8.0f / JOIN_BYTES_PER_US;
+            if ((c == 0 && ks == 1) || us < best) {
+                best = us;
+                p.cfg = c;
+                p.mtiles = int(mtiles);
+                p.ks = ks;
+                p.nps = int(nps);
+            }
+        }
     }
-    const int64_t steps = ceil_div(L.ntiles, 2), wgs = int64_t(p.mtiles) * p.nblocks;
-    int64_t ks = wgs >= 192 ? 1 : ceil_div(256, wgs);
-    ks = std::max<int64_t>(1, std::min<int64_t>(ks, steps / 8));
-    p.nps = int(ceil_div(ceil_div(steps, ks), 4) * 4);
-    p.ks = int(ceil_div(steps, p.nps));
     p.operand_bytes = round256(size_t(M) * size_t(p.Np) * (L.gated ? 4 : 2));
     p.ws_bytes = p.operand_bytes + (p.ks > 1 ? round256(size_t(p.ks) * size_t(M) * size_t(L.K) * 4) : 0);
     return p;
