@@ -452,19 +452,20 @@ __global__ void __launch_bounds__(256) i8_join_kernel(I8Args a) {
 }
 
 constexpr I8Cfg CFGS[] = {
-    {0, 1, 2, 8, 1, 1, 0}, {0, 2, 2, 8, 1, 1, 0}, {0, 4, 2, 8, 1, 1, 0},
+    {0, 1, 1, 8, 1, 1, 0}, {0, 1, 2, 8, 1, 1, 0},      // up to 16 rows, one or two column tiles
+    {0, 2, 1, 8, 1, 1, 0}, {0, 2, 2, 8, 1, 1, 0},      // 32 rows
     {1, 8, 4, 1, 2, 4, 5},      // 256 x 256
     {1, 4, 4, 1, 2, 4, 5},      // 128 x 256
     {1, 4, 2, 1, 2, 4, 5},      // 128 x 128
     {1, 2, 2, 1, 2, 4, 6},      // 64 x 128
     {1, 2, 2, 4, 2, 2, 5},      // 64 x 64, four groups
 };
-constexpr int FIRST_TILE = 3, NUM_CFGS = 8;
+constexpr int NUM_CFGS = 9, FIRST_TILE = 4;
 // Microseconds that a compute unit takes for one chunk of a workgroup's tile, and for the
 // tile besides (start, first loads, stores): from runs with one workgroup a unit over 4096 to
 // 14336 inputs.  128 x 128 and 64 x 128 with twice the groups on twice the wavefronts, and
 // 64 x 128 tiles of four wavefronts, were slower wherever they were tried.
-constexpr float CHUNK_US[NUM_CFGS] = {0, 0, 0, 0.75f, 0.43f, 0.28f, 0.15f, 0.09f};
+constexpr float CHUNK_US[NUM_CFGS] = {0, 0, 0.036f, 0.064f, 0.75f, 0.43f, 0.28f, 0.15f, 0.09f};
 constexpr float TILE_US = 4.0f, JOIN_US = 5.0f, JOIN_BYTES_PER_US = 4.0e6f;
 constexpr int ROWS_U = 4;
 
@@ -511,24 +512,29 @@ hipError_t launch_tiles(const I8Args &a, hipStream_t st) {
 template <bool GATED>
 hipError_t launch_any(int cfg, const I8Args &a, hipStream_t st) {
     switch (cfg) {
-        case 0: return launch_rows<0, GATED>(a, st);
+        // a gated weight's tiles come in pairs
+        case 0: if constexpr (GATED) return hipErrorInvalidValue; else return launch_rows<0, false>(a, st);
+        case 2: if constexpr (GATED) return hipErrorInvalidValue; else return launch_rows<2, false>(a, st);
         case 1: return launch_rows<1, GATED>(a, st);
-        case 2: return launch_rows<2, GATED>(a, st);
-        case 3: return launch_tiles<3, GATED>(a, st);
+        case 3: if constexpr (GATED) return launch_rows<3, true>(a, st); else return hipErrorInvalidValue;
         case 4: return launch_tiles<4, GATED>(a, st);
         case 5: return launch_tiles<5, GATED>(a, st);
         case 6: return launch_tiles<6, GATED>(a, st);
-        default: return launch_tiles<7, GATED>(a, st);
+        case 7: return launch_tiles<7, GATED>(a, st);
+        default: return launch_tiles<8, GATED>(a, st);
     }
 }
 
 }  // namespace
 
-// Few rows stream the weight through registers.  More take the tile and the split of the
-// input dimension whose time is least by the measured rates: rounds of workgroups over 256
-// compute units, and for a split the partial sums' way to memory and back and a launch.
-// Measured against every other tile at 128, 256, 512 and 1024 x 4096 x 4096 and 14336, 333 x
-// 5001 x 4128 and 77 x 5003 x 2080 gated, its choice was the fastest or within 4% of it.
+// Up to 16 rows stream the weight through registers, a workgroup one column tile of a plain
+// weight as long as that gives a compute unit at most two (4096 x 14336, one row: 10.1 us
+// against 10.4 with two tiles; 28672 x 4096, 16 rows: 19.8 against 18.9).  More rows take the
+// schedule and the split of the input dimension whose time is least by the measured rates:
+// rounds of workgroups over 256 compute units, and for a split the partial sums' way to
+// memory and back and a launch.  Measured against every other tile at 17 to 2048 x 4096 x
+// 4096 and 14336, 333 x 5001 x 4128, 1500 x 3000 x 2048, and gated 77 x 5003 x 2080, 32 and
+// 64 x 14336 x 4096 and 700 x 2000 x 4096, its choice was the fastest or within 6% of it.
 I8Plan make_i8_plan(const I8Layout &L, int64_t M) {
     I8Plan p;
     p.cps = int(L.kchunks);
@@ -538,20 +544,23 @@ I8Plan make_i8_plan(const I8Layout &L, int64_t M) {
         nb = ceil_div(L.ntiles, t.NT * t.WN);
     };
     int64_t mt, nb;
-    if (M <= 64) {
-        p.cfg = M <= 16 ? 0 : (M <= 32 ? 1 : 2);
+    if (M <= 16) {
+        p.cfg = !L.gated && L.ntiles <= 512 ? 0 : 1;
     } else {
         float best = 0.0f;
-        for (int c = FIRST_TILE; c < NUM_CFGS; ++c) {
-            blocks(c, mt, nb);
+        for (int c = FIRST_TILE - 1; c < NUM_CFGS; ++c) {
+            const bool rows = c < FIRST_TILE;
+            if (rows && M > 64) continue;
+            const int cfg = rows && !L.gated ? 2 : c;
+            blocks(cfg, mt, nb);
             for (int ks : {1, 2, 3, 4, 6, 8}) {
-                const int64_t cps = ceil_div(ceil_div(L.kchunks, ks), CFGS[c].WK) * CFGS[c].WK;
-                if (ks > 1 && (cps < 8 * CFGS[c].WK || ceil_div(L.kchunks, cps) < ks)) break;
-                float us = float(ceil_div(mt * nb * ks, 256)) * (float(cps) * CHUNK_US[c] + TILE_US);
+                const int64_t cps = ceil_div(ceil_div(L.kchunks, ks), CFGS[cfg].WK) * CFGS[cfg].WK;
+                if (ks > 1 && (rows || cps < 8 * CFGS[cfg].WK || ceil_div(L.kchunks, cps) < ks)) break;
+                float us = float(ceil_div(mt * nb * ks, 256)) * (float(rows ? L.kchunks : cps) * CHUNK_US[cfg] + TILE_US);
                 if (ks > 1) us += JOIN_US + float(ks) * float(M) * float(L.ntiles) * TILE_N * 8.0f / JOIN_BYTES_PER_US;
-                if ((c == FIRST_TILE && ks == 1) || us < best) {
+                if (best == 0.0f || us < best) {
                     best = us;
-                    p.cfg = c;
+                    p.cfg = cfg;
                     p.ks = ks;
                     p.cps = int(cps);
                 }

@@ -333,30 +333,41 @@ _FLOATS = (torch.bfloat16, torch.float32)
 
 
 def _norm_args(residual, y, post_weight, pre_weight, gate, eps):
-    """Checked arguments of both directions: (rows, C, gates, parameter dtype, contiguous tensors)."""
+    """Checked arguments of both directions: (rows, C, gates, parameter dtype)."""
     _tensor(residual, "residual", _FLOATS)
-    _need(residual.dim() >= 1 and residual.shape[-1] > 0, "residual must be [..., C]")
-    dev, C = residual.device, residual.shape[-1]
+    shape, dev = residual.shape, residual.device
+    if not shape or shape[-1] == 0:
+        _fail("residual must be [..., C]")
+    C = shape[-1]
     R = residual.numel() // C
     if y is not None:
         _tensor(y, "y", (torch.bfloat16,), dev)
-        _need(y.shape == residual.shape, "y must have the residual's shape")
-    else:
-        _need(post_weight is None and gate is None, "post_weight and gate need y")
-    params = [p for p in (post_weight, pre_weight, gate) if p is not None]
-    for p in params:
-        _tensor(p, "weights and gate", _FLOATS, dev)
-        _need(p.dtype == params[0].dtype, "weights and gate must have one dtype")
-    for p in (post_weight, pre_weight):
-        _need(p is None or tuple(p.shape) == (C,), "a norm weight must be [C]")
-    gates = 0
-    if gate is not None:
-        _need(gate.dim() in (1, 2) and gate.shape[-1] == C, "gate must be [C] or [B, C]")
-        gates = 1 if gate.dim() == 1 else gate.shape[0]
-        _need(gates > 0 and R % gates == 0, "the rows must divide evenly among the gates")
-    _need(eps > 0.0, "eps must be positive")
-    dt = _DTYPES[params[0].dtype] if params else 1
-    return R, C, gates, dt, [None if t is None else t.contiguous() for t in (residual, y, post_weight, pre_weight, gate)]
+        if y.shape != shape:
+            _fail("y must have the residual's shape")
+    elif post_weight is not None or gate is not None:
+        _fail("post_weight and gate need y")
+    dtype, gates = None, 0
+    for p in (post_weight, pre_weight, gate):
+        if p is None:
+            continue
+        _tensor(p, "weights and gate", _FLOATS if dtype is None else (dtype,), dev)
+        dtype = p.dtype
+        if p is gate:
+            gates = 1 if p.dim() == 1 else p.shape[0]
+            if p.dim() not in (1, 2) or p.shape[-1] != C:
+                _fail("gate must be [C] or [B, C]")
+            if gates == 0 or R % gates:
+                _fail("the rows must divide evenly among the gates")
+        elif p.dim() != 1 or p.shape[0] != C:
+            _fail("a norm weight must be [C]")
+    if not eps > 0.0:
+        _fail("eps must be positive")
+    return R, C, gates, 1 if dtype is None else _DTYPES[dtype]
+
+
+def _c(t):
+    """Contiguous, or None."""
+    return t if t is None or t.is_contiguous() else t.contiguous()
 
 
 def _p(t):
@@ -376,18 +387,19 @@ def block_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *, post_we
     gate [C], or [B, C] with one gate for each of B equal runs of rows.  x is bf16, or with
     int8=True the pair (codes int8 [..., C], scales float32 [...]) that linear_i8() and
     gated_i8() take.  residual_out may be the residual itself (in place)."""
-    R, C, gates, dt, (residual, y, post_weight, pre_weight, gate) = _norm_args(residual, y, post_weight, pre_weight,
-                                                                               gate, eps)
-    dev = residual.device
-    _need(not int8 or pre_weight is not None, "int8 output needs pre_weight")
-    r_out = _out(residual_out, residual.shape, residual.dtype, dev, "residual_out")
+    R, C, gates, dt = _norm_args(residual, y, post_weight, pre_weight, gate, eps)
+    shape, dev = residual.shape, residual.device
+    residual, y, post_weight, pre_weight, gate = _c(residual), _c(y), _c(post_weight), _c(pre_weight), _c(gate)
+    if int8 and pre_weight is None:
+        _fail("int8 output needs pre_weight")
+    r_out = _out(residual_out, shape, residual.dtype, dev, "residual_out")
     x = codes = scales = None
     if pre_weight is not None:
         if int8:
-            codes = torch.empty(residual.shape, dtype=torch.int8, device=dev)
-            scales = torch.empty(residual.shape[:-1], dtype=torch.float32, device=dev)
+            codes = torch.empty(shape, dtype=torch.int8, device=dev)
+            scales = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
         else:
-            x = torch.empty(residual.shape, dtype=torch.bfloat16, device=dev)
+            x = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     _call("qlinear_block_norm", dev, _p(residual), _DTYPES[residual.dtype], _p(y), _p(post_weight), _p(pre_weight),
           _p(gate), dt, gates, residual_scale, eps, R, C, _p(r_out), _p(x), _p(codes), _p(scales))
     return r_out, ((codes, scales) if int8 else x)
@@ -403,9 +415,10 @@ def block_norm_backward(dx: torch.Tensor | None, dresidual: torch.Tensor | None,
     the dequantised x); dresidual: gradient of r' from the rest of the network (its dtype), or
     None; residual_out and y as the forward pass returned and took them.  Parameter gradients
     are float32, None for parameters that are not given; their sums have a fixed order."""
-    R, C, gates, dt, (residual_out, y, post_weight, pre_weight, gate) = _norm_args(residual_out, y, post_weight,
-                                                                                   pre_weight, gate, eps)
+    R, C, gates, dt = _norm_args(residual_out, y, post_weight, pre_weight, gate, eps)
     dev = residual_out.device
+    residual_out, y, post_weight, pre_weight, gate = (_c(residual_out), _c(y), _c(post_weight), _c(pre_weight),
+                                                      _c(gate))
     _need((dx is not None) == (pre_weight is not None), "dx and pre_weight go together")
     if dx is not None:
         _tensor(dx, "dx", (torch.bfloat16,), dev)
