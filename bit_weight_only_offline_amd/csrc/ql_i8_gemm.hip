@@ -91,6 +91,82 @@ __device__ inline void emit(const I8Args &a, int m, int t, int at, F total) {
         emit_linear(a, m, a.xs[m], n, channels(a, t, at, n, count), total(t));
 }
 
+// Outputs of a wavefront's MT x NT tiles: tokens m_first + 16 i + c, channel tiles ct0 ... (c, g:
+// the lane's column and row group).  xs(i): the token's scale, ch(j): the channels of tile j.
+//
+// A lane holds four channels of a token, eight bytes of bf16.  Where rows allow it, sixteen
+// tokens of the wavefront's columns go through LDS (`mine`, out_bytes() of the wavefront's
+// own), so that the stores cover whole 16-byte pieces of contiguous runs of each row: 256 x
+// 256 tiles over 4096 inputs took 505 us for a 4096 x 32768 output so, 629 with eight-byte
+// stores, and a gated product that also stores [up | gate] 509 against 721.  STREAM: stores
+// that ask the caches to let go of the lines: the large tiles' outputs otherwise push out the
+// operands that the other workgroups read (468 against 409 us for 4096 x 32768 x 4096).
+template <int NT, bool GATED>
+constexpr int out_bytes() { return 16 * ((GATED ? NT / 2 : NT) * 32 + 16); }
+
+template <int MT, int NT, bool GATED, bool STREAM, typename X, typename C>
+__device__ inline void store_tiles(const I8Args &a, int m_first, int ct0, const i32x4 (&acc)[NT][MT], X xs, C ch,
+                                   uint8_t *mine, int lane) {
+    constexpr int CT = GATED ? NT / 2 : NT;                // channel tiles of the wavefront
+    constexpr int PIECES = 2 * CT, STRIDE = CT * 32 + 16, KINDS = GATED ? 3 : 1;
+    constexpr int ROWS = 64 / PIECES < 16 ? 64 / PIECES : 16;
+    const int g = lane >> 4, c = lane & 15;
+    if (!a.vec8 || a.out_f32) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int m = m_first + i * 16 + c;
+            if (m >= a.M) continue;
+#pragma unroll
+            for (int t = 0; t < CT; ++t) {
+                const int n = (ct0 + t) * TILE_N + 4 * g;
+                if constexpr (GATED) emit_gated(a, m, xs(i), n, ch(2 * t), ch(2 * t + 1), acc[2 * t][i], acc[2 * t + 1][i]);
+                else emit_linear(a, m, xs(i), n, ch(t), acc[t][i]);
+            }
+        }
+        return;
+    }
+    const int kinds = GATED && a.raw ? 3 : 1;
+    const int p_row = lane / PIECES, n_mine = ct0 * TILE_N + 8 * (lane % PIECES);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int mi = m_first + i * 16;
+        float v[CT][KINDS][4];
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+            if constexpr (GATED) {
+                scaled(ch(2 * t), xs(i), acc[2 * t][i], v[t][1]);
+                scaled(ch(2 * t + 1), xs(i), acc[2 * t + 1][i], v[t][2]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[t][0][r] = gate_act(v[t][2][r], a.act) * v[t][1][r];
+            } else {
+                scaled(ch(t), xs(i), acc[t][i], v[t][0]);
+            }
+        }
+        // one kind (h, up, gate) after another through the same bytes: a wavefront's LDS
+        // accesses keep their order
+#pragma unroll
+        for (int k = 0; k < KINDS; ++k) {
+            if (k >= kinds) continue;
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+                *reinterpret_cast<u32x2 *>(mine + c * STRIDE + t * 32 + g * 8) =
+                    u32x2{pack_bf16(v[t][k][0], v[t][k][1]), pack_bf16(v[t][k][2], v[t][k][3])};
+            uint16_t *const dst = k == 0 ? static_cast<uint16_t *>(a.out) : a.raw + (k == 1 ? 0 : a.N);
+            const int64_t ld = k == 0 ? a.N : 2 * int64_t(a.N);
+#pragma unroll
+            for (int r0 = 0; r0 < 16; r0 += ROWS) {
+                const int row = r0 + p_row, m = mi + row;
+                const u32x4 piece = *reinterpret_cast<const u32x4 *>(mine + (row & 15) * STRIDE + (lane % PIECES) * 16);
+                if (p_row < ROWS && m < a.M && n_mine < a.N) {
+                    u32x4 *const to = reinterpret_cast<u32x4 *>(dst + int64_t(m) * ld + n_mine);
+                    if constexpr (STREAM) __builtin_nontemporal_store(piece, to);
+                    else *to = piece;
+                }
+            }
+        }
+    }
+}
+
 // ---- few rows: the weight streams through registers ----------------------------------
 // One workgroup owns NT column tiles over the whole input dimension.  Its WK wavefronts
 // take the chunks in turn (chunk i goes to wavefront i mod WK), so together they read one
@@ -356,7 +432,6 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) i8_tile_kernel(I8Args a) {
         return;
     }
     // All scales and biases first: behind the first stores their loads could not be shared.
-    constexpr int CT = GATED ? NT / 2 : NT;                // channel tiles of the wavefront
     const int ct0 = GATED ? (nt0 + wn * NT) / 2 : nt0 + wn * NT;
     float xs[MT];
     Channels q[NT];
@@ -371,67 +446,188 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) i8_tile_kernel(I8Args a) {
         q[j] = Channels{};
         if (n < a.N) q[j] = channels(a, nt0 + wn * NT + j, 4 * g, (GATED && (j & 1) ? int64_t(a.N) : 0) + n, a.N - n);
     }
-    // A lane holds four channels of a token, eight bytes of bf16.  Sixteen tokens of the
-    // wavefront's columns go through LDS (its own part of the ring), so that
-    // the stores cover whole 16-byte pieces of contiguous runs of each row: 256 x 256 bf16
-    // tiles over 4096 inputs took 505 us a 4096 x 32768 output so, 629 with eight-byte stores,
-    // and a gated product that also stores [up | gate] 509 against 721.
-    if (a.vec8 && !a.out_f32) {
-        constexpr int PIECES = 2 * CT, STRIDE = CT * 32 + 16, KINDS = GATED ? 3 : 1;
-        constexpr int ROWS = 64 / PIECES < 16 ? 64 / PIECES : 16;
-        // behind the sums of the other groups, which may still be read
-        constexpr int SUMS = (WK - 1) * XA * XB * 1024;
-        static_assert(SUMS + WM * WN * KINDS * 16 * STRIDE <= S * STAGE, "output rows fit the ring");
-        uint8_t *const mine = lds + SUMS + wv * (KINDS * 16 * STRIDE);
-        const int kinds = GATED && a.raw ? 3 : 1;
-        const int p_row = lane / PIECES, n_mine = ct0 * TILE_N + 8 * (lane % PIECES);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int mi = m0 + (wm * MT + i) * 16;
-#pragma unroll
-            for (int t = 0; t < CT; ++t) {
-                float v[KINDS][4];
-                if constexpr (GATED) {
-                    scaled(q[2 * t], xs[i], acc[2 * t][i], v[1]);
-                    scaled(q[2 * t + 1], xs[i], acc[2 * t + 1][i], v[2]);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) v[0][r] = gate_act(v[2][r], a.act) * v[1][r];
-                } else {
-                    scaled(q[t], xs[i], acc[t][i], v[0]);
-                }
-#pragma unroll
-                for (int k = 0; k < KINDS; ++k)
-                    if (k < kinds)
-                        *reinterpret_cast<u32x2 *>(mine + k * 16 * STRIDE + c * STRIDE + t * 32 + g * 8) =
-                            u32x2{pack_bf16(v[k][0], v[k][1]), pack_bf16(v[k][2], v[k][3])};
-            }
-#pragma unroll
-            for (int k = 0; k < KINDS; ++k) {
-                if (k >= kinds) continue;
-                uint16_t *const dst = k == 0 ? static_cast<uint16_t *>(a.out) : a.raw + (k == 1 ? 0 : a.N);
-                const int64_t ld = k == 0 ? a.N : 2 * int64_t(a.N);
-#pragma unroll
-                for (int r0 = 0; r0 < 16; r0 += ROWS) {
-                    const int row = r0 + p_row, m = mi + row;
-                    const u32x4 piece =
-                        *reinterpret_cast<const u32x4 *>(mine + k * 16 * STRIDE + (row & 15) * STRIDE + (lane % PIECES) * 16);
-                    if (p_row < ROWS && m < a.M && n_mine < a.N)
-                        *reinterpret_cast<u32x4 *>(dst + int64_t(m) * ld + n_mine) = piece;
-                }
-            }
+    constexpr int SUMS = (WK - 1) * XA * XB * 1024;        // sums of the other groups may still be read
+    static_assert(SUMS + WM * WN * out_bytes<NT, GATED>() <= S * STAGE, "output rows fit the ring");
+    store_tiles<MT, NT, GATED, false>(a, m0 + wm * MT * 16, ct0, acc, [&](int i) { return xs[i]; }, [&](int j) { return q[j]; },
+                               lds + SUMS + wv * out_bytes<NT, GATED>(), lane);
+}
+
+// ---- large tiles ----------------------------------------------------------------------
+// Eight wavefronts, each 16 MT tokens x NT column tiles; a workgroup stays on its compute unit
+// and walks the tiles (item i, then i + the number of workgroups), so that the loads of the
+// next tile's first stages are under way while this tile's outputs are scaled and stored.
+//
+// A stage is two chunks: 128-byte runs of the activation rows (whole cache lines; a XOR
+// swizzle of their 16-byte pieces spreads the 16 rows of an operand read over all banks) and
+// two weight tiles of each column tile.  Two stages, one barrier each, in the middle: by then
+// every wavefront has read the stage's second half into registers and the next stage has
+// arrived, so the loads of the one after go to this stage's place.  Operands are read half a
+// stage ahead between the matrix instructions.  At 256 x 256 x 4096 a workgroup, stages of one
+// chunk in a ring of five took 54.4 us a tile (64-byte runs), these 52.7.  What bounds the
+// loop is power more than any unit: with all codes zero the same instructions take 43 us.
+template <int WM, int WN, int MT, int NT>
+constexpr int wide_stage() { return 2 * (MT * WM + NT * WN) * 1024; }
+template <int WM, int WN, int MT, int NT, bool GATED>
+constexpr int wide_lds() { return 2 * wide_stage<WM, WN, MT, NT>() + (16 * MT * WM + 2 * 16 * NT * WN) * 4 + WM * WN * out_bytes<NT, GATED>(); }
+
+template <int WM, int WN, int MT, int NT, bool GATED>
+__global__ void __launch_bounds__(64 * WM * WN) i8_wide_kernel(I8Args a) {
+    static_assert(!GATED || NT % 2 == 0, "up and gate tiles go together");
+    constexpr int W = WM * WN, T = 64 * W;
+    constexpr int MP = 16 * MT * WM, NTT = NT * WN, NP = 16 * NTT;
+    constexpr int XA = MP / 8, XB = 2 * NTT;               // 1 KiB loads a stage
+    static_assert(XA % W == 0 && XB % W == 0 && W % 2 == 0, "every wavefront issues the same loads");
+    constexpr int XAW = XA / W, LOADS = XAW + XB / W;
+    constexpr int STAGE = wide_stage<WM, WN, MT, NT>();
+    static_assert(wide_lds<WM, WN, MT, NT, GATED>() <= LDS_BYTES_MAX && MP <= T && NP <= T, "fits");
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    float *const l_xs = reinterpret_cast<float *>(lds + 2 * STAGE), *const l_s = l_xs + MP, *const l_b = l_s + NP;
+    uint8_t *const l_out = reinterpret_cast<uint8_t *>(l_b + NP);
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wv / WN, wn = wv % WN;
+    const int g = lane >> 4, c = lane & 15;
+
+    // Offsets inside a tile of this wavefront's first loads of rows and of weights; the others
+    // are a fixed distance on.  Rows and column tiles past the end lie past the buffers' ranges.
+    const int row = wv * 8 + lane / 8, my_chunk = wv & 1;
+    const uint32_t x_off = uint32_t(row) * uint32_t(a.K) + 16u * uint32_t((lane % 8) ^ ((row >> 1) & 7));
+    const uint32_t w_off = (uint32_t(wv >> 1) * uint32_t(a.kchunks) + uint32_t(my_chunk)) * TILE_BYTES + 16u * lane;
+    const uint32_t x_far = uint32_t(W * 8) * uint32_t(a.K), w_far = uint32_t(W / 2) * uint32_t(a.kchunks) * TILE_BYTES;
+
+    struct Item {
+        __amdgpu_buffer_rsrc_t xr, wr;
+        int m0, nt0;
+    };
+    // Items in the order of bands of eight row blocks; workgroup b runs on XCD b mod 8 and each
+    // XCD takes one contiguous run, so that what it runs together shares rows and columns.
+    const int items = a.mtiles * a.nblocks;
+    const int xcd = blockIdx.x & 7, q8 = items >> 3, r8 = items & 7;
+    const int run = q8 + (xcd < r8 ? 1 : 0), first = xcd * q8 + min(xcd, r8);
+    const int per_xcd = (int(gridDim.x) + 7 - xcd) >> 3;   // workgroups on this XCD
+    auto open = [&](int at) {
+        Item it;
+        const bool real = at < run;
+        const int tile = real ? first + at : 0;
+        const int band = tile / (8 * a.nblocks), in_band = tile - band * 8 * a.nblocks;
+        const int band_rows = min(8, a.mtiles - 8 * band);
+        it.m0 = (8 * band + in_band % band_rows) * MP;
+        it.nt0 = in_band / band_rows * NTT;
+        it.xr = make_rsrc(a.x + int64_t(it.m0) * a.K, real ? uint32_t(min(MP, a.M - it.m0)) * uint32_t(a.K) : 0u);
+        it.wr = make_rsrc(a.w + int64_t(it.nt0) * a.kchunks * TILE_BYTES,
+                          real ? uint32_t(min(NTT, a.ntiles - it.nt0)) * uint32_t(a.kchunks) * TILE_BYTES : 0u);
+        return it;
+    };
+    auto issue = [&](int q, const Item &it, int st, int buf) {
+        uint8_t *const base = lds + buf * STAGE + (wv + W * (q < XAW ? q : q - XAW)) * 1024;
+        if (q < XAW) {
+            uint32_t far = uint32_t(q) * x_far + uint32_t(st) * (2 * I8_CHUNK);
+            asm("" : "+s"(far));           // one scalar: the sum with x_off is not worth a register
+            ld128_lds(it.xr, x_off + far, base);
+        } else {
+            // a chunk past the last reads as zero, and so adds nothing whatever its inputs
+            uint32_t far = uint32_t(q - XAW) * w_far + uint32_t(st) * (2 * TILE_BYTES);
+            if (2 * st + my_chunk >= a.kchunks) far = OUT_OF_RANGE;
+            asm("" : "+s"(far));
+            ld128_lds(it.wr, w_off + far, base + XA * 1024);
         }
-        return;
-    }
+    };
+    // the tile's token and channel scales, 64 a wavefront
+    auto issue_scales = [&](const Item &it) {
+        constexpr int XW = MP / 64, SW = NP / 64;
+        static_assert(MP % 64 == 0 && NP % 64 == 0 && XW + SW <= W, "one load a wavefront");
+        if (wv < XW)
+            ld32_lds(make_rsrc(a.xs + it.m0, uint32_t(min(MP, a.M - it.m0)) * 4u), uint32_t(wv * 64 + lane) * 4u,
+                     reinterpret_cast<uint8_t *>(l_xs) + wv * 256);
+        else if (wv < XW + SW)
+            ld32_lds(make_rsrc(a.s + int64_t(it.nt0) * TILE_N, uint32_t(min(NTT, a.ntiles - it.nt0)) * TILE_N * 4u),
+                     uint32_t((wv - XW) * 64 + lane) * 4u, reinterpret_cast<uint8_t *>(l_s) + (wv - XW) * 256);
+    };
+
+    struct Operands {
+        u32x4 x[MT], w[NT];
+    };
+    constexpr int READS = MT + NT;
+    const uint8_t *const x_at = lds + (wm * MT * 16 + c) * 128, *const w_at = lds + (XA + 2 * wn * NT) * 1024 + lane * 16;
+    const int x_half[2] = {(g ^ (c >> 1)) * 16, ((4 + g) ^ (c >> 1)) * 16};
+    auto read = [&](Operands &f, int buf, int h, int r) {
+        if (r < MT) f.x[r] = *reinterpret_cast<const u32x4 *>(x_at + buf * STAGE + x_half[h] + r * 2048);
+        else f.w[r - MT] = *reinterpret_cast<const u32x4 *>(w_at + buf * STAGE + (r - MT) * 2048 + h * 1024);
+    };
+    i32x4 acc[NT][MT];
+    // half a stage: its operands f; reads of half h of buffer `from`; loads of stage st of `it`
+    auto multiply = [&](const Operands &f, Operands &next, int from, int h, bool fill, const Item &it, int st, int to) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int m = m0 + (wm * MT + i) * 16 + c;
-        if (m >= a.M) continue;
+        for (int j = 0; j < NT; ++j) {
 #pragma unroll
-        for (int t = 0; t < CT; ++t) {
-            const int n = (ct0 + t) * TILE_N + 4 * g;
-            if constexpr (GATED) emit_gated(a, m, xs[i], n, q[2 * t], q[2 * t + 1], acc[2 * t][i], acc[2 * t + 1][i]);
-            else emit_linear(a, m, xs[i], n, q[t], acc[t][i]);
+            for (int i = 0; i < MT; ++i) acc[j][i] = mma(f.w[j], f.x[i], acc[j][i]);
+#pragma unroll
+            for (int r = j * READS / (NT - 1); r < (j + 1) * READS / (NT - 1) && r < READS; ++r) read(next, from, h, r);
+            if (fill)
+#pragma unroll
+                for (int q = j * LOADS / NT; q < (j + 1) * LOADS / NT; ++q) issue(q, it, st, to);
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+
+    int at = int(blockIdx.x) >> 3;
+    if (at >= run) return;
+    Item cur = open(at);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int q = 0; q < LOADS; ++q) issue(q, cur, u, u);
+    wait_vmcnt<0>();
+    ring_barrier();
+    Operands f0, f1;
+    int buf = 0;
+    while (true) {
+        const Item next = open(at + per_xcd);
+        // at least two stages, so that the next tile's first two are loaded by this one's last
+        const int stages = max(2, (a.kchunks + 1) / 2);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < READS; ++r) read(f0, buf, 0, r);
+        for (int st = 0; st < stages; ++st) {
+            multiply(f0, f1, buf, 1, false, cur, 0, 0);
+            // a tile's first two stages had arrived before the last tile's stores, which
+            // need not be waited for here
+            if (st > 0) wait_vmcnt<0>();
+            ring_barrier();
+            const bool wrap = st + 2 >= stages;
+            const Item &from = wrap ? next : cur;
+            multiply(f1, f0, buf ^ 1, 0, true, from, wrap ? st + 2 - stages : st + 2, buf);
+            if (st == 0) issue_scales(cur);      // every wavefront is past the last tile's stores
+            buf ^= 1;
+        }
+        if (a.bias && tid < NP) {
+            const int tile = cur.nt0 + tid / TILE_N, n = (GATED ? tile >> 1 : tile) * TILE_N + tid % TILE_N;
+            l_b[tid] = n < a.N ? bf16_bits_to_f32(a.bias[(GATED && (tile & 1) ? int64_t(a.N) : 0) + n]) : 0.0f;
+        }
+        wait_vmcnt<0>();                                   // the next tile's first two stages
+        ring_barrier();
+
+        // The lane number by way of an empty statement that may change it: addresses of the
+        // outputs are then formed here, and do not sit in registers through the loop above.
+        int out_lane = lane;
+        asm volatile("" : "+v"(out_lane));
+        const int g = out_lane >> 4, c = out_lane & 15;
+        const int ct0 = GATED ? (cur.nt0 + wn * NT) / 2 : cur.nt0 + wn * NT;
+        store_tiles<MT, NT, GATED, true>(
+            a, cur.m0 + wm * MT * 16, ct0, acc, [&](int i) { return l_xs[(wm * MT + i) * 16 + c]; },
+            [&](int j) {
+                const int at4 = (wn * NT + j) * TILE_N + 4 * g;
+                return Channels{*reinterpret_cast<const f32x4 *>(l_s + at4),
+                                a.bias ? *reinterpret_cast<const f32x4 *>(l_b + at4) : f32x4{0.f, 0.f, 0.f, 0.f}};
+            },
+            l_out + wv * out_bytes<NT, GATED>(), out_lane);
+        at += per_xcd;
+        if (at >= run) break;
+        cur = next;
     }
 }
 
@@ -454,7 +650,7 @@ __global__ void __launch_bounds__(256) i8_join_kernel(I8Args a) {
 constexpr I8Cfg CFGS[] = {
     {0, 1, 1, 8, 1, 1, 0}, {0, 1, 2, 8, 1, 1, 0},      // up to 16 rows, one or two column tiles
     {0, 2, 1, 8, 1, 1, 0}, {0, 2, 2, 8, 1, 1, 0},      // 32 rows
-    {1, 8, 4, 1, 2, 4, 5},      // 256 x 256
+    {2, 8, 4, 1, 2, 4, 2},      // 256 x 256
     {1, 4, 4, 1, 2, 4, 5},      // 128 x 256
     {1, 4, 2, 1, 2, 4, 5},      // 128 x 128
     {1, 2, 2, 1, 2, 4, 6},      // 64 x 128
@@ -468,6 +664,7 @@ constexpr int NUM_CFGS = 9, FIRST_TILE = 4;
 constexpr float CHUNK_US[NUM_CFGS] = {0, 0, 0.036f, 0.064f, 0.75f, 0.43f, 0.28f, 0.15f, 0.09f};
 constexpr float TILE_US = 4.0f, JOIN_US = 5.0f, JOIN_BYTES_PER_US = 4.0e6f;
 constexpr int ROWS_U = 4;
+constexpr int WIDE_WGS = 256;    // workgroups that walk the large tiles: one a compute unit
 
 template <typename F>
 hipError_t allow_lds(F kern, size_t lds) {
@@ -485,28 +682,45 @@ hipError_t launch_rows(const I8Args &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <int I, bool GATED>
-hipError_t launch_tiles(const I8Args &a, hipStream_t st) {
-    constexpr I8Cfg t = CFGS[I];
-    constexpr size_t lds = size_t(t.S) * t.WK * (t.MT * t.WM + t.NT * t.WN) * TILE_BYTES;
-    const dim3 grid(unsigned(a.mtiles * a.nblocks), unsigned(a.ks));
-    const dim3 block(64 * t.WM * t.WN * t.WK);
-    if (a.ks == 1) {
-        auto kern = i8_tile_kernel<t.WM, t.WN, t.WK, t.MT, t.NT, t.S, GATED, false>;
-        static const hipError_t set = allow_lds(kern, lds);
-        if (set != hipSuccess) return set;
-        hipLaunchKernelGGL(kern, grid, block, lds, st, a);
-        return hipGetLastError();
-    }
-    auto kern = i8_tile_kernel<t.WM, t.WN, t.WK, t.MT, t.NT, t.S, GATED, true>;
-    static const hipError_t set = allow_lds(kern, lds);
-    if (set != hipSuccess) return set;
-    hipLaunchKernelGGL(kern, grid, block, lds, st, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+template <bool GATED>
+hipError_t launch_join(const I8Args &a, hipStream_t st) {
     const int64_t units = int64_t(a.M) * (GATED ? a.ntiles / 2 : a.ntiles) * 4;
     hipLaunchKernelGGL(i8_join_kernel<GATED>, dim3(unsigned(ceil_div(units, 256))), dim3(256), 0, st, a);
     return hipGetLastError();
+}
+
+// 256 x 256 either way.  Gated wavefronts take twice the columns and half the rows, so that
+// each of h, up and gate leaves in 128-byte lines.
+template <int I, bool GATED>
+hipError_t launch_wide(const I8Args &a, hipStream_t st) {
+    constexpr I8Cfg t = CFGS[I];
+    constexpr int WM = GATED ? 2 * t.WM : t.WM, WN = GATED ? t.WN / 2 : t.WN;
+    constexpr int MT = GATED ? t.MT / 2 : t.MT, NT = GATED ? 2 * t.NT : t.NT;
+    constexpr size_t lds = wide_lds<WM, WN, MT, NT, GATED>();
+    auto kern = i8_wide_kernel<WM, WN, MT, NT, GATED>;
+    static const hipError_t set = allow_lds(kern, lds);
+    if (set != hipSuccess) return set;
+    hipLaunchKernelGGL(kern, dim3(unsigned(std::min<int64_t>(int64_t(a.mtiles) * a.nblocks, WIDE_WGS))),
+                       dim3(64 * WM * WN), lds, st, a);
+    return hipGetLastError();
+}
+
+template <int I, bool GATED, bool SPLIT>
+hipError_t launch_tiles_of(const I8Args &a, hipStream_t st) {
+    constexpr I8Cfg t = CFGS[I];
+    constexpr size_t lds = size_t(t.S) * t.WK * (t.MT * t.WM + t.NT * t.WN) * TILE_BYTES;
+    auto kern = i8_tile_kernel<t.WM, t.WN, t.WK, t.MT, t.NT, t.S, GATED, SPLIT>;
+    static const hipError_t set = allow_lds(kern, lds);
+    if (set != hipSuccess) return set;
+    hipLaunchKernelGGL(kern, dim3(unsigned(a.mtiles * a.nblocks), unsigned(a.ks)), dim3(64 * t.WM * t.WN * t.WK), lds, st, a);
+    return hipGetLastError();
+}
+
+template <int I, bool GATED>
+hipError_t launch_tiles(const I8Args &a, hipStream_t st) {
+    if (a.ks == 1) return launch_tiles_of<I, GATED, false>(a, st);
+    const hipError_t e = launch_tiles_of<I, GATED, true>(a, st);
+    return e != hipSuccess ? e : launch_join<GATED>(a, st);
 }
 
 template <bool GATED>
@@ -517,7 +731,7 @@ hipError_t launch_any(int cfg, const I8Args &a, hipStream_t st) {
         case 2: if constexpr (GATED) return hipErrorInvalidValue; else return launch_rows<2, false>(a, st);
         case 1: return launch_rows<1, GATED>(a, st);
         case 3: if constexpr (GATED) return launch_rows<3, true>(a, st); else return hipErrorInvalidValue;
-        case 4: return launch_tiles<4, GATED>(a, st);
+        case 4: return launch_wide<4, GATED>(a, st);
         case 5: return launch_tiles<5, GATED>(a, st);
         case 6: return launch_tiles<6, GATED>(a, st);
         case 7: return launch_tiles<7, GATED>(a, st);
@@ -555,7 +769,7 @@ I8Plan make_i8_plan(const I8Layout &L, int64_t M) {
             blocks(cfg, mt, nb);
             for (int ks : {1, 2, 3, 4, 6, 8}) {
                 const int64_t cps = ceil_div(ceil_div(L.kchunks, ks), CFGS[cfg].WK) * CFGS[cfg].WK;
-                if (ks > 1 && (rows || cps < 8 * CFGS[cfg].WK || ceil_div(L.kchunks, cps) < ks)) break;
+                if (ks > 1 && (CFGS[cfg].kind != 1 || cps < 8 * CFGS[cfg].WK || ceil_div(L.kchunks, cps) < ks)) break;
                 float us = float(ceil_div(mt * nb * ks, 256)) * (float(rows ? L.kchunks : cps) * CHUNK_US[cfg] + TILE_US);
                 if (ks > 1) us += JOIN_US + float(ks) * float(M) * float(L.ntiles) * TILE_N * 8.0f / JOIN_BYTES_PER_US;
                 if (best == 0.0f || us < best) {

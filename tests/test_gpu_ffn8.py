@@ -91,7 +91,8 @@ def test_linear_matches(M, N, K):
         assert torch.equal(y16, y32.bfloat16())
 
 
-@pytest.mark.parametrize("M,N,K", [(3000, 1000, 544), (1100, 4100, 96), (520, 8200, 64)])
+@pytest.mark.parametrize("M,N,K", [(3000, 1000, 544), (1100, 4100, 96), (520, 8200, 64), (4200, 4300, 160),
+                                   (5000, 4200, 32), (1030, 5001, 4128), (600, 520, 20000)])
 def test_linear_large_tiles(M, N, K):
     Q = _Q()
     x, xs, w, ws, b = _linear_case(M, N, K, 11)
@@ -293,7 +294,7 @@ def test_gated_matches(M, N, K, act):
         assert torch.equal(h16, h32.bfloat16())
 
 
-@pytest.mark.parametrize("M,N,K", [(1500, 1000, 96), (600, 4104, 160)])
+@pytest.mark.parametrize("M,N,K", [(1500, 1000, 96), (600, 4104, 160), (2100, 4200, 224), (4400, 2101, 64), (520, 264, 20000)])
 def test_gated_large_tiles(M, N, K):
     Q = _Q()
     case = _gated_case(M, N, K, 3, True)
