@@ -31,35 +31,37 @@ constexpr int NSTEP = 32;                        // weight rows (contraction) pe
 constexpr int BACK_KP = 256, BACK_KQ = 4;        // inputs per workgroup, and chunks of them
 constexpr int BACK_WAVES = 8;
 
-// An LDS store of 8 bytes.  Written as assembly text because the compiler, which cannot tell
-// the stages of the ring apart, would wait before every store for the buffer->LDS loads in
-// flight; the step's barrier waits for the stores (lgkmcnt), and nothing reads them sooner.
-__device__ inline void lds_store8(uint8_t *p, u32x2 v) {
+// An LDS store of 8 bytes at p, or 16 KiB on (a decoded step's second place).  Written as
+// assembly text because the compiler, which cannot tell the stages of the ring apart, would
+// wait before every store for the buffer->LDS loads in flight; the step's barrier waits for
+// the stores (lgkmcnt), and nothing reads them sooner.
+__device__ inline void lds_store8(uint8_t *p, bool second, u32x2 v) {
+    static_assert(BACK_KP * 64 == 16384, "the offset below");
     const uint32_t at = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)p));
-    asm volatile("ds_write_b64 %0, %1" : : "v"(at), "v"(v) : "memory");
+    if (second) asm volatile("ds_write_b64 %0, %1 offset:16384" : : "v"(at), "v"(v) : "memory");
+    else asm volatile("ds_write_b64 %0, %1" : : "v"(at), "v"(v) : "memory");
 }
 
-// LDS: dy rows [MP][32] bf16 and packed tiles [2][4] KiB, four stages each; the decoded
-// operand [16][1] KiB, two stages.
-constexpr int back_lds(int mp) { return 4 * (mp * 64 + 8 * 1024) + 2 * BACK_KP * 64; }
+// LDS: operand rows [MP][64] bf16 (two steps; 128-byte runs, whole cache lines), two stages;
+// packed tiles [2][4] KiB, four; the decoded operand [16][1] KiB, two.
+constexpr int back_lds(int mp) { return 2 * mp * 128 + 4 * 8 * 1024 + 2 * BACK_KP * 64; }
 
 // One workgroup: MP = 16 MT WM rows of dy by 256 inputs, the contraction in steps of 32
 // packed rows (two tiles).  While step s is multiplied out of registers, the operands of
 // step s + 1 are read into registers, each wavefront decodes one of the eight packed tiles
-// of step s + 2 (the one it loaded itself), and the buffer->LDS loads of dy for s + 4 and of
-// tiles for s + 5 are issued; one barrier a step.
+// of step s + 2 (the one it loaded itself), and the buffer->LDS loads of tiles for s + 5 and,
+// every other step, of the rows for s + 3 and s + 4 are issued; one barrier a step.
 template <int WM, int WN, int MT, int NT, bool SPLIT>
 __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) {
     static_assert(WM * WN == BACK_WAVES && 16 * NT * WN == BACK_KP, "eight wavefronts over 256 inputs");
     constexpr int MP = 16 * MT * WM;
-    constexpr int NA = MP / 16;                      // 1 KiB loads of dy a step
+    constexpr int NA = MP / 8;                       // 1 KiB loads of rows for two steps
     // fewer loads than wavefronts: some are issued twice (the same bytes to the same place),
     // so that all wavefronts wait for the same count
     constexpr int NAW = NA < BACK_WAVES ? 1 : NA / BACK_WAVES;
-    constexpr int PER_STEP = NAW + 1;
-    constexpr int A_BYTES = MP * 64, R_BYTES = 8 * 1024, D_BYTES = BACK_KP * 64;
+    constexpr int A_BYTES = MP * 128, R_BYTES = 8 * 1024, D_BYTES = BACK_KP * 64;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    uint8_t *const ldsA = lds, *const ldsR = ldsA + 4 * A_BYTES, *const ldsD = ldsR + 4 * R_BYTES;
+    uint8_t *const ldsA = lds, *const ldsR = ldsA + 2 * A_BYTES, *const ldsD = ldsR + 4 * R_BYTES;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -84,20 +86,18 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
     const __amdgpu_buffer_rsrc_t yr =
         make_rsrc(a.dy + int64_t(m0) * a.ldy, uint32_t(m_here) * uint32_t(a.ldy) * 2u);
 
-    // piece p (eight packed rows) of row r of dy sits at piece p ^ row_swizzle(r)
-
-    uint32_t y_off[NAW];
-    const int y_col = 8 * ((lane & 3) ^ row_swizzle(lane >> 2));
-#pragma unroll
-    for (int q = 0; q < NAW; ++q) {
-        const int row = ((wv + BACK_WAVES * q) % NA) * 16 + (lane >> 2);
-        y_off[q] = row < m_here ? (uint32_t(row) * uint32_t(a.ldy) + uint32_t(y_col)) * 2u : OUT_OF_RANGE;
-    }
-    // u: the stage's place in the ring, (st - st0) mod 4, a constant where it matters
+    // piece p (eight packed rows) of row r of a pair of steps sits at piece p ^ r / 2 mod 8
+    // (rows past the end lie past the buffer's range; load q is a fixed distance on from load 0)
+    const int y_col = 8 * ((lane & 7) ^ ((lane >> 4) | ((wv & 1) << 2)));
+    const uint32_t y_off = (uint32_t((wv % NA) * 8 + (lane >> 3)) * uint32_t(a.ldy) + uint32_t(y_col)) * 2u;
+    const uint32_t y_far = uint32_t(BACK_WAVES * 16) * uint32_t(a.ldy);
+    // u: the stage's place in the ring, (st - st0) mod 4, a constant where it matters; rows of
+    // steps st and st + 1, st - st0 even
     auto issue_y = [&](int q, int st, int u) {
-        const uint32_t past = st < st1 && st * NSTEP + y_col < a.ldy ? 0u : OUT_OF_RANGE;
-        ld128_lds(yr, (y_off[q] + uint32_t(st) * (NSTEP * 2)) | past,
-                  ldsA + (u & 3) * A_BYTES + ((wv + BACK_WAVES * q) % NA) * 1024);
+        const uint32_t past = st * NSTEP + y_col < a.ldy ? 0u : OUT_OF_RANGE;
+        uint32_t far = st < st1 ? uint32_t(q) * y_far + uint32_t(st) * (NSTEP * 2) : OUT_OF_RANGE;
+        asm("" : "+s"(far));           // one scalar: the sum with y_off is not worth a register
+        ld128_lds(yr, (y_off + far) | past, ldsA + ((u >> 1) & 1) * A_BYTES + ((wv + BACK_WAVES * q) % NA) * 1024);
     };
     // This wavefront's packed tile of a step: tile wv / 4, chunk wv mod 4.  Its 16-byte piece
     // s lands at slot s ^ s / 16: the words that the 64 lanes read together then lie in 64
@@ -133,12 +133,14 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
     // upper half as bf16.  Permutes and subtractions run at the full vector rate, conversion
     // instructions at a quarter of it: with them a step of 128 x 256 took 0.69 us, without
     // any decoding 0.37.
+    uint32_t magic = 0x4B000000u;
+    asm("" : "+v"(magic));             // in a vector register, which leaves the selectors scalar
     auto decode = [&](const Packed &p, int u, int b) {
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            v[i] = __uint_as_float(__builtin_amdgcn_perm(0x4B000000u, p.w[i], 0x07040400u | uint32_t(b))) - 8388736.0f;
-        lds_store8(store_at[b] + (u & 1) * D_BYTES,
+            v[i] = __uint_as_float(__builtin_amdgcn_perm(magic, p.w[i], 0x07040400u | uint32_t(b))) - 8388736.0f;
+        lds_store8(store_at[b], u & 1,
                    u32x2{__builtin_amdgcn_perm(__float_as_uint(v[1]), __float_as_uint(v[0]), 0x07060302u),
                          __builtin_amdgcn_perm(__float_as_uint(v[3]), __float_as_uint(v[2]), 0x07060302u)});
     };
@@ -151,19 +153,25 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
 
     // x[i] is free again after its group of matrix instructions, so only w needs two sets
     u32x4 x[MT], w0[NT], w1[NT];
-    const uint8_t *const x_at = ldsA + (wm * MT * 16 + c) * 64 + ((g ^ row_swizzle(c)) * 16);
+    const uint8_t *const x_at[2] = {ldsA + (wm * MT * 16 + c) * 128 + ((g ^ (c >> 1)) * 16),
+                                    ldsA + (wm * MT * 16 + c) * 128 + (((4 + g) ^ (c >> 1)) * 16)};
     const uint8_t *w_at[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
         const int kt = wn * NT + j;
         w_at[j] = ldsD + kt * 1024 + (g * 16 + (c ^ (kt & 3) ^ (2 * (g & 1)))) * 16;
     }
-    auto read_x = [&](int u, int i) { x[i] = *reinterpret_cast<const u32x4 *>(x_at + (u & 3) * A_BYTES + i * 1024); };
+    auto read_x = [&](int u, int i) {
+        x[i] = *reinterpret_cast<const u32x4 *>(x_at[u & 1] + ((u >> 1) & 1) * A_BYTES + i * 2048);
+    };
     auto read_w = [&](u32x4 (&w)[NT], int u, int j) {
         w[j] = *reinterpret_cast<const u32x4 *>(w_at[j] + (u & 1) * D_BYTES);
     };
     auto step = [&](int st, int u, const u32x4 (&w)[NT], u32x4 (&next)[NT]) {
-        wait_vmcnt<2 * PER_STEP>();
+        // Arrived by now: tiles of st + 2, and before an odd step the rows of st + 1.  Issued
+        // since: tiles of st + 3 and st + 4, and in an odd step before its tiles the rows.
+        if (u & 1) wait_vmcnt<2>();
+        else wait_vmcnt<NAW + 2>();
         ring_barrier();
         Packed p;
         fetch(p, u + 2);
@@ -182,23 +190,22 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
             if (i >= D0 && i < D1)
 #pragma unroll
                 for (int b = (i - D0) * 4 / (D1 - D0); b < (i - D0 + 1) * 4 / (D1 - D0); ++b) decode(p, u + 2, b);
-            if (i == 0)
+            // rows of the pair of steps behind the next one, to the place of the last one
+            if (u & 1)
 #pragma unroll
-                for (int q = 0; q < NAW; ++q) issue_y(q, st + 4, u + 4);
-            if (i == (MT > 1 ? 1 : 0)) issue_w(st + 5, u + 5);
+                for (int q = i * NAW / MT; q < (i + 1) * NAW / MT; ++q) issue_y(q, st + 3, u + 3);
+            if (i == MT - 1) issue_w(st + 5, u + 5);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
 
     if (st0 < st1) {
-        // loads in the order of the steps: dy of s + 4 and tiles of s + 5 together
-        issue_w(st0, 0);
-        issue_w(st0 + 1, 1);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
+            issue_w(st0 + u, u);
+            if (u % 2 == 0)
 #pragma unroll
-            for (int q = 0; q < NAW; ++q) issue_y(q, st0 + u, u);
-            if (u < 2) issue_w(st0 + 2 + u, 2 + u);
+                for (int q = 0; q < NAW; ++q) issue_y(q, st0 + u, u);
         }
         wait_vmcnt<0>();
         ring_barrier();
