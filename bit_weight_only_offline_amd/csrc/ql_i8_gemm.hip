@@ -101,45 +101,60 @@ __device__ inline void emit(const I8Args &a, int m, int t, int at, F total) {
 // stores, and a gated product that also stores [up | gate] 509 against 721.  STREAM: stores
 // that ask the caches to let go of the lines: the large tiles' outputs otherwise push out the
 // operands that the other workgroups read (468 against 409 us for 4096 x 32768 x 4096).
+// Rows that no vector store fits (channel counts off eight, or off four for float32) go
+// through LDS too and leave element by element, neighbouring lanes to neighbouring addresses:
+// 28.9 us for 3000 x 5001 x 1024, 40.7 with each lane storing its own four channels.
 template <int NT, bool GATED>
-constexpr int out_bytes() { return 16 * ((GATED ? NT / 2 : NT) * 32 + 16); }
+constexpr int out_stride() { return (GATED ? (NT > 4 ? NT / 2 : 2) : NT) * 32 + 16; }
+template <int NT, bool GATED>
+constexpr int out_bytes() { return 16 * out_stride<NT, GATED>(); }
+
+// Sixteen tokens (from m) by T channel tiles (from channel n) as elements of type E.
+template <typename E, int T>
+__device__ inline void store_elements(const I8Args &a, E *dst, int64_t ld, int m, int n, const float (*v)[4],
+                                      uint8_t *mine, int stride, int lane) {
+    const int g = lane >> 4, c = lane & 15;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        if constexpr (sizeof(E) == 4)
+            *reinterpret_cast<f32x4 *>(mine + c * stride + t * 64 + g * 16) = f32x4{v[t][0], v[t][1], v[t][2], v[t][3]};
+        else
+            *reinterpret_cast<u32x2 *>(mine + c * stride + t * 32 + g * 8) =
+                u32x2{pack_bf16(v[t][0], v[t][1]), pack_bf16(v[t][2], v[t][3])};
+    }
+    constexpr int LINE = 16 * T, STEP = 64 / LINE > 0 ? 64 / LINE : 1;     // elements a row, rows a step
+    static_assert(LINE <= 64, "a row at most a wavefront");
+    const int row0 = lane / LINE, col = lane % LINE;
+    const uint8_t *from = mine + row0 * stride + col * sizeof(E);
+    E *to = dst + int64_t(m + row0) * ld + n + col;
+#pragma unroll 1
+    for (int row = row0; row < 16; row += STEP, from += STEP * stride, to += STEP * ld)
+        if (m + row < a.M && n + col < a.N) *to = *reinterpret_cast<const E *>(from);
+}
 
 template <int MT, int NT, bool GATED, bool STREAM, typename X, typename C>
 __device__ inline void store_tiles(const I8Args &a, int m_first, int ct0, const i32x4 (&acc)[NT][MT], X xs, C ch,
                                    uint8_t *mine, int lane) {
     constexpr int CT = GATED ? NT / 2 : NT;                // channel tiles of the wavefront
-    constexpr int PIECES = 2 * CT, STRIDE = CT * 32 + 16, KINDS = GATED ? 3 : 1;
+    constexpr int PIECES = 2 * CT, STRIDE = out_stride<NT, GATED>(), KINDS = GATED ? 3 : 1;
     constexpr int ROWS = 64 / PIECES < 16 ? 64 / PIECES : 16;
+    constexpr int HALF = CT > 1 ? CT / 2 : 1;              // float32 tiles that fit at a time
     const int g = lane >> 4, c = lane & 15;
-    if (!a.vec8 || a.out_f32) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int m = m_first + i * 16 + c;
-            if (m >= a.M) continue;
-#pragma unroll
-            for (int t = 0; t < CT; ++t) {
-                const int n = (ct0 + t) * TILE_N + 4 * g;
-                if constexpr (GATED) emit_gated(a, m, xs(i), n, ch(2 * t), ch(2 * t + 1), acc[2 * t][i], acc[2 * t + 1][i]);
-                else emit_linear(a, m, xs(i), n, ch(t), acc[t][i]);
-            }
-        }
-        return;
-    }
     const int kinds = GATED && a.raw ? 3 : 1;
     const int p_row = lane / PIECES, n_mine = ct0 * TILE_N + 8 * (lane % PIECES);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         const int mi = m_first + i * 16;
-        float v[CT][KINDS][4];
+        float v[KINDS][CT][4];
 #pragma unroll
         for (int t = 0; t < CT; ++t) {
             if constexpr (GATED) {
-                scaled(ch(2 * t), xs(i), acc[2 * t][i], v[t][1]);
-                scaled(ch(2 * t + 1), xs(i), acc[2 * t + 1][i], v[t][2]);
+                scaled(ch(2 * t), xs(i), acc[2 * t][i], v[1][t]);
+                scaled(ch(2 * t + 1), xs(i), acc[2 * t + 1][i], v[2][t]);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v[t][0][r] = gate_act(v[t][2][r], a.act) * v[t][1][r];
+                for (int r = 0; r < 4; ++r) v[0][t][r] = gate_act(v[2][t][r], a.act) * v[1][t][r];
             } else {
-                scaled(ch(t), xs(i), acc[t][i], v[t][0]);
+                scaled(ch(t), xs(i), acc[t][i], v[0][t]);
             }
         }
         // one kind (h, up, gate) after another through the same bytes: a wavefront's LDS
@@ -147,12 +162,31 @@ __device__ inline void store_tiles(const I8Args &a, int m_first, int ct0, const 
 #pragma unroll
         for (int k = 0; k < KINDS; ++k) {
             if (k >= kinds) continue;
+            const int64_t ld = k == 0 ? a.N : 2 * int64_t(a.N);
+            if (k == 0 && a.out_f32) {
+                float *const out = static_cast<float *>(a.out);
+                if (a.vec) {
+#pragma unroll
+                    for (int t = 0; t < CT; ++t) {
+                        const int n = (ct0 + t) * TILE_N + 4 * g;
+                        if (mi + c < a.M && n < a.N) store4_f32(out, int64_t(mi + c) * ld + n, v[0][t], 4, true);
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < CT; t += HALF)
+                        store_elements<float, HALF>(a, out, ld, mi, (ct0 + t) * TILE_N, v[0] + t, mine, STRIDE, lane);
+                }
+                continue;
+            }
+            uint16_t *const dst = k == 0 ? static_cast<uint16_t *>(a.out) : a.raw + (k == 1 ? 0 : a.N);
+            if (!a.vec8) {
+                store_elements<uint16_t, CT>(a, dst, ld, mi, ct0 * TILE_N, v[k], mine, STRIDE, lane);
+                continue;
+            }
 #pragma unroll
             for (int t = 0; t < CT; ++t)
                 *reinterpret_cast<u32x2 *>(mine + c * STRIDE + t * 32 + g * 8) =
-                    u32x2{pack_bf16(v[t][k][0], v[t][k][1]), pack_bf16(v[t][k][2], v[t][k][3])};
-            uint16_t *const dst = k == 0 ? static_cast<uint16_t *>(a.out) : a.raw + (k == 1 ? 0 : a.N);
-            const int64_t ld = k == 0 ? a.N : 2 * int64_t(a.N);
+                    u32x2{pack_bf16(v[k][t][0], v[k][t][1]), pack_bf16(v[k][t][2], v[k][t][3])};
 #pragma unroll
             for (int r0 = 0; r0 < 16; r0 += ROWS) {
                 const int row = r0 + p_row, m = mi + row;
