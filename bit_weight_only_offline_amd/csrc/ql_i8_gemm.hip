@@ -685,8 +685,8 @@ constexpr I8Cfg CFGS[] = {
     {0, 1, 1, 8, 1, 1, 0}, {0, 1, 2, 8, 1, 1, 0},      // up to 16 rows, one or two column tiles
     {0, 2, 1, 8, 1, 1, 0}, {0, 2, 2, 8, 1, 1, 0},      // 32 rows
     {2, 8, 4, 1, 2, 4, 2},      // 256 x 256
-    {1, 4, 4, 1, 2, 4, 5},      // 128 x 256
-    {1, 4, 2, 1, 2, 4, 5},      // 128 x 128
+    {1, 4, 4, 1, 2, 4, 6},      // 128 x 256
+    {1, 4, 2, 1, 2, 4, 6},      // 128 x 128
     {1, 2, 2, 1, 2, 4, 6},      // 64 x 128
     {1, 2, 2, 4, 2, 2, 5},      // 64 x 64, four groups
 };
