@@ -12,8 +12,9 @@
 //
 // Both are bound by memory: each row is read once, held in registers in float32 through all
 // of its reductions, and written once.  x is formed from the float32 r', not from its
-// rounded copy.  One workgroup walks a run of rows, so the weight vectors stay in registers
-// and the next row is on its way while this one is reduced.
+// rounded copy.  One workgroup walks several rows, so the weight vectors stay in registers and
+// the next row is on its way while this one is reduced.  8192 x 4096, float32 stream: 79 us,
+// 5.1 TB/s; backward, bf16 stream: 87 us, 4.6 TB/s, and 5.5 us for the column sums.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(TMAX) block_norm_kernel(NormArgs a) {
     __shared__ float red[2 * 16 * 4];
     const int T = blockDim.x, waves = T >> 6, t = threadIdx.x * V;
     int turn = 0;
-    const int row0 = blockIdx.x * a.rows_per_wg, row1 = min(a.R, row0 + a.rows_per_wg);
+    const int64_t row0 = blockIdx.x, row1 = a.R, by = gridDim.x;
     const float inv_c = 1.0f / float(a.C);
     const bool pf32 = !a.p_bf16;
 
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(TMAX) block_norm_kernel(NormArgs a) {
     int64_t gate_of = -1;
 
     Raw<V> ny[NV], nr[NV];
-    auto fetch = [&](int row) {
+    auto fetch = [&](int64_t row) {
         const __amdgpu_buffer_rsrc_t py = row_of(a.y, row, a.C, false), pr = row_of(a.r, row, a.C, RF32);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(TMAX) block_norm_kernel(NormArgs a) {
         }
     };
     if (KEEP && row0 < row1) fetch(row0);
-    for (int row = row0; row < row1; ++row) {
+    for (int64_t row = row0; row < row1; row += by) {
         float y[E], r[E];
         if (!KEEP) fetch(row);
 #pragma unroll
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(TMAX) block_norm_kernel(NormArgs a) {
             widen<V>(ny[v], false, y + v * V);
             widen<V>(nr[v], RF32, r + v * V);
         }
-        if (KEEP && row + 1 < row1) fetch(row + 1);
+        if (KEEP && row + by < row1) fetch(row + by);
 
         if (a.y) {
             float ip = 1.0f;
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(TMAX) block_norm_kernel(NormArgs a) {
 }
 
 // ---- backward --------------------------------------------------------------------------
-// Workgroup i walks rows of one gate (chunk i mod cpb of gate i / cpb), or, where there are
+// Workgroup i walks every cpb-th row of one gate (from i mod cpb, gate i / cpb), or, where there are
 // more gates than workgroups (cpb = 1), all rows of gpw gates.  The column sums stay in
 // registers and leave once a workgroup (dgate: once a gate where cpb = 1).
 template <int V, int NV, int TMAX, bool RF32>
@@ -260,13 +261,15 @@ __global__ void __launch_bounds__(TMAX, NV <= (V == 8 ? 1 : 4) ? 4 : 1) block_no
     const float inv_c = 1.0f / float(a.C);
     const bool pf32 = !a.p_bf16;
     const int i = blockIdx.x;
-    int64_t row0, row1;
+    int64_t row0, row1, by;
     if (a.cpb > 1) {
-        row0 = int64_t(i / a.cpb) * a.gate_rows + int64_t(i % a.cpb) * a.rows_per_wg;
-        row1 = min(row0 + a.rows_per_wg, int64_t(i / a.cpb + 1) * a.gate_rows);
+        row0 = int64_t(i / a.cpb) * a.gate_rows + i % a.cpb;
+        row1 = int64_t(i / a.cpb + 1) * a.gate_rows;
+        by = a.cpb;
     } else {
         row0 = int64_t(i) * a.rows_per_wg;
         row1 = min(int64_t(a.R), row0 + a.rows_per_wg);
+        by = 1;
     }
 
     const int step = T * V;
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(TMAX, NV <= (V == 8 ? 1 : 4) ? 4 : 1) block_no
         }
     };
     if (KEEP && row0 < row1) fetch(row0);
-    for (int64_t row = row0; row < row1; ++row) {
+    for (int64_t row = row0; row < row1; row += by) {
         float y[E], r[E], x[E], d[E];
         if (!KEEP) fetch(row);
 #pragma unroll
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(TMAX, NV <= (V == 8 ? 1 : 4) ? 4 : 1) block_no
             widen<V>(nx[v], false, x + v * V);
             widen<V>(nd[v], RF32, d + v * V);
         }
-        if (KEEP && row + 1 < row1) fetch(row + 1);
+        if (KEEP && row + by < row1) fetch(row + by);
 
         // n = dx w_pre replaces x in the second half: x itself is needed for dw_pre
         float ss[3] = {0.0f, 0.0f, 0.0f};
@@ -452,9 +455,9 @@ hipError_t launch_block_norm(const NormArgs &args, bool vec, hipStream_t st) {
     // as few values a thread as 512 threads allow (a short row's latency), then 1024 threads
     if (vec) NV = loads_per_thread(a.C, 8, a.C > 512 * 16 ? 1024 : 512, {1, 2, 4}, T);
     else NV = loads_per_thread(a.C, 1, a.C > 512 * 16 ? 1024 : 512, {4, 8, 16, 32}, T);
-    const int64_t wgs = std::min<int64_t>(a.R, 256 * (2048 / std::max(T, 256)));
-    a.rows_per_wg = int(ceil_div(a.R, wgs));
-    const int grid = int(ceil_div(a.R, a.rows_per_wg));
+    // Workgroup i takes rows i, i + grid, ..: rows in flight together are neighbours in memory
+    // (runs of rows to each instead: 95 against 79 us for 8192 x 4096 from memory).
+    const int grid = int(std::min<int64_t>(a.R, 512 * (2048 / std::max(T, 256))));
     if (vec) {
         if (NV == 1) return launch_fwd<8, 1, 1024>(a, T, grid, st);
         if (NV == 2) return launch_fwd<8, 2, 1024>(a, T, grid, st);

@@ -23,7 +23,6 @@ struct NormArgs {
     int R, C;
     int gate_rows;          // rows of one gate vector, 0: one vector for all rows
     int p_bf16, r_f32;
-    int rows_per_wg;
 };
 
 struct NormBackArgs {
