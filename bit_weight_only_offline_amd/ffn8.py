@@ -81,15 +81,16 @@ def _need(ok: bool, message: str) -> None:
 
 
 def _tensor(t, name: str, dtypes, device=None) -> torch.Tensor:
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and not t.requires_grad and t.is_cuda
+            and (device is None or t.device == device)):
+        return t
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
         _fail(f"{name} must be a tensor of {' or '.join(str(d).replace('torch.', '') for d in dtypes)}")
     if t.requires_grad:
         _fail(f"{name} must not require grad: call the backward functions")
     if not t.is_cuda:
         _fail("the library runs on a HIP device only")
-    if device is not None and t.device != device:
-        _fail(f"{name} must be on {device}")
-    return t
+    _fail(f"{name} must be on {device}")
 
 
 def _out(out, shape, dtype, device, name="out") -> torch.Tensor:
@@ -347,18 +348,21 @@ def _norm_args(residual, y, post_weight, pre_weight, gate, eps):
     elif post_weight is not None or gate is not None:
         _fail("post_weight and gate need y")
     dtype, gates = None, 0
+    allowed = _FLOATS
     for p in (post_weight, pre_weight, gate):
         if p is None:
             continue
-        _tensor(p, "weights and gate", _FLOATS if dtype is None else (dtype,), dev)
-        dtype = p.dtype
+        _tensor(p, "weights and gate", allowed, dev)
+        if dtype is None:
+            dtype = p.dtype
+            allowed = (dtype,)
         if p is gate:
             gates = 1 if p.dim() == 1 else p.shape[0]
             if p.dim() not in (1, 2) or p.shape[-1] != C:
                 _fail("gate must be [C] or [B, C]")
             if gates == 0 or R % gates:
                 _fail("the rows must divide evenly among the gates")
-        elif p.dim() != 1 or p.shape[0] != C:
+        elif p.dim() != 1 or len(p) != C:
             _fail("a norm weight must be [C]")
     if not eps > 0.0:
         _fail("eps must be positive")
@@ -392,16 +396,17 @@ def block_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *, post_we
     residual, y, post_weight, pre_weight, gate = _c(residual), _c(y), _c(post_weight), _c(pre_weight), _c(gate)
     if int8 and pre_weight is None:
         _fail("int8 output needs pre_weight")
-    r_out = _out(residual_out, shape, residual.dtype, dev, "residual_out")
+    r_out = torch.empty_like(residual) if residual_out is None else \
+        _out(residual_out, shape, residual.dtype, dev, "residual_out")
     x = codes = scales = None
     if pre_weight is not None:
         if int8:
-            codes = torch.empty(shape, dtype=torch.int8, device=dev)
-            scales = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+            codes = torch.empty_like(residual, dtype=torch.int8)
+            scales = residual.new_empty(shape[:-1], dtype=torch.float32)
         else:
-            x = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    _call("qlinear_block_norm", dev, _p(residual), _DTYPES[residual.dtype], _p(y), _p(post_weight), _p(pre_weight),
-          _p(gate), dt, gates, residual_scale, eps, R, C, _p(r_out), _p(x), _p(codes), _p(scales))
+            x = torch.empty_like(residual, dtype=torch.bfloat16)
+    _call("qlinear_block_norm", dev, residual.data_ptr(), _DTYPES[residual.dtype], _p(y), _p(post_weight),
+          _p(pre_weight), _p(gate), dt, gates, residual_scale, eps, R, C, r_out.data_ptr(), _p(x), _p(codes), _p(scales))
     return r_out, ((codes, scales) if int8 else x)
 
 
@@ -428,10 +433,10 @@ def block_norm_backward(dx: torch.Tensor | None, dresidual: torch.Tensor | None,
         _tensor(dresidual, "dresidual", (residual_out.dtype,), dev)
         _need(dresidual.shape == residual_out.shape, "dresidual must have the residual's shape")
         dresidual = dresidual.contiguous()
-    dr = torch.empty(residual_out.shape, dtype=residual_out.dtype, device=dev)
-    dy = None if y is None else torch.empty(y.shape, dtype=torch.bfloat16, device=dev)
-    dpost, dpre, dgate = (None if t is None else torch.empty(t.shape, dtype=torch.float32, device=dev)
-                          for t in (post_weight, pre_weight, gate))
+    dr = torch.empty_like(residual_out)
+    dy = None if y is None else torch.empty_like(y)
+    dpost, dpre, dgate = [None if t is None else torch.empty_like(t, dtype=torch.float32)
+                          for t in (post_weight, pre_weight, gate)]
     ws, nbytes = _space(workspace, block_norm_backward_workspace_bytes(R, C, gates), dev)
     _call("qlinear_block_norm_backward", dev, _p(dx), _p(dresidual), _p(residual_out), _DTYPES[residual_out.dtype],
           _p(y), _p(post_weight), _p(pre_weight), _p(gate), dt, gates, residual_scale, eps, R, C, _p(dr), _p(dy),
