@@ -46,10 +46,10 @@ inline I8Layout make_i8_layout(int64_t N, int64_t K, bool gated) {
 // Schedules of the forward products.
 //   kind 0 (few rows): one workgroup per NT column tiles over the whole input dimension,
 //          its WK wavefronts taking the chunks in turn; MT row tiles of 16
-//   kind 1 (tiles): WM x WN wavefronts, each MT x NT tiles of 16 x 16, WK times on alternate
-//          chunks; operands staged through LDS, S stages
-//   kind 2 (large tiles): the same with two stages of two chunks, each workgroup walking
-//          several tiles
+//   kind 1 (tiles): WN wavefronts (WM is 1), each MT x NT tiles of 16 x 16, WK times on
+//          alternate stages of two chunks; activations staged through LDS, S stages
+//   kind 2 (large tiles): WM x WN wavefronts, both operands staged through LDS, S stages of
+//          two chunks, each workgroup walking several tiles
 struct I8Cfg { int kind, MT, NT, WK, WM, WN, S; };
 
 struct I8Plan {

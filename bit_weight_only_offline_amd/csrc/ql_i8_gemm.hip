@@ -11,6 +11,7 @@
 // and stores them together.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "ql_act.hpp"
@@ -105,7 +106,10 @@ __device__ inline void emit(const I8Args &a, int m, int t, int at, F total) {
 // through LDS too and leave element by element, neighbouring lanes to neighbouring addresses:
 // 28.9 us for 3000 x 5001 x 1024, 40.7 with each lane storing its own four channels.
 template <int NT, bool GATED>
-constexpr int out_stride() { return (GATED ? (NT > 4 ? NT / 2 : 2) : NT) * 32 + 16; }
+constexpr int out_stride() {                               // float32: up to two tiles or half of them at a time
+    constexpr int CT = GATED ? NT / 2 : NT;
+    return (CT <= 2 ? CT * 64 : CT * 32) + 16;
+}
 template <int NT, bool GATED>
 constexpr int out_bytes() { return 16 * out_stride<NT, GATED>(); }
 
@@ -127,7 +131,7 @@ __device__ inline void store_elements(const I8Args &a, E *dst, int64_t ld, int m
     const int row0 = lane / LINE, col = lane % LINE;
     const uint8_t *from = mine + row0 * stride + col * sizeof(E);
     E *to = dst + int64_t(m + row0) * ld + n + col;
-#pragma unroll 1
+#pragma unroll 4
     for (int row = row0; row < 16; row += STEP, from += STEP * stride, to += STEP * ld)
         if (m + row < a.M && n + col < a.N) *to = *reinterpret_cast<const E *>(from);
 }
@@ -138,7 +142,7 @@ __device__ inline void store_tiles(const I8Args &a, int m_first, int ct0, const 
     constexpr int CT = GATED ? NT / 2 : NT;                // channel tiles of the wavefront
     constexpr int PIECES = 2 * CT, STRIDE = out_stride<NT, GATED>(), KINDS = GATED ? 3 : 1;
     constexpr int ROWS = 64 / PIECES < 16 ? 64 / PIECES : 16;
-    constexpr int HALF = CT > 1 ? CT / 2 : 1;              // float32 tiles that fit at a time
+    constexpr int HALF = CT <= 2 ? CT : CT / 2;            // float32 tiles that fit at a time
     const int g = lane >> 4, c = lane & 15;
     const int kinds = GATED && a.raw ? 3 : 1;
     const int p_row = lane / PIECES, n_mine = ct0 * TILE_N + 8 * (lane % PIECES);
@@ -287,32 +291,80 @@ __global__ void __launch_bounds__(64 * WK) i8_rows_kernel(I8Args a) {
     }
 }
 
-// ---- tiles: both operands staged through LDS ------------------------------------------
-// WM x WN wavefronts, each 16 MT tokens x NT column tiles, WK times: the WK groups take
-// alternate chunks (64 inputs) and their sums meet in LDS at the end, which keeps a compute
-// unit's matrix cores busy where there are too few tiles for several workgroups.  A stage is
-// WK chunks of 16 MT WM activation rows and of NT WN weight tiles; S stages form a ring that
-// direct buffer->LDS loads fill.  Activation rows are loaded in 64-byte runs; a XOR swizzle of their
-// 16-byte pieces, applied to the global address of each lane, spreads the 16 rows of an
-// operand read over all banks.  Weight tiles are stored in operand order, so their reads are
-// linear.
-template <int WM, int WN, int WK, int MT, int NT, int S, bool GATED, bool SPLIT>
-__global__ void __launch_bounds__(64 * WM * WN * WK) i8_tile_kernel(I8Args a) {
+// The end of a wavefront's MT x NT tiles (tokens from m, tiles from nt, of which those before
+// nt_end exist): partial sums of a split, or outputs through `mine`.
+template <int MT, int NT, bool GATED, bool SPLIT>
+__device__ inline void finish_tiles(const I8Args &a, int m0, int nt, int nt_end, const i32x4 (&acc)[NT][MT], uint8_t *mine,
+                                    int lane) {
+    const int g = lane >> 4, c = lane & 15;
+    if constexpr (SPLIT) {
+        const int64_t width = int64_t(a.ntiles) * TILE_N;
+        int32_t *part = a.part + int64_t(blockIdx.y) * a.M * width;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int m = m0 + i * 16 + c;
+            if (m >= a.M) continue;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                if (nt + j < nt_end)
+                    *reinterpret_cast<i32x4 *>(part + int64_t(m) * width + (nt + j) * TILE_N + 4 * g) = acc[j][i];
+        }
+    } else {
+        // All scales and biases first: behind the first stores their loads could not be shared.
+        const int ct0 = GATED ? nt / 2 : nt;
+        float xs[MT];
+        Channels q[NT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int m = m0 + i * 16 + c;
+            xs[i] = m < a.M ? a.xs[m] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const int n = (ct0 + (GATED ? j / 2 : j)) * TILE_N + 4 * g;
+            q[j] = Channels{};
+            if (n < a.N) q[j] = channels(a, nt + j, 4 * g, (GATED && (j & 1) ? int64_t(a.N) : 0) + n, a.N - n);
+        }
+        store_tiles<MT, NT, GATED, false>(a, m0, ct0, acc, [&](int i) { return xs[i]; }, [&](int j) { return q[j]; }, mine, lane);
+    }
+}
+
+// ---- tiles: activations through LDS, the weight straight to registers ------------------
+// WN wavefronts, each all 16 MT tokens x its own NT column tiles, WK times on alternate stages
+// (their sums meet in LDS at the end, which keeps a compute unit's matrix cores busy where
+// there are too few tiles for several workgroups).  No two wavefronts of a group read the same
+// weight tile, so it would gain nothing from LDS: packed in operand order it goes from memory
+// to the registers it is multiplied from, S stages ahead, and LDS holds and serves the
+// activations alone.  With both staged, LDS traffic was what the small tiles waited for: a
+// chunk of a 64 x 128 tile took 0.15 us and takes 0.13, of a 128 x 128 tile 0.28 and 0.235.
+// 2048 x 4096 x 14336 from memory went from 107 us to 98.3 (2.45 POP/s: power bounds it),
+// 256 x 4096 x 14336 from 29.0 to 24.3, 64 x 8192 x 8192 from 16.4 to 13.5.  The small tiles
+// are bound by their 6 to 12 KiB of operands a chunk, about 100 bytes a nanosecond and unit.
+//
+// A stage is two chunks: 128-byte runs of the rows, pieces swizzled as for the large
+// tiles.  One barrier a stage, in its middle: by then every wavefront has read the stage's
+// second half into registers and the next stage has arrived, so the loads of the stage S on
+// go to this one's place.  The loop takes whole rounds of the ring; the stages left, already
+// loaded, follow it without another wait (leaving the loop in the middle instead made the
+// compiler wait for loads just issued at the loop's head, where it joins the paths).
+template <int WN, int WK, int MT, int NT, int S, bool GATED>
+constexpr int tile_lds() {
+    const int ring = S * WK * MT * 2048, rows = (WK - 1) * WN * MT * NT * 1024 + WN * out_bytes<NT, GATED>();
+    return ring > rows ? ring : rows;
+}
+
+template <int WN, int WK, int MT, int NT, int S, bool GATED, bool SPLIT>
+__global__ void __launch_bounds__(64 * WN * WK) i8_tile_kernel(I8Args a) {
     static_assert(!GATED || NT % 2 == 0, "up and gate tiles go together");
-    constexpr int W = WM * WN * WK;
-    constexpr int MP = 16 * MT * WM, NTT = NT * WN;
-    constexpr int XA = MP / 16, XB = NTT;              // 1 KiB loads a chunk
-    constexpr int NA = XA * WK, NB = XB * WK;          // and a stage
-    // every wavefront issues the same number of loads; where they do not divide evenly some
-    // are issued twice (the same bytes to the same place)
-    constexpr int NAW = (NA + W - 1) / W, NBW = (NB + W - 1) / W, PER_STAGE = NAW + NBW;
-    constexpr int STAGE = (NA + NB) * 1024;
-    static_assert(S * STAGE <= LDS_BYTES_MAX && S >= 4 && S <= 6, "ring fits the LDS");
+    constexpr int MP = 16 * MT, NTT = NT * WN;
+    constexpr int XL = MP / 8 / WN;                       // 1 KiB loads of rows a wavefront and stage
+    constexpr int PER_STAGE = XL + 2 * NT;
+    static_assert(XL * WN * 8 == MP && WN % 2 == 0, "loads divide evenly");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wk = wv / (WM * WN), wm = wv / WN % WM, wn = wv % WN;
+    const int wk = wv / WN, wn = wv % WN;
     const int g = lane >> 4, c = lane & 15;
 
     // Block b runs on XCD b mod 8: give each XCD one contiguous run of the tile order, and
@@ -329,42 +381,43 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) i8_tile_kernel(I8Args a) {
     const int nt_here = min(NTT, a.ntiles - nt0), m_here = min(MP, a.M - m0);
 
     const int kc0 = SPLIT ? int(blockIdx.y) * a.cps : 0;
-    const int nck = SPLIT ? min(a.kchunks - kc0, a.cps) : a.kchunks;   // chunks, and stages of them
-    const int nst = (nck + WK - 1) / WK;
+    const int nck = SPLIT ? min(a.kchunks - kc0, a.cps) : a.kchunks;
+    const int nst = (nck + 2 * WK - 1) / (2 * WK);
 
     const __amdgpu_buffer_rsrc_t wr =
         make_rsrc(a.w + int64_t(nt0) * a.kchunks * TILE_BYTES, uint32_t(nt_here) * uint32_t(a.kchunks) * TILE_BYTES);
     const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x + int64_t(m0) * a.K, uint32_t(m_here) * uint32_t(a.K));
 
-    // load l of a stage: chunk l / XA, 16 rows l mod XA; then chunk l / XB, tile l mod XB
-    uint32_t off[PER_STAGE];
+    // Chunks past the last are multiplied with weights that read as zero, so the activations
+    // there need only lie in the buffer's range or past it.
+    uint32_t x_off[XL], w_off[NT];
 #pragma unroll
-    for (int q = 0; q < NAW; ++q) {
-        const int l = (wv + W * q) % NA, row = (l % XA) * 16 + lane / 4;
-        off[q] = row < m_here ? uint32_t(row) * uint32_t(a.K) + uint32_t(kc0 + l / XA) * I8_CHUNK +
-                                    16u * uint32_t((lane % 4) ^ row_swizzle(row))
-                              : OUT_OF_RANGE;
+    for (int q = 0; q < XL; ++q) {
+        const int row = (wn + WN * q) * 8 + (lane >> 3), piece = (lane & 7) ^ ((row >> 1) & 7);
+        x_off[q] = row < m_here ? uint32_t(row) * uint32_t(a.K) + uint32_t(kc0 + 2 * wk) * I8_CHUNK + 16u * uint32_t(piece)
+                                : OUT_OF_RANGE;
     }
 #pragma unroll
-    for (int q = 0; q < NBW; ++q) {
-        const int l = (wv + W * q) % NB, tile = l % XB;
-        off[NAW + q] = tile < nt_here ? (uint32_t(tile) * uint32_t(a.kchunks) + uint32_t(kc0 + l / XB)) * TILE_BYTES + 16u * lane
-                                      : OUT_OF_RANGE;
+    for (int j = 0; j < NT; ++j) {
+        const int tile = wn * NT + j;
+        w_off[j] = tile < nt_here ? (uint32_t(tile) * uint32_t(a.kchunks) + uint32_t(kc0 + 2 * wk)) * TILE_BYTES + 16u * lane
+                                  : OUT_OF_RANGE;
     }
-    // load q of stage st; past the last chunk it reads as zero, so that every step of the
-    // loop issues and waits for the same number of loads, and the sums stay as they are
-    auto issue = [&](int q, int st, int buf) {
-        uint8_t *base = lds + buf * STAGE;
-        if (q < NAW) {
-            const int l = (wv + W * q) % NA;
-            const uint32_t past = st * WK + l / XA < nck ? 0u : OUT_OF_RANGE;
-            ld128_lds(xr, (off[q] + uint32_t(st) * (WK * I8_CHUNK)) | past, base + l * 1024);
-        } else {
-            const int l = (wv + W * (q - NAW)) % NB;
-            const uint32_t past = st * WK + l / XB < nck ? 0u : OUT_OF_RANGE;
-            ld128_lds(wr, (off[q] + uint32_t(st) * (WK * TILE_BYTES)) | past, base + (NA + l) * 1024);
-        }
+    uint8_t *const ring = lds + wk * (S * MP * 128);
+    auto load_x = [&](int st, int u) {
+        const uint32_t past = st < nst ? 0u : OUT_OF_RANGE;
+#pragma unroll
+        for (int q = 0; q < XL; ++q)
+            ld128_lds(xr, (x_off[q] + uint32_t(st) * (WK * 2 * I8_CHUNK)) | past, ring + u * (MP * 128) + (wn + WN * q) * 1024);
     };
+    u32x4 w[S][2][NT], x0[MT], x1[MT];
+    auto load_w = [&](int st, int u, int h) {
+        const uint32_t past = (st * WK + wk) * 2 + h < nck ? 0u : OUT_OF_RANGE;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            w[u][h][j] = ld128(wr, (w_off[j] + uint32_t(st) * (WK * 2 * TILE_BYTES) + uint32_t(h) * TILE_BYTES) | past);
+    };
+    const uint8_t *const x_at[2] = {ring + c * 128 + ((g ^ (c >> 1)) * 16), ring + c * 128 + (((4 + g) ^ (c >> 1)) * 16)};
 
     i32x4 acc[NT][MT];
 #pragma unroll
@@ -372,67 +425,57 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) i8_tile_kernel(I8Args a) {
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
 
-    // A stage's operands in registers.  Reads of the next stage and loads further ahead are
-    // spread between the matrix instructions of this one: issued together behind a barrier,
-    // by all wavefronts at once, they would leave the matrix cores idle.
-    struct Operands {
-        u32x4 x[MT], w[NT];
-    };
-    constexpr int READS = MT + NT;
-    const uint32_t x_at = uint32_t((wk * XA + wm * MT) * 1024 + c * 64 + ((g ^ row_swizzle(c)) * 16));
-    const uint32_t w_at = uint32_t((NA + wk * XB + wn * NT) * 1024 + lane * 16);
-    auto read = [&](Operands &f, const uint8_t *stage, int r) {
-        if (r < MT) f.x[r] = *reinterpret_cast<const u32x4 *>(stage + x_at + r * 1024);
-        else f.w[r - MT] = *reinterpret_cast<const u32x4 *>(stage + w_at + (r - MT) * 1024);
-    };
-    auto slot = [](int s, int by) { return s + by >= S ? s + by - S : s + by; };
-    // Multiplies stage operands `f` while `next` is read from slot `from` and stage `st` is
-    // loaded into slot `to`.
-    auto multiply = [&](const Operands &f, Operands &next, int from, int st, int to) {
-        const uint8_t *ahead = lds + from * STAGE;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
+    for (int u = 0; u < S; ++u) {
+        load_x(u, u);
+        __builtin_amdgcn_sched_barrier(0);               // the waits count loads in this order
+        load_w(u, u, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        load_w(u, u, 1);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    wait_vmcnt<(S - 1) * PER_STAGE>();
+    ring_barrier();
 #pragma unroll
-            for (int i = 0; i < MT; ++i) acc[j][i] = mma(f.w[j], f.x[i], acc[j][i]);
+    for (int i = 0; i < MT; ++i) x0[i] = *reinterpret_cast<const u32x4 *>(x_at[0] + i * 2048);
+    auto multiply = [&](const u32x4 (&wt)[NT], const u32x4 (&x)[MT], u32x4 (&next)[MT], const uint8_t *from) {
 #pragma unroll
-            for (int r = j * READS / (NT - 1); r < (j + 1) * READS / (NT - 1) && r < READS; ++r) read(next, ahead, r);
+        for (int i = 0; i < MT; ++i) {
 #pragma unroll
-            for (int q = j * PER_STAGE / NT; q < (j + 1) * PER_STAGE / NT; ++q) issue(q, st, to);
+            for (int j = 0; j < NT; ++j) acc[j][i] = mma(wt[j], x[i], acc[j][i]);
+            next[i] = *reinterpret_cast<const u32x4 *>(from + i * 2048);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-
-    // One barrier for two stages.  At the barrier before stages st and st + 1 the operands of
-    // st are in registers, st + 1 and st + 2 have arrived, st + 3 .. st + S - 2 are on their
-    // way, and the slots of st and of the stage before it are free: st + S - 1 and st + S go
-    // there.  Past the last stage loads read as zero and nothing uses what is read.
+    int st = 0;
+    for (; st + S <= nst; st += S) {
 #pragma unroll
-    for (int u = 0; u < S - 1; ++u)
-#pragma unroll
-        for (int q = 0; q < PER_STAGE; ++q) issue(q, u, u);
-    Operands f0, f1;
-    wait_vmcnt<(S - 2) * PER_STAGE>();
+        for (int u = 0; u < S; ++u) {
+            multiply(w[u][0], x0, x1, x_at[1] + u * (MP * 128));
+            wait_vmcnt<(S - 2) * PER_STAGE>();
+            ring_barrier();
+            load_x(st + u + S, u);
+            __builtin_amdgcn_sched_barrier(0);
+            load_w(st + u + S, u, 0);
+            multiply(w[u][1], x1, x0, x_at[0] + (u + 1) % S * (MP * 128));
+            load_w(st + u + S, u, 1);
+        }
+    }
+    // what is left has been loaded
+    wait_vmcnt<0>();
     ring_barrier();
 #pragma unroll
-    for (int r = 0; r < READS; ++r) read(f0, lds, r);
-    int st = 0, at = 0;                                   // at: slot of stage st
-    while (true) {
-        wait_vmcnt<(S - 4) * PER_STAGE>();
-        ring_barrier();
-        multiply(f0, f1, slot(at, 1), st + S - 1, slot(at, S - 1));
-        if (st + 1 == nst) break;
-        multiply(f1, f0, slot(at, 2), st + S, at);
-        st += 2;
-        at = slot(at, 2);
-        if (st == nst) break;
+    for (int u = 0; u < S - 1; ++u) {
+        if (st + u < nst) {
+            multiply(w[u][0], x0, x1, x_at[1] + u * (MP * 128));
+            multiply(w[u][1], x1, x0, x_at[0] + (u + 1) * (MP * 128));
+        }
     }
-    wait_vmcnt<0>();
     ring_barrier();                                       // the ring is free for what follows
     if constexpr (WK > 1) {
         // the later groups hand their sums to the first: 1 KiB a tile, 16 bytes a lane
-        static_assert((WK - 1) * XA * XB <= S * STAGE / 1024, "sums fit the ring");
-        i32x4 *const at = reinterpret_cast<i32x4 *>(lds) + (wm * WN + wn) * (MT * NT) * 64 + lane;
-        constexpr int GROUP = WM * WN * MT * NT * 64;
+        i32x4 *const at = reinterpret_cast<i32x4 *>(lds) + wn * (MT * NT) * 64 + lane;
+        constexpr int GROUP = WN * MT * NT * 64;
         if (wk > 0) {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -448,42 +491,8 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) i8_tile_kernel(I8Args a) {
 #pragma unroll
                 for (int i = 0; i < MT; ++i) acc[j][i] += at[k * GROUP + (j * MT + i) * 64];
     }
-
-    if constexpr (SPLIT) {
-        const int64_t width = int64_t(a.ntiles) * TILE_N;
-        int32_t *part = a.part + int64_t(blockIdx.y) * a.M * width;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int m = m0 + (wm * MT + i) * 16 + c;
-            if (m >= a.M) continue;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int tile = wn * NT + j;
-                if (tile < nt_here)
-                    *reinterpret_cast<i32x4 *>(part + int64_t(m) * width + (nt0 + tile) * TILE_N + 4 * g) = acc[j][i];
-            }
-        }
-        return;
-    }
-    // All scales and biases first: behind the first stores their loads could not be shared.
-    const int ct0 = GATED ? (nt0 + wn * NT) / 2 : nt0 + wn * NT;
-    float xs[MT];
-    Channels q[NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int m = m0 + (wm * MT + i) * 16 + c;
-        xs[i] = m < a.M ? a.xs[m] : 0.0f;
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int n = (ct0 + (GATED ? j / 2 : j)) * TILE_N + 4 * g;
-        q[j] = Channels{};
-        if (n < a.N) q[j] = channels(a, nt0 + wn * NT + j, 4 * g, (GATED && (j & 1) ? int64_t(a.N) : 0) + n, a.N - n);
-    }
-    constexpr int SUMS = (WK - 1) * XA * XB * 1024;        // sums of the other groups may still be read
-    static_assert(SUMS + WM * WN * out_bytes<NT, GATED>() <= S * STAGE, "output rows fit the ring");
-    store_tiles<MT, NT, GATED, false>(a, m0 + wm * MT * 16, ct0, acc, [&](int i) { return xs[i]; }, [&](int j) { return q[j]; },
-                               lds + SUMS + wv * out_bytes<NT, GATED>(), lane);
+    constexpr int SUMS = (WK - 1) * WN * MT * NT * 1024;   // sums of the other groups may still be read
+    finish_tiles<MT, NT, GATED, SPLIT>(a, m0, nt0 + wn * NT, nt0 + nt_here, acc, lds + SUMS + wn * out_bytes<NT, GATED>(), lane);
 }
 
 // ---- large tiles ----------------------------------------------------------------------
@@ -682,21 +691,24 @@ __global__ void __launch_bounds__(256) i8_join_kernel(I8Args a) {
 }
 
 constexpr I8Cfg CFGS[] = {
-    {0, 1, 1, 8, 1, 1, 0}, {0, 1, 2, 8, 1, 1, 0},      // up to 16 rows, one or two column tiles
-    {0, 2, 1, 8, 1, 1, 0}, {0, 2, 2, 8, 1, 1, 0},      // 32 rows
+    {0, 1, 1, 8, 1, 1, 0}, {0, 1, 2, 8, 1, 1, 0},      // 16 rows, one or two column tiles
     {2, 8, 4, 1, 2, 4, 2},      // 256 x 256
-    {1, 4, 4, 1, 2, 4, 6},      // 128 x 256
-    {1, 4, 2, 1, 2, 4, 6},      // 128 x 128
-    {1, 2, 2, 1, 2, 4, 6},      // 64 x 128
-    {1, 2, 2, 4, 2, 2, 5},      // 64 x 64, four groups
+    {1, 8, 2, 1, 1, 8, 3},      // 128 x 256
+    {1, 8, 1, 1, 1, 8, 4},      // 128 x 128
+    {1, 4, 2, 1, 1, 4, 4},      // 64 x 128
+    {1, 4, 1, 2, 1, 4, 4},      // 64 x 64, two groups
+    {1, 2, 1, 2, 1, 4, 6},      // 32 x 64, two groups
 };
-constexpr int NUM_CFGS = 9, FIRST_TILE = 4;
+constexpr int NUM_CFGS = 8, WIDE = 2, SHARED = 4;
 // Microseconds that a compute unit takes for one chunk of a workgroup's tile, and for the
-// tile besides (start, first loads, stores): from runs with one workgroup a unit over 4096 to
-// 14336 inputs.  128 x 128 and 64 x 128 with twice the groups on twice the wavefronts, and
-// 64 x 128 tiles of four wavefronts, were slower wherever they were tried.
-constexpr float CHUNK_US[NUM_CFGS] = {0, 0, 0.036f, 0.064f, 0.75f, 0.43f, 0.28f, 0.15f, 0.09f};
-constexpr float TILE_US = 4.0f, JOIN_US = 5.0f, JOIN_BYTES_PER_US = 4.0e6f;
+// tile besides (start, first loads, stores), which workgroups that share a compute unit hide
+// from each other (from SHARED on; larger ones have it to themselves).  From runs with one
+// workgroup a unit over 4096 to 14336 inputs.  Also tried, and slower at most sizes: 64 x 128
+// with two groups, 64 x 64 with one or four, 128 x 256 of four wavefronts, rings of up to six
+// stages for the larger tiles.
+constexpr float CHUNK_US[NUM_CFGS] = {0.039f, 0.039f, 0.75f, 0.33f, 0.235f, 0.13f, 0.087f, 0.06f};
+constexpr float TILE_US[NUM_CFGS] = {4.0f, 4.0f, 6.0f, 6.5f, 5.8f, 4.7f, 4.5f, 4.5f};
+constexpr float JOIN_US = 5.0f, JOIN_BYTES_PER_US = 4.0e6f;
 constexpr int ROWS_U = 4;
 constexpr int WIDE_WGS = 256;    // workgroups that walk the large tiles: one a compute unit
 
@@ -742,11 +754,13 @@ hipError_t launch_wide(const I8Args &a, hipStream_t st) {
 template <int I, bool GATED, bool SPLIT>
 hipError_t launch_tiles_of(const I8Args &a, hipStream_t st) {
     constexpr I8Cfg t = CFGS[I];
-    constexpr size_t lds = size_t(t.S) * t.WK * (t.MT * t.WM + t.NT * t.WN) * TILE_BYTES;
-    auto kern = i8_tile_kernel<t.WM, t.WN, t.WK, t.MT, t.NT, t.S, GATED, SPLIT>;
+    // a gated weight's tiles come in pairs
+    constexpr int NT = GATED && t.NT == 1 ? 2 : t.NT, WN = t.WN * t.NT / NT;
+    constexpr size_t lds = tile_lds<WN, t.WK, t.MT, NT, t.S, GATED>();
+    auto kern = i8_tile_kernel<WN, t.WK, t.MT, NT, t.S, GATED, SPLIT>;
     static const hipError_t set = allow_lds(kern, lds);
     if (set != hipSuccess) return set;
-    hipLaunchKernelGGL(kern, dim3(unsigned(a.mtiles * a.nblocks), unsigned(a.ks)), dim3(64 * t.WM * t.WN * t.WK), lds, st, a);
+    hipLaunchKernelGGL(kern, dim3(unsigned(a.mtiles * a.nblocks), unsigned(a.ks)), dim3(64 * WN * t.WK), lds, st, a);
     return hipGetLastError();
 }
 
@@ -762,14 +776,13 @@ hipError_t launch_any(int cfg, const I8Args &a, hipStream_t st) {
     switch (cfg) {
         // a gated weight's tiles come in pairs
         case 0: if constexpr (GATED) return hipErrorInvalidValue; else return launch_rows<0, false>(a, st);
-        case 2: if constexpr (GATED) return hipErrorInvalidValue; else return launch_rows<2, false>(a, st);
         case 1: return launch_rows<1, GATED>(a, st);
-        case 3: if constexpr (GATED) return launch_rows<3, true>(a, st); else return hipErrorInvalidValue;
-        case 4: return launch_wide<4, GATED>(a, st);
+        case 2: return launch_wide<2, GATED>(a, st);
+        case 3: return launch_tiles<3, GATED>(a, st);
+        case 4: return launch_tiles<4, GATED>(a, st);
         case 5: return launch_tiles<5, GATED>(a, st);
         case 6: return launch_tiles<6, GATED>(a, st);
-        case 7: return launch_tiles<7, GATED>(a, st);
-        default: return launch_tiles<8, GATED>(a, st);
+        default: return launch_tiles<7, GATED>(a, st);
     }
 }
 
@@ -780,9 +793,12 @@ hipError_t launch_any(int cfg, const I8Args &a, hipStream_t st) {
 // against 10.4 with two tiles; 28672 x 4096, 16 rows: 19.8 against 18.9).  More rows take the
 // schedule and the split of the input dimension whose time is least by the measured rates:
 // rounds of workgroups over 256 compute units, and for a split the partial sums' way to
-// memory and back and a launch.  Measured against every other tile at 17 to 2048 x 4096 x
-// 4096 and 14336, 333 x 5001 x 4128, 1500 x 3000 x 2048, and gated 77 x 5003 x 2080, 32 and
-// 64 x 14336 x 4096 and 700 x 2000 x 4096, its choice was the fastest or within 6% of it.
+// memory and back and a launch.  Up to 32 rows the streaming kernel, 16 rows a workgroup, is
+// one of them (32 x 4096 x 14336: 12.8 us, 32 x 64 tiles in two splits 13.9).  Measured
+// against every other choice at 20 to 2048 x 4096 x 4096 and 14336, 32 to 128 x 14336 x 4096
+// and 8192 x 8192, 333 x 5008 x 4128, 1500 x 3008 x 2048, and gated at 20 to 512 x 14336 x
+// 4096, 77 x 5003 x 2080, 100 and 700 x 2000 x 4096 and 1500 x 3000 x 2048, its choice was the
+// fastest or within 8% of it.
 I8Plan make_i8_plan(const I8Layout &L, int64_t M) {
     I8Plan p;
     p.cps = int(L.kchunks);
@@ -796,19 +812,18 @@ I8Plan make_i8_plan(const I8Layout &L, int64_t M) {
         p.cfg = !L.gated && L.ntiles <= 512 ? 0 : 1;
     } else {
         float best = 0.0f;
-        for (int c = FIRST_TILE - 1; c < NUM_CFGS; ++c) {
-            const bool rows = c < FIRST_TILE;
-            if (rows && M > 64) continue;
-            const int cfg = rows && !L.gated ? 2 : c;
-            blocks(cfg, mt, nb);
+        for (int c = M <= 32 ? 1 : WIDE; c < NUM_CFGS; ++c) {
+            blocks(c, mt, nb);
+            const int step = 2 * CFGS[c].WK;                             // chunks of a stage
             for (int ks : {1, 2, 3, 4, 6, 8}) {
-                const int64_t cps = ceil_div(ceil_div(L.kchunks, ks), CFGS[cfg].WK) * CFGS[cfg].WK;
-                if (ks > 1 && (CFGS[cfg].kind != 1 || cps < 8 * CFGS[cfg].WK || ceil_div(L.kchunks, cps) < ks)) break;
-                float us = float(ceil_div(mt * nb * ks, 256)) * (float(rows ? L.kchunks : cps) * CHUNK_US[cfg] + TILE_US);
+                const int64_t cps = ks == 1 ? L.kchunks : ceil_div(ceil_div(L.kchunks, ks), step) * step;
+                if (ks > 1 && (CFGS[c].kind != 1 || cps < 8 * CFGS[c].WK || ceil_div(L.kchunks, cps) < ks)) break;
+                const float rounds = float(ceil_div(mt * nb * ks, 256));
+                float us = rounds * float(cps) * CHUNK_US[c] + (c >= SHARED ? 1.0f : rounds) * TILE_US[c];
                 if (ks > 1) us += JOIN_US + float(ks) * float(M) * float(L.ntiles) * TILE_N * 8.0f / JOIN_BYTES_PER_US;
                 if (best == 0.0f || us < best) {
                     best = us;
-                    p.cfg = cfg;
+                    p.cfg = c;
                     p.ks = ks;
                     p.cps = int(cps);
                 }
