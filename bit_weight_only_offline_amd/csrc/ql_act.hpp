@@ -46,24 +46,30 @@ __device__ inline uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
 
+// Vectors at any element's address: the compute units' memory access is set up to take loads
+// and stores at every alignment, and the compiler, told that these are not aligned, emits
+// single instructions for them.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
 // Four consecutive values of one row at element index i, of which the first `count` exist.
-// vec: the row starts four-element aligned, so one store serves.
-__device__ inline void store4_bf16(uint16_t *p, int64_t i, const float (&v)[4], int count, bool vec) {
-    if (vec && count >= 4) {
-        *reinterpret_cast<u32x2 *>(p + i) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+__device__ inline void store4_bf16(uint16_t *p, int64_t i, const float (&v)[4], int count) {
+    if (count >= 4) {
+        *reinterpret_cast<u32x2_any *>(p + i) = u32x2_any{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
     } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 3; ++r)
             if (r < count) reinterpret_cast<__bf16 *>(p)[i + r] = (__bf16)v[r];
     }
 }
-__device__ inline void store4_f32(float *p, int64_t i, const float (&v)[4], int count, bool vec) {
-    if (vec && count >= 4) {
-        *reinterpret_cast<f32x4 *>(p + i) = f32x4{v[0], v[1], v[2], v[3]};
+__device__ inline void store4_f32(float *p, int64_t i, const float (&v)[4], int count) {
+    if (count >= 4) {
+        *reinterpret_cast<f32x4_any *>(p + i) = f32x4_any{v[0], v[1], v[2], v[3]};
     } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (r < count) p[i + r] = v[r];
+        if (count > 0) p[i] = v[0];
+        if (count > 1) p[i + 1] = v[1];
+        if (count > 2) p[i + 2] = v[2];
     }
 }
 

@@ -71,18 +71,10 @@ struct I8Args {
     int M, N, K, ntiles, kchunks;
     int mtiles, nblocks, ks, cps;
     int act, out_f32;
-    int vec, vec8;          // rows of out (and raw) may be stored four / eight channels at a time
+    int pieces;             // rows of out and raw lie on 16-byte boundaries
 };
 
 I8Plan make_i8_plan(const I8Layout &L, int64_t M);
-
-// Rows of 64 bytes in LDS (four 16-byte pieces): piece p of row r sits at place
-// p ^ row_swizzle(r).  An operand read takes one piece of each of 16 rows with 16 lanes, four
-// such sets in one instruction, and the LDS serves 16 lanes at a time: either 16 consecutive
-// ones, or (as the conflict counter shows) lanes 0-3, 12-15, 20-23, 24-27 and their like.
-// With r / 4 negated both kinds of groups touch all 64 banks once; with r / 4 itself the
-// second kind meets twice in half of them.
-__host__ __device__ constexpr int row_swizzle(int r) { return (-(r >> 2)) & 3; }
 
 // Launch arguments of the backward products  dx = operand . q.
 struct I8BackArgs {

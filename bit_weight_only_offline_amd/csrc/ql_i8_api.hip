@@ -59,8 +59,7 @@ ql_status forward(const void *codes, const float *scales, int64_t M, int64_t N, 
     a.M = int(M);
     a.act = act;
     a.out_f32 = out_dtype == QL_F32 ? 1 : 0;
-    a.vec = N % 4 == 0 && aligned(out, 4 * es) && aligned(raw, 8);
-    a.vec8 = N % 8 == 0 && aligned(out, 16) && aligned(raw, 16);
+    a.pieces = N % 8 == 0 && aligned(out, 16) && aligned(raw, 16);
     return from_hip(launch_i8_forward(L, p, a, (hipStream_t)stream));
 }
 

@@ -57,8 +57,8 @@ __device__ inline void emit_linear(const I8Args &a, int m, float xs, int n, cons
     float v[4];
     scaled(q, xs, sum, v);
     const int64_t i = int64_t(m) * a.N + n;
-    if (a.out_f32) store4_f32(static_cast<float *>(a.out), i, v, count, a.vec);
-    else store4_bf16(static_cast<uint16_t *>(a.out), i, v, count, a.vec);
+    if (a.out_f32) store4_f32(static_cast<float *>(a.out), i, v, count);
+    else store4_bf16(static_cast<uint16_t *>(a.out), i, v, count);
 }
 
 // Gated: the same of an up and a gate tile.
@@ -72,12 +72,12 @@ __device__ inline void emit_gated(const I8Args &a, int m, float xs, int n, const
 #pragma unroll
     for (int r = 0; r < 4; ++r) h[r] = gate_act(g[r], a.act) * u[r];
     const int64_t i = int64_t(m) * a.N + n;
-    if (a.out_f32) store4_f32(static_cast<float *>(a.out), i, h, count, a.vec);
-    else store4_bf16(static_cast<uint16_t *>(a.out), i, h, count, a.vec);
+    if (a.out_f32) store4_f32(static_cast<float *>(a.out), i, h, count);
+    else store4_bf16(static_cast<uint16_t *>(a.out), i, h, count);
     if (a.raw) {
         const int64_t j = int64_t(m) * 2 * a.N + n;
-        store4_bf16(a.raw, j, u, count, a.vec);
-        store4_bf16(a.raw, j + a.N, g, count, a.vec);
+        store4_bf16(a.raw, j, u, count);
+        store4_bf16(a.raw, j + a.N, g, count);
     }
 }
 
@@ -102,39 +102,15 @@ __device__ inline void emit(const I8Args &a, int m, int t, int at, F total) {
 // stores, and a gated product that also stores [up | gate] 509 against 721.  STREAM: stores
 // that ask the caches to let go of the lines: the large tiles' outputs otherwise push out the
 // operands that the other workgroups read (468 against 409 us for 4096 x 32768 x 4096).
-// Rows that no vector store fits (channel counts off eight, or off four for float32) go
-// through LDS too and leave element by element, neighbouring lanes to neighbouring addresses:
-// 28.9 us for 3000 x 5001 x 1024, 40.7 with each lane storing its own four channels.
+// Rows may start anywhere (channel counts off eight): the stores are whole pieces all the same,
+// which memory takes at any address, and element by element only where a row ends (333 x 5001
+// x 4128 to float32 from memory 15.4 us, 17.0 with elements throughout).  Such stores do not
+// cover whole cache lines and are not streamed (gated 1500 x 5001 x 1024 with [up | gate]:
+// 27.6 us, 37.7 with streaming stores).
 template <int NT, bool GATED>
-constexpr int out_stride() {                               // float32: up to two tiles or half of them at a time
-    constexpr int CT = GATED ? NT / 2 : NT;
-    return (CT <= 2 ? CT * 64 : CT * 32) + 16;
-}
+constexpr int out_stride() { return (GATED ? NT / 2 : NT) * 32 + 16; }
 template <int NT, bool GATED>
 constexpr int out_bytes() { return 16 * out_stride<NT, GATED>(); }
-
-// Sixteen tokens (from m) by T channel tiles (from channel n) as elements of type E.
-template <typename E, int T>
-__device__ inline void store_elements(const I8Args &a, E *dst, int64_t ld, int m, int n, const float (*v)[4],
-                                      uint8_t *mine, int stride, int lane) {
-    const int g = lane >> 4, c = lane & 15;
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-        if constexpr (sizeof(E) == 4)
-            *reinterpret_cast<f32x4 *>(mine + c * stride + t * 64 + g * 16) = f32x4{v[t][0], v[t][1], v[t][2], v[t][3]};
-        else
-            *reinterpret_cast<u32x2 *>(mine + c * stride + t * 32 + g * 8) =
-                u32x2{pack_bf16(v[t][0], v[t][1]), pack_bf16(v[t][2], v[t][3])};
-    }
-    constexpr int LINE = 16 * T, STEP = 64 / LINE > 0 ? 64 / LINE : 1;     // elements a row, rows a step
-    static_assert(LINE <= 64, "a row at most a wavefront");
-    const int row0 = lane / LINE, col = lane % LINE;
-    const uint8_t *from = mine + row0 * stride + col * sizeof(E);
-    E *to = dst + int64_t(m + row0) * ld + n + col;
-#pragma unroll 4
-    for (int row = row0; row < 16; row += STEP, from += STEP * stride, to += STEP * ld)
-        if (m + row < a.M && n + col < a.N) *to = *reinterpret_cast<const E *>(from);
-}
 
 template <int MT, int NT, bool GATED, bool STREAM, typename X, typename C>
 __device__ inline void store_tiles(const I8Args &a, int m_first, int ct0, const i32x4 (&acc)[NT][MT], X xs, C ch,
@@ -142,7 +118,6 @@ __device__ inline void store_tiles(const I8Args &a, int m_first, int ct0, const 
     constexpr int CT = GATED ? NT / 2 : NT;                // channel tiles of the wavefront
     constexpr int PIECES = 2 * CT, STRIDE = out_stride<NT, GATED>(), KINDS = GATED ? 3 : 1;
     constexpr int ROWS = 64 / PIECES < 16 ? 64 / PIECES : 16;
-    constexpr int HALF = CT <= 2 ? CT : CT / 2;            // float32 tiles that fit at a time
     const int g = lane >> 4, c = lane & 15;
     const int kinds = GATED && a.raw ? 3 : 1;
     const int p_row = lane / PIECES, n_mine = ct0 * TILE_N + 8 * (lane % PIECES);
@@ -169,24 +144,14 @@ __device__ inline void store_tiles(const I8Args &a, int m_first, int ct0, const 
             const int64_t ld = k == 0 ? a.N : 2 * int64_t(a.N);
             if (k == 0 && a.out_f32) {
                 float *const out = static_cast<float *>(a.out);
-                if (a.vec) {
 #pragma unroll
-                    for (int t = 0; t < CT; ++t) {
-                        const int n = (ct0 + t) * TILE_N + 4 * g;
-                        if (mi + c < a.M && n < a.N) store4_f32(out, int64_t(mi + c) * ld + n, v[0][t], 4, true);
-                    }
-                } else {
-#pragma unroll
-                    for (int t = 0; t < CT; t += HALF)
-                        store_elements<float, HALF>(a, out, ld, mi, (ct0 + t) * TILE_N, v[0] + t, mine, STRIDE, lane);
+                for (int t = 0; t < CT; ++t) {
+                    const int n = (ct0 + t) * TILE_N + 4 * g;
+                    if (mi + c < a.M && n < a.N) store4_f32(out, int64_t(mi + c) * ld + n, v[0][t], a.N - n);
                 }
                 continue;
             }
             uint16_t *const dst = k == 0 ? static_cast<uint16_t *>(a.out) : a.raw + (k == 1 ? 0 : a.N);
-            if (!a.vec8) {
-                store_elements<uint16_t, CT>(a, dst, ld, mi, ct0 * TILE_N, v[k], mine, STRIDE, lane);
-                continue;
-            }
 #pragma unroll
             for (int t = 0; t < CT; ++t)
                 *reinterpret_cast<u32x2 *>(mine + c * STRIDE + t * 32 + g * 8) =
@@ -194,11 +159,18 @@ __device__ inline void store_tiles(const I8Args &a, int m_first, int ct0, const 
 #pragma unroll
             for (int r0 = 0; r0 < 16; r0 += ROWS) {
                 const int row = r0 + p_row, m = mi + row;
-                const u32x4 piece = *reinterpret_cast<const u32x4 *>(mine + (row & 15) * STRIDE + (lane % PIECES) * 16);
+                const uint8_t *const from = mine + (row & 15) * STRIDE + (lane % PIECES) * 16;
+                const u32x4 piece = *reinterpret_cast<const u32x4 *>(from);
                 if (p_row < ROWS && m < a.M && n_mine < a.N) {
-                    u32x4 *const to = reinterpret_cast<u32x4 *>(dst + int64_t(m) * ld + n_mine);
-                    if constexpr (STREAM) __builtin_nontemporal_store(piece, to);
-                    else *to = piece;
+                    uint16_t *const to = dst + int64_t(m) * ld + n_mine;
+                    if (n_mine + 8 > a.N) {
+#pragma unroll 1
+                        for (int e = 0; n_mine + e < a.N; ++e) to[e] = reinterpret_cast<const uint16_t *>(from)[e];
+                    } else if (STREAM && a.pieces) {
+                        __builtin_nontemporal_store(piece, reinterpret_cast<u32x4 *>(to));
+                    } else {
+                        *reinterpret_cast<u32x4_any *>(to) = piece;
+                    }
                 }
             }
         }
@@ -576,8 +548,17 @@ __global__ void __launch_bounds__(64 * WM * WN) i8_wide_kernel(I8Args a) {
             ld128_lds(it.wr, w_off + far, base + XA * 1024);
         }
     };
+    // The lane number formed anew, where it is used once a tile: the compiler, which cannot
+    // see through the empty statement, then keeps neither it nor the addresses that follow from
+    // it in registers through the loop, whose operands and sums take all 256.
+    auto lane_again = [] {
+        uint32_t all = ~0u;
+        asm volatile("" : "+s"(all));
+        return int(__builtin_amdgcn_mbcnt_hi(all, __builtin_amdgcn_mbcnt_lo(all, 0)));
+    };
     // the tile's token and channel scales, 64 a wavefront
     auto issue_scales = [&](const Item &it) {
+        const int lane = lane_again();
         constexpr int XW = MP / 64, SW = NP / 64;
         static_assert(MP % 64 == 0 && NP % 64 == 0 && XW + SW <= W, "one load a wavefront");
         if (wv < XW)
@@ -647,17 +628,15 @@ __global__ void __launch_bounds__(64 * WM * WN) i8_wide_kernel(I8Args a) {
             if (st == 0) issue_scales(cur);      // every wavefront is past the last tile's stores
             buf ^= 1;
         }
-        if (a.bias && tid < NP) {
-            const int tile = cur.nt0 + tid / TILE_N, n = (GATED ? tile >> 1 : tile) * TILE_N + tid % TILE_N;
-            l_b[tid] = n < a.N ? bf16_bits_to_f32(a.bias[(GATED && (tile & 1) ? int64_t(a.N) : 0) + n]) : 0.0f;
+        if (a.bias && wv * 64 < NP) {
+            const int at_b = wv * 64 + lane_again(), tile = cur.nt0 + at_b / TILE_N;
+            const int n = (GATED ? tile >> 1 : tile) * TILE_N + at_b % TILE_N;
+            l_b[at_b] = n < a.N ? bf16_bits_to_f32(a.bias[(GATED && (tile & 1) ? int64_t(a.N) : 0) + n]) : 0.0f;
         }
         wait_vmcnt<0>();                                   // the next tile's first two stages
         ring_barrier();
 
-        // The lane number by way of an empty statement that may change it: addresses of the
-        // outputs are then formed here, and do not sit in registers through the loop above.
-        int out_lane = lane;
-        asm volatile("" : "+v"(out_lane));
+        const int out_lane = lane_again();
         const int g = out_lane >> 4, c = out_lane & 15;
         const int ct0 = GATED ? (cur.nt0 + wn * NT) / 2 : cur.nt0 + wn * NT;
         store_tiles<MT, NT, GATED, true>(
