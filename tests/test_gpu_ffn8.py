@@ -346,11 +346,13 @@ def test_gated_backward_matches(M, N, K, act):
     loss = (arg + 10) * 8 * E                                 # of the logistic factors
     _close(draw[:, :N], d * a, (H + loss) * (d * a).abs() + E, "dup")
     _close(draw[:, N:], d * u * da, H * (d * u * da).abs() + 4 * loss * (d * u).abs() * (1 + z.abs()) ** 2 + E, "dgate")
-    # the product reads the rounded draw that it returns
+    # the product's operand is the scaled gradient, rounded once
     w = torch.cat([up.to(D) * us.to(D)[:, None], gt.to(D) * gs.to(D)[:, None]])
-    ref = torch.mm(draw.to(D), w)
-    size = torch.mm(draw.to(D).abs(), w.abs())
-    _close(dx, ref, (H + 4 * N * E) * size + H * ref.abs(), "dx")
+    exact = torch.cat([d * a, d * u * da], 1)
+    slip = torch.cat([loss * (d * a).abs(), 4 * loss * (d * u).abs() * (1 + z.abs()) ** 2], 1)
+    ref = torch.mm(exact, w)
+    size = torch.mm(exact.abs(), w.abs())
+    _close(dx, ref, (H + 4 * N * E) * size + torch.mm(slip, w.abs()) + H * ref.abs(), "dx")
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
