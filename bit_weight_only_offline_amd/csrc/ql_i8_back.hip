@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
     // so that all wavefronts wait for the same count
     constexpr int NAW = NA < BACK_WAVES ? 1 : NA / BACK_WAVES;
     constexpr int A_BYTES = MP * 128, R_BYTES = 8 * 1024, D_BYTES = BACK_KP * 64;
+    constexpr bool LATE = MT == 8;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     uint8_t *const ldsA = lds, *const ldsR = ldsA + 2 * A_BYTES, *const ldsD = ldsR + 4 * R_BYTES;
 
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
     }
     auto fetch = [&](Packed &p, int u) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p.w[i] = *reinterpret_cast<const uint32_t *>(fetch_at[i] + (u & 3) * R_BYTES) ^ 0x80808080u;
+        for (int i = 0; i < 4; ++i) p.w[i] = *reinterpret_cast<const uint32_t *>(fetch_at[i] + (u & 3) * R_BYTES);
     };
     // Byte b (input 4 dj + b of the group) of four channels.  A byte u = q + 128 in the low
     // bits of 2^23 is the float 2^23 + u; 2^23 + 128 less gives q exactly, and so does its
@@ -141,7 +142,10 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
     // instructions at a quarter of it.
     uint32_t magic = 0x4B000000u;
     asm("" : "+v"(magic));             // in a vector register, which leaves the selectors scalar
-    auto decode = [&](const Packed &p, int u, int b) {
+    auto decode = [&](Packed &p, int u, int b) {
+        if (b == 0)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p.w[i] ^= 0x80808080u;
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -178,7 +182,15 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
         // since: tiles of st + 3 and st + 4, and in an odd step before its tiles the rows.
         if (u & 1) wait_vmcnt<2>();
         else wait_vmcnt<NAW + 2>();
-        ring_barrier();
+        if constexpr (LATE) {
+            // all but the last two reads of x: the stores of the last step, which are older, are
+            // done, and so are its reads of w
+            asm volatile("s_waitcnt lgkmcnt(2)" : : : "memory");
+            __builtin_amdgcn_s_barrier();
+            compiler_fence();
+        } else {
+            ring_barrier();
+        }
         Packed p;
         fetch(p, u + 2);
 #pragma unroll
@@ -189,7 +201,8 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
                                                                     __builtin_bit_cast(bf16x8, x[i]), acc[j][i], 0, 0, 0);
             read_x(u + 1, i);
 #pragma unroll
-            for (int j = i * NT / MT; j < (i + 1) * NT / MT; ++j) read_w(next, u + 1, j);
+            for (int j = 0; j < NT; ++j)
+                if (LATE ? i == j + 1 : i == ((j + 1) * MT - 1) / NT) read_w(next, u + 1, j);
             // decoding starts behind a group of matrix instructions, under which its words
             // arrive, and ends before the last, under which its stores finish
             constexpr int D0 = MT >= 8 ? 2 : (MT >= 2 ? 1 : 0), D1 = MT >= 8 ? 6 : (MT >= 4 ? 3 : MT);
@@ -197,9 +210,16 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
 #pragma unroll
                 for (int b = (i - D0) * 4 / (D1 - D0); b < (i - D0 + 1) * 4 / (D1 - D0); ++b) decode(p, u + 2, b);
             // rows of the pair of steps behind the next one, to the place of the last one
+            if (LATE && (u & 1) && i == 3) {
+                // this wavefront's last reads of that place are older than the words it has
+                // decoded since; past this barrier, so are all the others'
+                __builtin_amdgcn_s_barrier();
+                compiler_fence();
+            }
             if (u & 1)
 #pragma unroll
-                for (int q = i * NAW / MT; q < (i + 1) * NAW / MT; ++q) issue_y(q, st + 3, u + 3);
+                for (int q = 0; q < NAW; ++q)
+                    if (i == (LATE ? 4 + q * (MT - 4) / NAW : ((q + 1) * MT - 1) / NAW)) issue_y(q, st + 3, u + 3);
             if (i == MT - 1) issue_w(st + 5, u + 5);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -224,9 +244,11 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
         }
         ring_barrier();
 #pragma unroll
-        for (int i = 0; i < MT; ++i) read_x(0, i);
-#pragma unroll
         for (int j = 0; j < NT; ++j) read_w(w0, 0, j);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) read_x(0, i);
+        __builtin_amdgcn_sched_barrier(0);
         // the slot of step st0's tiles is decoded: those of step st0 + 4 go there
         issue_w(st0 + 4, 0);
         // whole groups of four: steps past the end read as zero and add nothing
