@@ -16,12 +16,12 @@
 // instead needs no pass over dy, but a multiplication and a rounding for every code in the
 // inner loop, where decoding is what keeps the matrix cores waiting.)
 //
-// From memory, 2048 x 4096 x 14336 takes 207 us: 8 for the operand and 199 for the product,
-// 1.21 PFLOP/s on 448 tiles, 1.75 rounds of the 256 compute units.  Gated 2048 x 14336 x 4096
-// takes 476: 77 for du, dg and the operand (414 MB, memory-bound), 386 for the product, 1.25
-// PFLOP/s in two splits on all compute units at once, 13 to join them.  The matrix
-// instructions alone, on random data, run at 2.1 PFLOP/s and a library's bf16 product with
-// nothing to decode at 1.46: power bounds the loop next to its decoding.
+// From memory, 2048 x 4096 x 14336 takes 213 us: 8 for the operand and 205 for the product,
+// 1.17 PFLOP/s on 448 tiles, 1.75 rounds of the 256 compute units.  Gated 2048 x 14336 x 4096
+// takes 481: 77 for du, dg and the operand (411 MB, memory-bound), 386 for the product, 1.25
+// PFLOP/s in two splits on all compute units at once, 13 to join them.  The matrix cores are
+// busy for 58% of the cycles; without any decoding the product would take some 4% less, with
+// all data zero 13% less, as the clock then stays at 2.4 GHz in place of 2.17.
 #include <hip/hip_runtime.h>
 
 #include "ql_act.hpp"
@@ -67,6 +67,10 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
     // so that all wavefronts wait for the same count
     constexpr int NAW = NA < BACK_WAVES ? 1 : NA / BACK_WAVES;
     constexpr int A_BYTES = MP * 128, R_BYTES = 8 * 1024, D_BYTES = BACK_KP * 64;
+    // The largest tile does not wait at a step's barrier for its last two reads of x, which it
+    // uses last (213 us against 219.6 for 2048 x 4096 x 14336 from memory; the smaller tiles read
+    // up to the end).  Rows loaded over the place those reads take theirs from then need a
+    // barrier of their own, every other step.
     constexpr bool LATE = MT == 8;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     uint8_t *const ldsA = lds, *const ldsR = ldsA + 2 * A_BYTES, *const ldsD = ldsR + 4 * R_BYTES;
