@@ -680,13 +680,14 @@ constexpr I8Cfg CFGS[] = {
 };
 constexpr int NUM_CFGS = 8, WIDE = 2, SHARED = 4;
 // Microseconds that a compute unit takes for one chunk of a workgroup's tile, and for the
-// tile besides (start, first loads, stores), which workgroups that share a compute unit hide
-// from each other (from SHARED on; larger ones have it to themselves).  From runs with one
-// workgroup a unit over 4096 to 14336 inputs.  Also tried, and slower at most sizes: 64 x 128
-// with two groups, 64 x 64 with one or four, 128 x 256 of four wavefronts, rings of up to six
-// stages for the larger tiles.
-constexpr float CHUNK_US[NUM_CFGS] = {0.039f, 0.039f, 0.75f, 0.33f, 0.235f, 0.13f, 0.087f, 0.06f};
-constexpr float TILE_US[NUM_CFGS] = {4.0f, 4.0f, 6.0f, 6.5f, 5.8f, 4.7f, 4.5f, 4.5f};
+// tile besides: start, first loads, stores.  From SHARED on workgroups share a unit and hide
+// those from each other: a second round's costs nothing, one of the rounds after it two fifths
+// (128 x 128) or a fifth.  From runs with one workgroup a unit over 4096 to 14336 inputs and
+// with several over 160 to 512.  Also tried, and slower at most sizes: 64 x 128 with two
+// groups, 64 x 64 with one or four, 128 x 256 of four wavefronts, rings of up to six stages for
+// the larger tiles.
+constexpr float CHUNK_US[NUM_CFGS] = {0.039f, 0.039f, 0.75f, 0.36f, 0.235f, 0.13f, 0.087f, 0.06f};
+constexpr float TILE_US[NUM_CFGS] = {4.0f, 4.0f, 8.0f, 6.0f, 6.2f, 4.7f, 4.5f, 4.5f};
 constexpr float JOIN_US = 5.0f, JOIN_BYTES_PER_US = 4.0e6f;
 constexpr int ROWS_U = 4;
 constexpr int WIDE_WGS = 256;    // workgroups that walk the large tiles: one a compute unit
@@ -774,10 +775,11 @@ hipError_t launch_any(int cfg, const I8Args &a, hipStream_t st) {
 // rounds of workgroups over 256 compute units, and for a split the partial sums' way to
 // memory and back and a launch.  Up to 32 rows the streaming kernel, 16 rows a workgroup, is
 // one of them (32 x 4096 x 14336: 12.8 us, 32 x 64 tiles in two splits 13.9).  Measured
-// against every other choice at 20 to 2048 x 4096 x 4096 and 14336, 32 to 128 x 14336 x 4096
-// and 8192 x 8192, 333 x 5008 x 4128, 1500 x 3008 x 2048, and gated at 20 to 512 x 14336 x
-// 4096, 77 x 5003 x 2080, 100 and 700 x 2000 x 4096 and 1500 x 3000 x 2048, its choice was the
-// fastest or within 8% of it.
+// against every other choice at 20 to 4096 x 4096 x 4096 and 14336, 32 to 4096 x 14336 x 4096,
+// 32 to 128 x 8192 x 8192, 333 x 5008 x 4128, 1500 x 3008 x 2048, 2000 x 8192 x 256, 8192 x 1024 x
+// 512 and 2100 x 4200 x 224, and gated at 20 to 4096 x 14336 x 4096, 77 x 5003 x 2080, 100 and 700
+// x 2000 x 4096, 1000 x 8192 x 2048 and 1500 x 3000 x 2048, its choice was the fastest or within
+// 8% of it.
 I8Plan make_i8_plan(const I8Layout &L, int64_t M) {
     I8Plan p;
     p.cps = int(L.kchunks);
@@ -798,7 +800,10 @@ I8Plan make_i8_plan(const I8Layout &L, int64_t M) {
                 const int64_t cps = ks == 1 ? L.kchunks : ceil_div(ceil_div(L.kchunks, ks), step) * step;
                 if (ks > 1 && (CFGS[c].kind != 1 || cps < 8 * CFGS[c].WK || ceil_div(L.kchunks, cps) < ks)) break;
                 const float rounds = float(ceil_div(mt * nb * ks, 256));
-                float us = rounds * float(cps) * CHUNK_US[c] + (c >= SHARED ? 1.0f : rounds) * TILE_US[c];
+                const float starts = c < SHARED ? rounds : 1.0f + std::max(0.0f, rounds - 2.0f) * (c == SHARED ? 0.4f : 0.2f);
+                // compute units that a last round leaves idle leave their power to the others
+                const float work = c == WIDE ? std::max(1.0f, float(mt * nb) / 256.0f) : rounds;
+                float us = work * float(cps) * CHUNK_US[c] + starts * TILE_US[c];
                 if (ks > 1) us += JOIN_US + float(ks) * float(M) * float(L.ntiles) * TILE_N * 8.0f / JOIN_BYTES_PER_US;
                 if (best == 0.0f || us < best) {
                     best = us;

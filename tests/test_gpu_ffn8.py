@@ -101,6 +101,50 @@ def test_linear_large_tiles(M, N, K):
     _close(y, ref, tol, (M, N, K))
 
 
+# tiles of every size, with the input dimension whole and split
+@pytest.mark.parametrize("M,N,K", [(20, 200, 14336), (1900, 8035, 352), (1578, 3949, 640), (67, 5792, 21184), (1024, 4090, 8224),
+                                   (8580, 71, 13376), (270, 3658, 288), (67, 2146, 12544), (200, 4099, 4128),
+                                   (298, 582, 14400), (251, 31, 2816), (33, 334, 12736), (17, 16, 11712)])
+def test_linear_schedules(M, N, K):
+    Q = _Q()
+    x, xs, w, ws, b = _linear_case(M, N, K, 13)
+    print("linear_i8", M, N, K, flush=True)
+    pw = Q.pack_channel(w, ws)
+    y = Q.linear_i8(x, xs, pw, bias=b, out_dtype=torch.float32)
+    ref, tol = _linear_ref(x, xs, w, ws, b)
+    _close(y, ref, tol, (M, N, K))
+    assert torch.equal(Q.linear_i8(x, xs, pw, bias=b), y.bfloat16())
+
+
+# outputs that start at any element, through each way they are stored
+@pytest.mark.parametrize("start", range(8))
+@pytest.mark.parametrize("M,N,K", [(5, 37, 64), (40, 100, 96), (70, 61, 8224), (300, 4100, 160), (2100, 2901, 544),
+                                   (2400, 2104, 1056)])
+def test_outputs_at_any_element(M, N, K, start):
+    Q = _Q()
+    x, xs, w, ws, b = _linear_case(M, N, K, 5)
+    pw = Q.pack_channel(w, ws)
+    print("linear_i8 at", start, M, N, K, flush=True)
+    for dtype in (torch.bfloat16, torch.float32):
+        room = torch.full((start + M * N + 8,), 7.0, dtype=dtype, device="cuda")
+        out = room[start:start + M * N].view(M, N)
+        Q.linear_i8(x, xs, pw, bias=b, out_dtype=dtype, out=out)
+        assert torch.equal(out, Q.linear_i8(x, xs, pw, bias=b, out_dtype=dtype))
+        assert bool((room[:start] == 7).all()) and bool((room[start + M * N:] == 7).all())
+    if N > 3000:
+        return
+    gx, gxs, up, us, gt, gs, gb = _gated_case(M, N, K, 6, True)
+    pg = Q.pack_gated(up, us, gt, gs)
+    want, want_raw = Q.gated_i8(gx, gxs, pg, bias=gb, keep_raw=True)
+    room = torch.full((start + M * N + 8,), 7.0, dtype=torch.bfloat16, device="cuda")
+    rooms = torch.full((start + 2 * M * N + 8,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out, raw = room[start:start + M * N].view(M, N), rooms[start:start + 2 * M * N].view(M, 2 * N)
+    Q.gated_i8(gx, gxs, pg, bias=gb, out=out, raw=raw)
+    assert torch.equal(out, want) and torch.equal(raw, want_raw)
+    for t, n in ((room, M * N), (rooms, 2 * M * N)):
+        assert bool((t[:start] == 7).all()) and bool((t[start + n:] == 7).all())
+
+
 @pytest.mark.parametrize("M", [1, 20, 64, 70, 260])
 def test_linear_longest_rows_do_not_wrap(M):
     """The largest input dimension with all codes -128: sums of 2146959360, just below 2^31."""
@@ -302,6 +346,21 @@ def test_gated_large_tiles(M, N, K):
     h = Q.gated_i8(case[0], case[1], pw, bias=case[6], out_dtype=torch.float32)
     _, _, _, _, ref, tol = _gated_ref(*case, "silu")
     _close(h, ref, tol, (M, N, K))
+
+
+@pytest.mark.parametrize("M,N,K", [(1913, 3977, 544), (325, 8329, 640), (65, 4470, 14464), (1060, 1186, 4000), (8241, 40, 15104),
+                                   (77, 5730, 288), (190, 900, 19136), (33, 4098, 32), (325, 320, 12384), (35, 16, 32),
+                                   (80, 1300, 14144), (25, 779, 128)])
+def test_gated_schedules(M, N, K):
+    Q = _Q()
+    case = _gated_case(M, N, K, 17, True)
+    print("gated_i8", M, N, K, flush=True)
+    pw = Q.pack_gated(*case[2:6])
+    h, raw = Q.gated_i8(case[0], case[1], pw, bias=case[6], keep_raw=True, out_dtype=torch.float32)
+    u, eu, z, ez, ref, tol = _gated_ref(*case, "silu")
+    _close(h, ref, tol, (M, N, K))
+    _close(raw[:, :N], u, eu + H * u.abs(), "up")
+    _close(raw[:, N:], z, ez + H * z.abs(), "gate")
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
