@@ -106,8 +106,11 @@ def _space(workspace, need: int, device) -> tuple:
     if need == 0:
         return None, 0
     if workspace is None:
-        workspace = _Q.workspace(device, need)
-    if workspace.numel() * workspace.element_size() < need or workspace.device != device:
+        # found without the stream object that _Q.workspace() builds (3 us)
+        workspace = _Q._WS.get((device.type, device.index, torch._C._cuda_getCurrentRawStream(device.index)))
+        if workspace is None or workspace.numel() < need:
+            workspace = _Q.workspace(device, need)
+    elif workspace.numel() * workspace.element_size() < need or workspace.device != device:
         _fail(f"workspace needs {need} bytes on {device}")
     return workspace.data_ptr(), need
 
