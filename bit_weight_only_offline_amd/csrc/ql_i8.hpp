@@ -76,10 +76,24 @@ struct I8Args {
 
 I8Plan make_i8_plan(const I8Layout &L, int64_t M);
 
+// Launch arguments of the pass that forms the operand of a backward product.
+struct I8BackOperand {
+    const uint16_t *dy;     // bf16 [M, N]: dy, or dh
+    const uint16_t *raw;    // gated: bf16 [M, 2N] = [up | gate]
+    const float *s;         // channel scales in tile order
+    uint16_t *draw;         // gated: bf16 [M, 2N]
+    uint16_t *operand;      // fp16 [M, Np] (gated [M, 2Np])
+    int32_t *ex;            // [splits][M]
+    int64_t M, N, Np;
+    int64_t groups;         // of eight channels in a split
+    int act;
+};
+
 // Launch arguments of the backward products  dx = operand . q.
 struct I8BackArgs {
-    const uint16_t *dy;     // the operand: scaled gradients, bf16, rows of ldy elements in packed
+    const uint16_t *dy;     // the operand: scaled gradients, fp16, rows of ldy elements in packed
                             // row order, ldy a multiple of 8, zero past the last channel
+    const int32_t *ex;      // [ks][M]: split s of row m is the scaled gradients times 2^ex[s][m]
     const uint8_t *w;
     uint16_t *dx;           // bf16 [M, K]
     float *part;            // float32 partial sums [ks][M][K] or null
@@ -92,7 +106,7 @@ struct I8BackPlan {
     int cfg = 0, mtiles = 1, nblocks = 1;
     int ks = 1, nps = 0;
     int64_t Np = 0;                           // N rounded up to eight (gated: to a tile)
-    size_t operand_bytes = 0, ws_bytes = 0;   // the operand, then partial sums
+    size_t operand_bytes = 0, ex_bytes = 0, ws_bytes = 0;   // the operand, its exponents, partial sums
 };
 
 I8BackPlan make_i8_back_plan(const I8Layout &L, int64_t M);

@@ -1,28 +1,38 @@
-// Backward products with frozen per-channel INT8 weights on the bf16 matrix cores.
+// Backward products with frozen per-channel INT8 weights on the fp16 matrix cores.
 //
 //   linear   dx[m, k] = sum_n dy[m, n] s[n] q[n, k]
 //   gated    du = dh act(g),  dg = dh u act'(g)  (one pass), then the same product over the
 //            rows of both weights, up and gate tiles alternating as they are packed
 //
 // The product contracts over the weight's rows, across the direction it is packed in, and
-// needs it in bf16.  A workgroup therefore turns each 32-row step of its weight columns
+// needs it in fp16.  A workgroup therefore turns each 32-row step of its weight columns
 // into operand order once, through LDS, for all of its rows of dy: a thread takes the four
 // inputs of one 32-bit word from four consecutive channels, and since a byte permute picks
 // any byte of a word, the transposition costs no shuffles of its own.
 //
-// int8 codes are exact in bf16, the channel scales are not: they are folded into dy (or du
-// and dg) in float32 before its rounding to bf16, in the pass that forms the product's
-// operand.  That rounding is the only one before the float32 sums.  (Scaling the codes
-// instead needs no pass over dy, but a multiplication and a rounding for every code in the
-// inner loop, where decoding is what keeps the matrix cores waiting.)
+// int8 codes are exact in fp16, the channel scales are not: they are folded into dy (or du
+// and dg) in float32, in the pass that forms the product's operand.  That pass rounds the
+// scaled gradient once, to fp16's eleven bits: an eighth of the error of the bf16 result's own
+// rounding, so that the result is as good as one from a float32 operand.  (bf16 has eight
+// bits, and as much error again as the result: 0.0023 in place of 0.0017 against 64 bits.)
+// What fp16 lacks is range, which each row therefore gets by itself: it is scaled by a power
+// of two, exact both ways, that takes its largest finite value to 2^14 .. 2^15 (the part of a
+// row that one split contracts over, where the contraction is split).  Values down
+// to 2^-28 of the row's largest keep eleven bits, smaller ones lose them one by one, and the
+// sums stay below 2^43.  (Scaling the codes instead needs no pass over dy, but a
+// multiplication and a rounding for every code in the inner loop, where decoding is what
+// keeps the matrix cores waiting.)
 //
-// From memory, 2048 x 4096 x 14336 takes 213 us: 8 for the operand and 205 for the product,
+// From memory, 2048 x 4096 x 14336 takes 216 us: 10 for the operand and 206 for the product,
 // 1.17 PFLOP/s on 448 tiles, 1.75 rounds of the 256 compute units.  Gated 2048 x 14336 x 4096
-// takes 481: 77 for du, dg and the operand (411 MB, memory-bound), 386 for the product, 1.25
+// takes 475: 77 for du, dg and the operand (411 MB, memory-bound), 385 for the product, 1.25
 // PFLOP/s in two splits on all compute units at once, 13 to join them.  The matrix cores are
-// busy for 58% of the cycles; without any decoding the product would take some 4% less, with
-// all data zero 13% less, as the clock then stays at 2.4 GHz in place of 2.17.
+// busy for 63% of the cycles, at 2.18 GHz; power bounds them rather than decoding, which takes 6
+// instructions for four codes (11 for bf16, at the same times): with all codes zero the call
+// takes 188 us where it takes 207 with random ones.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 #include "ql_act.hpp"
 #include "ql_decode.hpp"
@@ -32,6 +42,9 @@
 
 namespace ql {
 namespace {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t OUT_OF_RANGE = 0x80000000u;   // a buffer offset that reads as zero
 constexpr int NSTEP = 32;                        // weight rows (contraction) per step
@@ -49,7 +62,7 @@ __device__ inline void lds_store8(uint8_t *p, bool second, u32x2 v) {
     else asm volatile("ds_write_b64 %0, %1" : : "v"(at), "v"(v) : "memory");
 }
 
-// LDS: operand rows [MP][64] bf16 (two steps; 128-byte runs, whole cache lines), two stages;
+// LDS: operand rows [MP][64] fp16 (two steps; 128-byte runs, whole cache lines), two stages;
 // packed tiles [2][4] KiB, four; the decoded operand [16][1] KiB, two.
 constexpr int back_lds(int mp) { return 2 * mp * 128 + 4 * 8 * 1024 + 2 * BACK_KP * 64; }
 
@@ -68,7 +81,7 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
     constexpr int NAW = NA < BACK_WAVES ? 1 : NA / BACK_WAVES;
     constexpr int A_BYTES = MP * 128, R_BYTES = 8 * 1024, D_BYTES = BACK_KP * 64;
     // The largest tile does not wait at a step's barrier for its last two reads of x, which it
-    // uses last (213 us against 219.6 for 2048 x 4096 x 14336 from memory; the smaller tiles read
+    // uses last (216 us against 220 for 2048 x 4096 x 14336 from memory; the smaller tiles read
     // up to the end).  Rows loaded over the place those reads take theirs from then need a
     // barrier of their own, every other step.
     constexpr bool LATE = MT == 8;
@@ -141,22 +154,18 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
         for (int i = 0; i < 4; ++i) p.w[i] = *reinterpret_cast<const uint32_t *>(fetch_at[i] + (u & 3) * R_BYTES);
     };
     // Byte b (input 4 dj + b of the group) of four channels.  A byte u = q + 128 in the low
-    // bits of 2^23 is the float 2^23 + u; 2^23 + 128 less gives q exactly, and so does its
-    // upper half as bf16.  Permutes and subtractions run at the full vector rate, conversion
-    // instructions at a quarter of it.
-    uint32_t magic = 0x4B000000u;
-    asm("" : "+v"(magic));             // in a vector register, which leaves the selectors scalar
+    // bits of 2^10 is the fp16 number 2^10 + u, and 2^10 + 128 less gives q exactly.  One
+    // permute takes the bytes of two channels, one XOR makes both numbers of them (0x80 turns
+    // q into u), one subtraction both codes.
     auto decode = [&](Packed &p, int u, int b) {
-        if (b == 0)
+        u32x2 o;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p.w[i] ^= 0x80808080u;
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = __uint_as_float(__builtin_amdgcn_perm(magic, p.w[i], 0x07040400u | uint32_t(b))) - 8388736.0f;
-        lds_store8(store_at[b], u & 1,
-                   u32x2{__builtin_amdgcn_perm(__float_as_uint(v[1]), __float_as_uint(v[0]), 0x07060302u),
-                         __builtin_amdgcn_perm(__float_as_uint(v[3]), __float_as_uint(v[2]), 0x07060302u)});
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t two =
+                __builtin_amdgcn_perm(p.w[2 * i + 1], p.w[2 * i], 0x0C040C00u | uint32_t(b) * 0x10001u) ^ 0x64806480u;
+            o[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, two) - f16x2{(_Float16)1152.0f, (_Float16)1152.0f});
+        }
+        lds_store8(store_at[b], u & 1, o);
     };
 
     f32x4 acc[NT][MT];
@@ -201,8 +210,8 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
         for (int i = 0; i < MT; ++i) {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[j]),
-                                                                    __builtin_bit_cast(bf16x8, x[i]), acc[j][i], 0, 0, 0);
+                acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, w[j]),
+                                                                   __builtin_bit_cast(f16x8, x[i]), acc[j][i], 0, 0, 0);
             read_x(u + 1, i);
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -228,6 +237,17 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
             __builtin_amdgcn_sched_barrier(0);
         }
     };
+
+    // exponents of this lane's rows, ahead of the loop where there are registers for them
+    int ex[MT];
+    auto read_ex = [&] {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int m = m0 + (wm * MT + i) * 16 + c;
+            ex[i] = m < a.M ? -a.ex[int64_t(SPLIT ? blockIdx.y : 0) * a.M + m] : 0;
+        }
+    };
+    if (MT < 8) read_ex();
 
     if (st0 < st1) {
 #pragma unroll
@@ -263,8 +283,16 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
             step(st + 3, 3, w1, w0);
         }
     }
+    if (MT == 8) read_ex();
     wait_vmcnt<0>();
     ring_barrier();                                  // LDS is free for the output rows
+    // the rows' powers of two taken back
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[j][i][r] = __builtin_amdgcn_ldexpf(acc[j][i][r], ex[i]);
 
     if constexpr (SPLIT) {
 #pragma unroll
@@ -315,85 +343,202 @@ __global__ void __launch_bounds__(256) i8_back_join_kernel(const float *__restri
     reinterpret_cast<u32x2 *>(dx)[e] = u32x2{pack_bf16(t[0], t[1]), pack_bf16(t[2], t[3])};
 }
 
-// du, dg for V consecutive channels a thread: draw [M, 2N] = [du | dg] in bf16, and the
-// product's operand [M][16 ntiles], both scaled by their channels and in packed tile order
-// (zero past N).
-template <int V>
-__global__ void __launch_bounds__(256) gate_back_kernel(const uint16_t *__restrict__ dh, const uint16_t *__restrict__ raw,
-                                                        const float *__restrict__ s, uint16_t *__restrict__ draw,
-                                                        uint16_t *__restrict__ operand, int64_t M, int64_t N,
-                                                        int64_t Np, int act) {
-    const int64_t per_row = Np / V, e = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (e >= M * per_row) return;
-    const int64_t m = e / per_row, n = (e % per_row) * V;
-    const int64_t up_at = (n / TILE_N) * 2 * TILE_N + n % TILE_N;    // the gate's 16 further on
-    uint16_t *const op = operand + m * 2 * Np + up_at;
-    if constexpr (V == 8) {
-        u32x4 du{0u, 0u, 0u, 0u}, dg = du, su = du, sg = du;
-        if (n < N) {                                                  // N is a multiple of eight
-            const u32x4 d = *reinterpret_cast<const u32x4 *>(dh + m * N + n);
-            const u32x4 u = *reinterpret_cast<const u32x4 *>(raw + m * 2 * N + n);
-            const u32x4 g = *reinterpret_cast<const u32x4 *>(raw + m * 2 * N + N + n);
+// ---- the operand -----------------------------------------------------------------------
+// Groups of eight consecutive channels of a row.  Rows of dh, raw, dy and draw start at any
+// element; of a group that the row ends in (`left` of it exist) the rest is zero.
+__device__ inline u32x4 load8(const uint16_t *row, int64_t n, int64_t left) {
+    if (left >= 8) return *reinterpret_cast<const u32x4_any *>(row + n);
+    u32x4 v{0u, 0u, 0u, 0u};
+    if (n >= 8) {
+        // the row's last eight, moved to the front
+        const u32x4 w = *reinterpret_cast<const u32x4_any *>(row + n + left - 8);
+        const int gone = 8 - int(left), words = gone >> 1;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                float o[2], p[2];
+        for (int i = 0; i < 4; ++i) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const float dv = bf16_bits_to_f32((d[w] >> (16 * b)) & 0xFFFFu);
-                    const float uv = bf16_bits_to_f32((u[w] >> (16 * b)) & 0xFFFFu);
-                    const float gv = bf16_bits_to_f32((g[w] >> (16 * b)) & 0xFFFFu);
-                    float f, df;
-                    gate_act_grad(gv, act, f, df);
-                    o[b] = dv * f;
-                    p[b] = dv * uv * df;
-                }
-                const float *us = s + up_at + 2 * w, *gs = us + TILE_N;
-                du[w] = pack_bf16(o[0], o[1]);
-                dg[w] = pack_bf16(p[0], p[1]);
-                su[w] = pack_bf16(o[0] * us[0], o[1] * us[1]);
-                sg[w] = pack_bf16(p[0] * gs[0], p[1] * gs[1]);
-            }
-            *reinterpret_cast<u32x4 *>(draw + m * 2 * N + n) = du;
-            *reinterpret_cast<u32x4 *>(draw + m * 2 * N + N + n) = dg;
+            for (int d = 0; i + d < 4; ++d) v[i] |= words == d ? w[i + d] : 0u;
         }
-        *reinterpret_cast<u32x4 *>(op) = su;
-        *reinterpret_cast<u32x4 *>(op + TILE_N) = sg;
+        if (gone & 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = (v[i] >> 16) | (i < 3 ? v[(i + 1) & 3] << 16 : 0u);
+        return v;
+    }
+#pragma unroll 1
+    for (int e = 0; e < left; ++e) {
+        const uint32_t w = uint32_t(row[e]) << (16 * (e & 1));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] |= (e >> 1) == i ? w : 0u;
+    }
+    return v;
+}
+__device__ inline void store8(uint16_t *p, int64_t left, const float (&v)[8]) {
+    const u32x4 o{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+    if (left >= 8) {
+        *reinterpret_cast<u32x4_any *>(p) = o;
     } else {
-        float o = 0.0f, p = 0.0f;
-        if (n < N) {
-            const float dv = bf16_bits_to_f32(dh[m * N + n]), uv = bf16_bits_to_f32(raw[m * 2 * N + n]);
-            const float gv = bf16_bits_to_f32(raw[m * 2 * N + N + n]);
-            float f, df;
-            gate_act_grad(gv, act, f, df);
-            o = dv * f;
-            p = dv * uv * df;
-            reinterpret_cast<__bf16 *>(draw)[m * 2 * N + n] = (__bf16)o;
-            reinterpret_cast<__bf16 *>(draw)[m * 2 * N + N + n] = (__bf16)p;
-            o *= s[up_at];
-            p *= s[up_at + TILE_N];
-        }
-        reinterpret_cast<__bf16 *>(op)[0] = (__bf16)o;
-        reinterpret_cast<__bf16 *>(op)[TILE_N] = (__bf16)p;
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < left) p[e] = uint16_t(o[e >> 1] >> (16 * (e & 1)));
     }
 }
-
-// The linear product's operand: dy [M, N] times the channel scales, rows of Np, zero past N.
-template <int V>
-__global__ void __launch_bounds__(256) scale_back_kernel(const uint16_t *__restrict__ dy, const float *__restrict__ s,
-                                                         uint16_t *__restrict__ operand, int64_t M, int64_t N,
-                                                         int64_t Np) {
-    const int64_t per_row = Np / V, e = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (e >= M * per_row) return;
-    const int64_t m = e / per_row, n = (e % per_row) * V;
-    if constexpr (V == 8) {
-        const u32x4 d = *reinterpret_cast<const u32x4 *>(dy + m * N + n);
-        u32x4 o;
+__device__ inline void unpack8(const u32x4 &r, float (&v)[8]) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-            o[w] = pack_bf16(bf16_bits_to_f32(d[w] & 0xFFFFu) * s[n + 2 * w], bf16_bits_to_f32(d[w] >> 16) * s[n + 2 * w + 1]);
-        *reinterpret_cast<u32x4 *>(operand + m * Np + n) = o;
+    for (int e = 0; e < 8; ++e) v[e] = bf16_bits_to_f32((r[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+}
+
+// TPR threads form the rows of the product's operand, one row at a time, from
+//   plain  dy [M, N]:                    dy s
+//   gated  dh [M, N], raw [M, 2N]:       [du us | dg gs], and draw = [du | dg] in bf16
+// in packed tile order (zero past N) as fp16, and of each row the part of split blockIdx.y:
+// scaled by a power of two that takes its largest finite value into [2^14, 2^15), whose exponent
+// goes to `ex`.  (By splits, so that few rows too are spread over many compute units: the pass
+// for gated 1 x 14336 takes 4.1 us, 7.8 with a workgroup for the whole row.)  A group stays in
+// registers in float32 between the maximum and the rounding (NV groups a thread; NV = 0:
+// rows of any length, read and formed again, and draw written the second time).  The threads
+// walk the rows: their channels' scales stay in registers, and the next row is on its way
+// while this one's maximum is found.
+template <bool GATED, int TPR, int NV>
+__global__ void __launch_bounds__(TPR == 64 ? 256 : TPR, 4) back_operand_kernel(I8BackOperand a) {
+    struct Scales {
+        f32x4 s[GATED ? 2 : 1][2];
+    };
+    constexpr int ROWS = TPR == 64 ? 4 : 1, KINDS = GATED ? 2 : 1, WAVES = TPR / 64;
+    __shared__ float red[2][16];
+    // this thread's groups: t, t + TPR, .. below `groups`
+    const int64_t first = int64_t(blockIdx.y) * a.groups, t = first + threadIdx.x % TPR;
+    const int64_t groups = min(a.Np / 8, first + a.groups);
+    int32_t *const ex_out = a.ex + int64_t(blockIdx.y) * a.M;
+    int turn = 0;
+    // the operand's KINDS x 8 values of group j, and (draw) the stores of du and dg
+    auto form = [&](int64_t m, int64_t j, const u32x4 (&in)[GATED ? 3 : 1], const Scales &s, bool draw, float (&v)[KINDS][8]) {
+        const int64_t n = 8 * j, left = a.N - n;
+        float d[8];
+        unpack8(in[0], d);
+        if constexpr (GATED) {
+            float u[8], g[8];
+            unpack8(in[1], u);
+            unpack8(in[2], g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float f, df;
+                gate_act_grad(g[e], a.act, f, df);
+                v[0][e] = d[e] * f;
+                v[1][e] = d[e] * u[e] * df;
+            }
+            if (draw && left > 0) {
+                store8(a.draw + m * 2 * a.N + n, left, v[0]);
+                store8(a.draw + m * 2 * a.N + a.N + n, left, v[1]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[0][e] = d[e];
+        }
+#pragma unroll
+        for (int k = 0; k < KINDS; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[k][e] *= s.s[k][e >> 2][e & 3];      // zero times zero past N
+    };
+    auto scales = [&](int64_t j, Scales &s) {
+        const float *p = a.s + (GATED ? (j / 2) * 2 * TILE_N + 8 * (j & 1) : 8 * j);
+#pragma unroll
+        for (int k = 0; k < KINDS; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) s.s[k][h] = *reinterpret_cast<const f32x4 *>(p + k * TILE_N + 4 * h);
+    };
+    auto fetch = [&](int64_t m, int64_t j, u32x4 (&in)[GATED ? 3 : 1]) {
+        const int64_t n = 8 * j, left = a.N - n;
+#pragma unroll
+        for (int k = 0; k < (GATED ? 3 : 1); ++k) in[k] = u32x4{0u, 0u, 0u, 0u};
+        if (j >= groups || left <= 0) return;
+        in[0] = load8(a.dy + m * a.N, n, left);
+        if constexpr (GATED) {
+            in[1] = load8(a.raw + m * 2 * a.N, n, left);
+            in[2] = load8(a.raw + m * 2 * a.N + a.N, n, left);
+        }
+    };
+    auto largest = [&](const float (&v)[KINDS][8], float &top) {
+#pragma unroll
+        for (int k = 0; k < KINDS; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float w = fabsf(v[k][e]);
+                top = w < INFINITY ? fmaxf(top, w) : top;
+            }
+    };
+    auto put = [&](int64_t m, int64_t j, const float (&v)[KINDS][8], int ex) {
+        const int64_t n = 8 * j;
+        uint16_t *const op = a.operand + m * KINDS * a.Np + (GATED ? (n / TILE_N) * 2 * TILE_N + n % TILE_N : n);
+#pragma unroll
+        for (int k = 0; k < KINDS; ++k) {
+            f16x8 o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = (_Float16)__builtin_amdgcn_ldexpf(v[k][e], ex);
+            *reinterpret_cast<f16x8 *>(op + k * TILE_N) = o;
+        }
+    };
+    // the exponent for a row's largest value, over the row's threads
+    auto exponent = [&](float top) {
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+        if constexpr (WAVES > 1) {
+            // two halves in turn: one is written again only past the next row's barrier
+            float *const half = red[turn];
+            turn ^= 1;
+            if ((threadIdx.x & 63) == 0) half[threadIdx.x >> 6] = top;
+            __syncthreads();
+            top = half[0];
+#pragma unroll
+            for (int w = 1; w < WAVES; ++w) top = fmaxf(top, half[w]);
+        }
+        return top > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
+    };
+    int64_t m = int64_t(blockIdx.x) * ROWS + threadIdx.x / TPR;
+    const int64_t by = int64_t(gridDim.x) * ROWS;
+    if constexpr (NV > 0) {
+        Scales s[NV];
+        u32x4 in[NV][GATED ? 3 : 1];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (m < a.M) fetch(m, t + i * TPR, in[i]);
+            if (t + i * TPR < groups) scales(t + i * TPR, s[i]);
+        }
+        for (; m < a.M; m += by) {
+            float v[NV][KINDS][8], top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (t + i * TPR < groups) {
+                    form(m, t + i * TPR, in[i], s[i], true, v[i]);
+                    largest(v[i], top);
+                }
+            if (m + by < a.M)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) fetch(m + by, t + i * TPR, in[i]);
+            const int ex = exponent(top);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (t + i * TPR < groups) put(m, t + i * TPR, v[i], ex);
+            if (t == first) ex_out[m] = ex;
+        }
     } else {
-        reinterpret_cast<__bf16 *>(operand)[m * Np + n] = (__bf16)(n < N ? bf16_bits_to_f32(dy[m * N + n]) * s[n] : 0.0f);
+        for (; m < a.M; m += by) {
+            Scales s;
+            u32x4 in[GATED ? 3 : 1];
+            float v[KINDS][8], top = 0.0f;
+            for (int64_t j = t; j < groups; j += TPR) {
+                fetch(m, j, in);
+                scales(j, s);
+                form(m, j, in, s, false, v);
+                largest(v, top);
+            }
+            const int ex = exponent(top);
+            for (int64_t j = t; j < groups; j += TPR) {
+                fetch(m, j, in);
+                scales(j, s);
+                form(m, j, in, s, true, v);
+                put(m, j, v, ex);
+            }
+            if (t == first) ex_out[m] = ex;
+        }
     }
 }
 
@@ -405,6 +550,24 @@ constexpr int back_rows(const BackCfg &t) { return 16 * t.MT * t.WM; }
 // operands and stores; of a split's second launch, besides its sums' way to memory and back.
 constexpr float STEP_US[NUM_BACK_CFGS] = {0.86f, 0.53f, 0.45f, 0.33f};
 constexpr float START_US = 5.0f, JOIN_US = 5.0f, JOIN_BYTES_PER_US = 4.0e6f;
+
+// The operand pass: the fewest threads a row that hold it (its part of a split) in registers, one
+// group each of a gated row and two of a plain one, and as many workgroups as the compute units
+// hold.
+template <bool GATED>
+hipError_t launch_operand(const I8BackOperand &a, int ks, hipStream_t st) {
+    constexpr int NV = GATED ? 1 : 2;
+    const auto grid = [&](int64_t rows, int64_t most) {
+        return dim3(unsigned(std::min(ceil_div(a.M, rows), ceil_div(most, ks))), unsigned(ks));
+    };
+    if (a.groups <= 64 * NV) hipLaunchKernelGGL((back_operand_kernel<GATED, 64, NV>), grid(4, 2048), dim3(256), 0, st, a);
+    else if (a.groups <= 128 * NV) hipLaunchKernelGGL((back_operand_kernel<GATED, 128, NV>), grid(1, 4096), dim3(128), 0, st, a);
+    else if (a.groups <= 256 * NV) hipLaunchKernelGGL((back_operand_kernel<GATED, 256, NV>), grid(1, 2048), dim3(256), 0, st, a);
+    else if (a.groups <= 512 * NV) hipLaunchKernelGGL((back_operand_kernel<GATED, 512, NV>), grid(1, 1024), dim3(512), 0, st, a);
+    else if (a.groups <= 1024 * NV) hipLaunchKernelGGL((back_operand_kernel<GATED, 1024, NV>), grid(1, 512), dim3(1024), 0, st, a);
+    else hipLaunchKernelGGL((back_operand_kernel<GATED, 1024, 0>), grid(1, 512), dim3(1024), 0, st, a);
+    return hipGetLastError();
+}
 
 template <int I>
 hipError_t launch_back(const I8BackArgs &a, hipStream_t st) {
@@ -469,32 +632,37 @@ I8BackPlan make_i8_back_plan(const I8Layout &L, int64_t M) {
         }
     }
     p.operand_bytes = round256(size_t(M) * size_t(p.Np) * (L.gated ? 4 : 2));
-    p.ws_bytes = p.operand_bytes + (p.ks > 1 ? round256(size_t(p.ks) * size_t(M) * size_t(L.K) * 4) : 0);
+    p.ex_bytes = round256(size_t(p.ks) * size_t(M) * 4);
+    p.ws_bytes = p.operand_bytes + p.ex_bytes + (p.ks > 1 ? round256(size_t(p.ks) * size_t(M) * size_t(L.K) * 4) : 0);
     return p;
 }
 
 hipError_t launch_i8_backward(const I8Layout &L, const I8BackPlan &p, const uint16_t *dy, const uint16_t *raw, int act,
                               int64_t M, const void *pw, const void *ps, uint16_t *dx, uint16_t *draw, void *ws,
                               hipStream_t st) {
-    uint16_t *operand = static_cast<uint16_t *>(ws);
-    const float *sc = static_cast<const float *>(ps);
-    const bool vec = L.N % 8 == 0;
-    const dim3 grid(unsigned(ceil_div(M * p.Np / (vec ? 8 : 1), 256)));
-    if (L.gated) {
-        if (vec) hipLaunchKernelGGL(gate_back_kernel<8>, grid, dim3(256), 0, st, dy, raw, sc, draw, operand, M, L.N, p.Np, act);
-        else hipLaunchKernelGGL(gate_back_kernel<1>, grid, dim3(256), 0, st, dy, raw, sc, draw, operand, M, L.N, p.Np, act);
-    } else {
-        if (vec) hipLaunchKernelGGL(scale_back_kernel<8>, grid, dim3(256), 0, st, dy, sc, operand, M, L.N, p.Np);
-        else hipLaunchKernelGGL(scale_back_kernel<1>, grid, dim3(256), 0, st, dy, sc, operand, M, L.N, p.Np);
-    }
-    const hipError_t e = hipGetLastError();
+    uint8_t *const at = static_cast<uint8_t *>(ws);
+    I8BackOperand o{};
+    o.dy = dy;
+    o.raw = raw;
+    o.s = static_cast<const float *>(ps);
+    o.draw = draw;
+    o.operand = reinterpret_cast<uint16_t *>(at);
+    o.ex = reinterpret_cast<int32_t *>(at + p.operand_bytes);
+    o.M = M;
+    o.N = L.N;
+    o.Np = p.Np;
+    // a step of the contraction is two packed tiles: 16 channels of a gated weight, 32 of a plain one
+    o.groups = p.ks > 1 ? int64_t(p.nps) * (L.gated ? 2 : 4) : p.Np / 8;
+    o.act = act;
+    const hipError_t e = L.gated ? launch_operand<true>(o, p.ks, st) : launch_operand<false>(o, p.ks, st);
     if (e != hipSuccess) return e;
     I8BackArgs a{};
     a.w = static_cast<const uint8_t *>(pw);
-    a.dy = operand;
+    a.dy = o.operand;
+    a.ex = o.ex;
     a.ldy = (L.gated ? 2 : 1) * p.Np;
     a.dx = dx;
-    a.part = p.ks > 1 ? reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + p.operand_bytes) : nullptr;
+    a.part = p.ks > 1 ? reinterpret_cast<float *>(at + p.operand_bytes + p.ex_bytes) : nullptr;
     a.M = int(M);
     a.K = int(L.K);
     a.ntiles = int(L.ntiles);

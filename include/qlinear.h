@@ -434,12 +434,15 @@ ql_status qlinear_i8_gated_forward(const void *codes, const float *scales, int64
  *   linear   dx[m, k] = sum_n dy[m, n] s[n] q[n, k]
  *   gated    dup = dh act(gate), dgate = dh up act'(gate), draw = [dup | dgate],
  *            dx = dup . Up + dgate . Gate
- * The channel scales are folded into dy (dup and dgate) in float32 before its one rounding to
- * bf16; the codes are exact in bf16, sums are float32.
+ * The channel scales are folded into dy (dup and dgate) in float32.  The result is rounded once,
+ * to eleven bits (fp16, each row scaled by a power of two of its own: values below 2^-28 of
+ * their row's largest keep fewer), an eighth of the error of dx's own rounding to bf16; the codes
+ * are exact, sums are float32.
  *   dy, dh  bf16 [M, N]; raw, draw bf16 [M, 2N]; dx bf16 [M, K]; all 16-byte aligned
  *   draw's column sums are the gradient of the biases.
  *   workspace  qlinear_i8_backward_workspace_bytes() bytes, 256-byte aligned (NULL if 0): the
- *              scaled operand, and float32 partial sums where the contraction is split
+ *              scaled operand, its rows' exponents, and float32 partial sums where the
+ *              contraction is split
  */
 ql_status qlinear_i8_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated, size_t *bytes);
 ql_status qlinear_i8_backward(const void *dy, int64_t M, int64_t N, int64_t K, const void *packed_w,
