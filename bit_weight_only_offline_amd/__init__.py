@@ -330,29 +330,18 @@ def tile_shapes():
     return out
 
 
-_WS = {}
-
-
 def workspace(device, nbytes: int) -> torch.Tensor:
-    """A shared workspace of at least nbytes on device, reused across calls on the
-    device's current stream (the library does not depend on its contents on entry).
+    """A new workspace of at least nbytes on device, for one call (the library does not depend
+    on its contents on entry).
 
-    There is one per (device, stream): calls on one stream run in order, so they may share
-    it, while calls on two streams may overlap and must not.  It is allocated while that
-    stream is current, so when it grows, the old buffer goes back to torch's allocator
-    ordered after the work already queued on the stream."""
-    d = torch.device(device)
-    if d.index is None:
-        d = torch.device(d.type, torch.cuda.current_device())
-    key = (d.type, d.index, torch.cuda.current_stream(d).cuda_stream)
-    ws = _WS.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=d)
-        _WS[key] = ws
-    return ws
+    Every call that is given none takes one of its own, from torch's allocator while the stream
+    of the call is current: calls from several threads or on several streams share nothing, its
+    memory is used again only by what that stream is given later, and a call captured into a
+    graph has memory of the graph's own pool."""
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
-_shared_workspace = workspace
+_new_workspace = workspace
 
 
 def linear(x: torch.Tensor, pw: PackedWeight, bias: torch.Tensor | None = None, act=None,
@@ -361,7 +350,7 @@ def linear(x: torch.Tensor, pw: PackedWeight, bias: torch.Tensor | None = None, 
     """Y = A . D(Wq)^T + b for bf16 x [..., K] (or [..., 2K] = [up | gate] with act="swiglu").
 
     workspace: a uint8 device buffer (any contents) that stays owned by the caller and
-    may be reused (a shared one per device is used when omitted).  schedule: (tile,
+    may be reused (when omitted, the call takes a new one).  schedule: (tile,
     splits) or a Schedule to override the automatic choice.  Inference only: inputs that
     require grad are rejected."""
     if x.requires_grad or (bias is not None and bias.requires_grad):
@@ -390,7 +379,7 @@ def linear(x: torch.Tensor, pw: PackedWeight, bias: torch.Tensor | None = None, 
     ws_need = workspace_bytes(pw.fmt, M, pw.N, pw.K, pw.group, act, schedule)
     if ws_need:
         if workspace is None:
-            workspace = _shared_workspace(x.device, ws_need)
+            workspace = _new_workspace(x.device, ws_need)
         elif workspace.numel() < ws_need or workspace.device != x.device:
             raise QLinearError(f"workspace needs {ws_need} bytes on {x.device}")
     _check(lib().qlinear_forward_ex(_ptr(x2), M, pw.N, pw.K, _ptr(pw.w), _ptr(pw.s), _ptr(pw.aux), pw.fmt,
@@ -518,7 +507,7 @@ def grouped_linear(x: torch.Tensor, pe: PackedExperts, tokens_per_expert: torch.
         out = torch.empty((T, pe.N), dtype=out_dtype, device=x.device)
     nbytes = grouped_workspace_bytes(pe.fmt, T, pe.E, pe.N, pe.K, pe.group)
     if workspace is None:
-        workspace = _shared_workspace(x.device, nbytes)
+        workspace = _new_workspace(x.device, nbytes)
     elif workspace.numel() < nbytes or workspace.device != x.device:
         raise QLinearError(f"workspace needs {nbytes} bytes on {x.device}")
     od = 1 if out_dtype == torch.float32 else 0
@@ -591,7 +580,7 @@ def linear_a8(x: torch.Tensor, pw: PackedWeight, bias: torch.Tensor | None = Non
         bias = bias.contiguous()
     need = a8_workspace_bytes(pw.fmt, M, pw.N, pw.K, pw.group)
     if workspace is None:
-        workspace = _shared_workspace(x.device, need)
+        workspace = _new_workspace(x.device, need)
     od = 1 if out_dtype == torch.float32 else 0
     _check(lib().qlinear_forward_a8(_ptr(x2), M, pw.N, pw.K, _ptr(pw.w), _ptr(pw.s), pw.fmt, pw.group, _ptr(bias),
                                     _ptr(out), od, _ptr(workspace), workspace.numel(),

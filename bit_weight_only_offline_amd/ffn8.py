@@ -101,18 +101,16 @@ def _out(out, shape, dtype, device, name="out") -> torch.Tensor:
     return out
 
 
-def _space(workspace, need: int, device) -> tuple:
-    """(pointer, bytes) of the caller's workspace, or of the shared one of this stream."""
+def _space(workspace, need: int, device):
+    """The caller's workspace, or a new one; None where none is needed.  It is held until the
+    call has queued its work."""
     if need == 0:
-        return None, 0
+        return None
     if workspace is None:
-        # found without the stream object that _Q.workspace() builds (3 us)
-        workspace = _Q._WS.get((device.type, device.index, torch._C._cuda_getCurrentRawStream(device.index)))
-        if workspace is None or workspace.numel() < need:
-            workspace = _Q.workspace(device, need)
-    elif workspace.numel() * workspace.element_size() < need or workspace.device != device:
+        return _Q.workspace(device, need)
+    if workspace.numel() * workspace.element_size() < need or workspace.device != device:
         _fail(f"workspace needs {need} bytes on {device}")
-    return workspace.data_ptr(), need
+    return workspace
 
 
 def _aligned(t: torch.Tensor) -> torch.Tensor:
@@ -260,9 +258,10 @@ def linear_i8(codes: torch.Tensor, scales: torch.Tensor, pw: ChannelWeight, bias
     lead, M, codes, scales = _activations(codes, scales, pw)
     bias = _bias(bias, pw.N, pw)
     out = _out(out, (*lead, pw.N), out_dtype, pw.device)
-    ws, nbytes = _space(workspace, i8_workspace_bytes(M, pw.N, pw.K), pw.device)
+    need = i8_workspace_bytes(M, pw.N, pw.K)
+    ws = _space(workspace, need, pw.device)
     _call("qlinear_i8_forward", pw.device, codes.data_ptr(), scales.data_ptr(), M, pw.N, pw.K, pw.w.data_ptr(),
-          pw.s.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(), _DTYPES[out_dtype], ws, nbytes)
+          pw.s.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(), _DTYPES[out_dtype], _p(ws), need)
     return out
 
 
@@ -283,10 +282,11 @@ def gated_i8(codes: torch.Tensor, scales: torch.Tensor, pw: GatedWeight, bias: t
     out = _out(out, (*lead, pw.N), out_dtype, pw.device)
     if keep_raw or raw is not None:
         raw = _out(raw, (*lead, 2 * pw.N), torch.bfloat16, pw.device, "raw")
-    ws, nbytes = _space(workspace, i8_workspace_bytes(M, pw.N, pw.K, True), pw.device)
+    need = i8_workspace_bytes(M, pw.N, pw.K, True)
+    ws = _space(workspace, need, pw.device)
     _call("qlinear_i8_gated_forward", pw.device, codes.data_ptr(), scales.data_ptr(), M, pw.N, pw.K, pw.w.data_ptr(),
           pw.s.data_ptr(), None if bias is None else bias.data_ptr(), GATE_ACTS[act], out.data_ptr(),
-          _DTYPES[out_dtype], None if raw is None else raw.data_ptr(), ws, nbytes)
+          _DTYPES[out_dtype], None if raw is None else raw.data_ptr(), _p(ws), need)
     return out if raw is None else (out, raw)
 
 
@@ -301,9 +301,10 @@ def linear_i8_backward(dy: torch.Tensor, pw: ChannelWeight, out: torch.Tensor | 
     dy = _aligned(dy)
     M = dy.numel() // pw.N
     out = _out(out, (*dy.shape[:-1], pw.K), torch.bfloat16, pw.device)
-    ws, nbytes = _space(workspace, i8_backward_workspace_bytes(M, pw.N, pw.K), pw.device)
+    need = i8_backward_workspace_bytes(M, pw.N, pw.K)
+    ws = _space(workspace, need, pw.device)
     _call("qlinear_i8_backward", pw.device, dy.data_ptr(), M, pw.N, pw.K, pw.w.data_ptr(), pw.s.data_ptr(),
-          out.data_ptr(), ws, nbytes)
+          out.data_ptr(), _p(ws), need)
     return out
 
 
@@ -327,9 +328,10 @@ def gated_i8_backward(dh: torch.Tensor, raw: torch.Tensor, pw: GatedWeight, act:
     M = dh.numel() // pw.N
     out = _out(out, (*lead, pw.K), torch.bfloat16, pw.device)
     draw = _out(draw, (*lead, 2 * pw.N), torch.bfloat16, pw.device, "draw")
-    ws, nbytes = _space(workspace, i8_backward_workspace_bytes(M, pw.N, pw.K, True), pw.device)
+    need = i8_backward_workspace_bytes(M, pw.N, pw.K, True)
+    ws = _space(workspace, need, pw.device)
     _call("qlinear_i8_gated_backward", pw.device, dh.data_ptr(), raw.data_ptr(), M, pw.N, pw.K, pw.w.data_ptr(),
-          pw.s.data_ptr(), GATE_ACTS[act], out.data_ptr(), draw.data_ptr(), ws, nbytes)
+          pw.s.data_ptr(), GATE_ACTS[act], out.data_ptr(), draw.data_ptr(), _p(ws), need)
     return out, draw
 
 
@@ -440,8 +442,9 @@ def block_norm_backward(dx: torch.Tensor | None, dresidual: torch.Tensor | None,
     dy = None if y is None else torch.empty_like(y)
     dpost, dpre, dgate = [None if t is None else torch.empty_like(t, dtype=torch.float32)
                           for t in (post_weight, pre_weight, gate)]
-    ws, nbytes = _space(workspace, block_norm_backward_workspace_bytes(R, C, gates), dev)
+    need = block_norm_backward_workspace_bytes(R, C, gates)
+    ws = _space(workspace, need, dev)
     _call("qlinear_block_norm_backward", dev, _p(dx), _p(dresidual), _p(residual_out), _DTYPES[residual_out.dtype],
           _p(y), _p(post_weight), _p(pre_weight), _p(gate), dt, gates, residual_scale, eps, R, C, _p(dr), _p(dy),
-          _p(dpost), _p(dpre), _p(dgate), ws, nbytes)
+          _p(dpost), _p(dpre), _p(dgate), _p(ws), need)
     return dr, dy, dpost, dpre, dgate

@@ -1,0 +1,143 @@
+"""How the 8-bit operators are called: workspaces in graphs and threads, and what their
+arguments may be."""
+import threading
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def _Q():
+    import bit_weight_only_offline_amd as Q
+    return Q
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _codes(g, rows, cols):
+    return torch.randint(-128, 128, (rows, cols), generator=g, device="cuda", dtype=torch.int8)
+
+
+def _bf(g, shape):
+    return torch.randn(shape, generator=g, device="cuda").bfloat16()
+
+
+def _scales(g, n, typical=1e-3):
+    return torch.exp(torch.randn((n,), generator=g, device="cuda")) * typical
+
+
+# ---- workspaces --------------------------------------------------------------------------
+
+def _call(kind, seed, M):
+    """(function of no arguments, its main input, bytes of its workspace), at sizes that use one."""
+    Q, g = _Q(), _gen(seed)
+    if kind in ("linear", "linear back"):
+        N, K = 1024, 14336
+        pw = Q.pack_channel(_codes(g, N, K), _scales(g, N))
+        if kind == "linear":
+            x, xs = _codes(g, M, K), _scales(g, M)
+            return (lambda: (Q.linear_i8(x, xs, pw),)), x, Q.i8_workspace_bytes(M, N, K)
+        dy = _bf(g, (M, N))
+        return (lambda: (Q.linear_i8_backward(dy, pw),)), dy, Q.i8_backward_workspace_bytes(M, N, K)
+    if kind in ("gated", "gated back"):
+        N, K = (320, 14144) if kind == "gated" else (1000, 1056)
+        pw = Q.pack_gated(_codes(g, N, K), _scales(g, N, 1e-6), _codes(g, N, K), _scales(g, N, 1e-6))
+        if kind == "gated":
+            x, xs = _codes(g, M, K), _scales(g, M, 1.0)
+            return (lambda: Q.gated_i8(x, xs, pw, keep_raw=True)), x, Q.i8_workspace_bytes(M, N, K, True)
+        dh, raw = _bf(g, (M, N)), _bf(g, (M, 2 * N))
+        return (lambda: Q.gated_i8_backward(dh, raw, pw)), dh, Q.i8_backward_workspace_bytes(M, N, K, True)
+    C = 512
+    dx, r, y, w = _bf(g, (M, C)), _bf(g, (M, C)), _bf(g, (M, C)), torch.rand((3, C), generator=g, device="cuda")
+    return ((lambda: Q.block_norm_backward(dx, None, r, y, post_weight=w[0], pre_weight=w[1], gate=w[2])), dx,
+            Q.block_norm_backward_workspace_bytes(M, C, 1))
+
+
+KINDS = ["linear", "gated", "linear back", "gated back", "norm back"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_graph_keeps_its_workspace(kind):
+    """Warmed up and captured on a stream, then a larger call on that stream and new tensors of
+    the first workspace's size: replays give the right results and leave those tensors alone."""
+    f, x, need = _call(kind, 1, 70)
+    big, _, more = _call(kind, 2, 190)
+    assert 0 < need < more
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            f()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = f()
+    with torch.cuda.stream(side):
+        big()
+        others = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in (need, need, more, need // 2 + 1) * 3]
+    side.synchronize()
+    g = _gen(9)
+    for i in range(4):
+        x.copy_(torch.randint(-100, 100, x.shape, generator=g, device="cuda").to(x.dtype))
+        torch.cuda.synchronize()
+        print(kind, "replay", i, flush=True)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = f()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), i
+        assert all(bool((t == 0x5A).all()) for t in others), i
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_graphs_of_one_stream_replay_on_two(kind):
+    """Two graphs captured one after the other and replayed at the same time, next to eager
+    calls on a third stream."""
+    calls = [_call(kind, s, 70) for s in (3, 4, 5)]
+    want = [tuple(t.clone() for t in f()) for f, _, _ in calls]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for f, _, _ in calls[:2]:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(f())
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for i in range(4):
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                for _ in range(3):
+                    graph.replay()
+        with torch.cuda.stream(streams[2]):
+            for _ in range(3):
+                eager = calls[2][0]()
+        torch.cuda.synchronize()
+        for got, w in zip((*outs, eager), want):
+            assert all(torch.equal(a, b) for a, b in zip(got, w)), i
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_threads_on_one_stream(kind):
+    """Threads that queue their calls on one stream, each with inputs of its own: the launches of
+    one call may fall between those of another."""
+    calls = [_call(kind, 10 + s, 70 + 10 * s) for s in range(3)]
+    want = [tuple(t.clone() for t in f()) for f, _, _ in calls]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(k):
+        for i in range(60):
+            got = calls[k][0]()
+            if i % 6 == 0 and not all(torch.equal(a, b) for a, b in zip(got, want[k])):
+                wrong.append((k, i))
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong, wrong
