@@ -344,6 +344,17 @@ def workspace(device, nbytes: int) -> torch.Tensor:
 _new_workspace = workspace
 
 
+def _space(workspace, need: int, device) -> torch.Tensor:
+    """The caller's workspace, which has to be `need` bytes in one piece (an expanded or strided
+    view holds fewer than it has elements, or the bytes of others), or a new one."""
+    if workspace is None:
+        return _new_workspace(device, need)
+    if (not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous()
+            or workspace.numel() * workspace.element_size() < need):
+        raise QLinearError(f"workspace must be a contiguous tensor of {need} bytes on {device}")
+    return workspace
+
+
 def linear(x: torch.Tensor, pw: PackedWeight, bias: torch.Tensor | None = None, act=None,
            out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
            workspace: torch.Tensor | None = None, schedule=None) -> torch.Tensor:
@@ -378,10 +389,7 @@ def linear(x: torch.Tensor, pw: PackedWeight, bias: torch.Tensor | None = None, 
         raise QLinearError("out must be a contiguous [M, N] tensor of out_dtype on x's device")
     ws_need = workspace_bytes(pw.fmt, M, pw.N, pw.K, pw.group, act, schedule)
     if ws_need:
-        if workspace is None:
-            workspace = _new_workspace(x.device, ws_need)
-        elif workspace.numel() < ws_need or workspace.device != x.device:
-            raise QLinearError(f"workspace needs {ws_need} bytes on {x.device}")
+        workspace = _space(workspace, ws_need, x.device)
     _check(lib().qlinear_forward_ex(_ptr(x2), M, pw.N, pw.K, _ptr(pw.w), _ptr(pw.s), _ptr(pw.aux), pw.fmt,
                                     pw.group, pw.has_zeros, _ptr(bias), act_id, _ptr(out),
                                     1 if out_dtype == torch.float32 else 0,
@@ -506,14 +514,11 @@ def grouped_linear(x: torch.Tensor, pe: PackedExperts, tokens_per_expert: torch.
     if out is None:
         out = torch.empty((T, pe.N), dtype=out_dtype, device=x.device)
     nbytes = grouped_workspace_bytes(pe.fmt, T, pe.E, pe.N, pe.K, pe.group)
-    if workspace is None:
-        workspace = _new_workspace(x.device, nbytes)
-    elif workspace.numel() < nbytes or workspace.device != x.device:
-        raise QLinearError(f"workspace needs {nbytes} bytes on {x.device}")
+    workspace = _space(workspace, nbytes, x.device)
     od = 1 if out_dtype == torch.float32 else 0
     _check(lib().qlinear_grouped_forward(_ptr(x), T, _ptr(tokens_per_expert.contiguous()), pe.E, pe.N, pe.K,
                                          _ptr(pe.w), _ptr(pe.s), _ptr(pe.aux), pe.fmt, pe.group, pe.has_zeros,
-                                         _ptr(bias), _ptr(out), od, _ptr(workspace), workspace.numel(),
+                                         _ptr(bias), _ptr(out), od, _ptr(workspace), workspace.numel() * workspace.element_size(),
                                          _stream(x.device)), "qlinear_grouped_forward")
     return out
 
@@ -579,11 +584,10 @@ def linear_a8(x: torch.Tensor, pw: PackedWeight, bias: torch.Tensor | None = Non
             raise QLinearError("bias must be bf16 [N]")
         bias = bias.contiguous()
     need = a8_workspace_bytes(pw.fmt, M, pw.N, pw.K, pw.group)
-    if workspace is None:
-        workspace = _new_workspace(x.device, need)
+    workspace = _space(workspace, need, x.device)
     od = 1 if out_dtype == torch.float32 else 0
     _check(lib().qlinear_forward_a8(_ptr(x2), M, pw.N, pw.K, _ptr(pw.w), _ptr(pw.s), pw.fmt, pw.group, _ptr(bias),
-                                    _ptr(out), od, _ptr(workspace), workspace.numel(),
+                                    _ptr(out), od, _ptr(workspace), workspace.numel() * workspace.element_size(),
                                     -1 if tile is None else int(tile), _stream(x.device)), "qlinear_forward_a8")
     return out.reshape(*lead, pw.N)
 

@@ -104,13 +104,7 @@ def _out(out, shape, dtype, device, name="out") -> torch.Tensor:
 def _space(workspace, need: int, device):
     """The caller's workspace, or a new one; None where none is needed.  It is held until the
     call has queued its work."""
-    if need == 0:
-        return None
-    if workspace is None:
-        return _Q.workspace(device, need)
-    if workspace.numel() * workspace.element_size() < need or workspace.device != device:
-        _fail(f"workspace needs {need} bytes on {device}")
-    return workspace
+    return None if need == 0 else _Q._space(workspace, need, device)
 
 
 def _aligned(t: torch.Tensor) -> torch.Tensor:

@@ -141,3 +141,63 @@ def test_threads_on_one_stream(kind):
         t.join()
     torch.cuda.synchronize()
     assert not wrong, wrong
+
+
+def _no_workspaces(need):
+    """Tensors of at least `need` elements that are no workspace of `need` bytes."""
+    room = torch.zeros(2 * need + 64, dtype=torch.uint8, device="cuda")
+    return [room[:1].expand(need), room[:2 * need].view(need, 2)[:, 0], room[:2 * need:2], room[:need - 1],
+            torch.zeros(need, dtype=torch.uint8), bytearray(need), need]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_workspaces_that_are_none(kind):
+    """Expanded and strided views, on the CPU, too small, no tensor: refused before anything is
+    queued.  A view of a larger tensor, and of another type, are workspaces."""
+    Q, g, M = _Q(), _gen(1), 70
+    if kind == "linear":
+        pw, x, xs = Q.pack_channel(_codes(g, 1024, 14336), _scales(g, 1024)), _codes(g, M, 14336), _scales(g, M)
+        need, f = Q.i8_workspace_bytes(M, 1024, 14336), lambda w: Q.linear_i8(x, xs, pw, workspace=w)
+    elif kind == "gated":
+        pw = Q.pack_gated(_codes(g, 320, 14144), _scales(g, 320), _codes(g, 320, 14144), _scales(g, 320))
+        x, xs = _codes(g, M, 14144), _scales(g, M)
+        need, f = Q.i8_workspace_bytes(M, 320, 14144, True), lambda w: Q.gated_i8(x, xs, pw, workspace=w)
+    elif kind == "linear back":
+        pw, dy = Q.pack_channel(_codes(g, 64, 96), _scales(g, 64)), _bf(g, (M, 64))
+        need, f = Q.i8_backward_workspace_bytes(M, 64, 96), lambda w: Q.linear_i8_backward(dy, pw, workspace=w)
+    elif kind == "gated back":
+        pw = Q.pack_gated(_codes(g, 64, 96), _scales(g, 64), _codes(g, 64, 96), _scales(g, 64))
+        dy, raw = _bf(g, (M, 64)), _bf(g, (M, 128))
+        need, f = Q.i8_backward_workspace_bytes(M, 64, 96, True), lambda w: Q.gated_i8_backward(dy, raw, pw, workspace=w)[0]
+    else:
+        r, w0 = _bf(g, (M, 64)), torch.ones(64, device="cuda")
+        need = Q.block_norm_backward_workspace_bytes(M, 64, 0)
+        f = lambda w: Q.block_norm_backward(r, None, r, pre_weight=w0, workspace=w)[0]  # noqa: E731
+    assert need > 0
+    for i, bad in enumerate(_no_workspaces(need)):
+        with pytest.raises(Q.QLinearError):
+            f(bad)
+            pytest.fail(f"workspace {i} was taken")
+    want = f(None)
+    room = torch.full((need + 512,), 7, dtype=torch.uint8, device="cuda")
+    assert torch.equal(f(room[256:256 + need]), want)
+    assert bool((room[:256] == 7).all()) and bool((room[256 + need:] == 7).all())
+    assert torch.equal(f(torch.zeros((need + 7) // 8, dtype=torch.float64, device="cuda")), want)
+
+
+def test_workspaces_that_are_none_of_the_weight_only_products():
+    Q, g = _Q(), _gen(2)
+    N, K, G, M = 1024, 2048, 128, 64
+    codes, s, _ = Q.quantize("int4", torch.randn((N, K), generator=g, device="cuda"), G)
+    pw = Q.pack("int4", N, K, G, codes, s, None)
+    x = _bf(g, (M, K))
+    calls = [(Q.workspace_bytes("int4", M, N, K, G, None, (12, 4)), lambda w: Q.linear(x, pw, schedule=(12, 4), workspace=w)),
+             (Q.a8_workspace_bytes("int4", M, N, K, G), lambda w: Q.linear_a8(x, pw, workspace=w))]
+    for need, f in calls:
+        assert need > 0
+        want = f(None)
+        for i, bad in enumerate(_no_workspaces(need)):
+            with pytest.raises(Q.QLinearError):
+                f(bad)
+                pytest.fail(f"workspace {i} was taken")
+        assert torch.equal(f(torch.zeros(need, dtype=torch.uint8, device="cuda")), want)
