@@ -96,8 +96,11 @@ def _tensor(t, name: str, dtypes, device=None) -> torch.Tensor:
 def _out(out, shape, dtype, device, name="out") -> torch.Tensor:
     if out is None:
         return torch.empty(*shape, dtype=dtype, device=device)   # (shape,) takes 0.35 us longer to parse
-    if out.dtype != dtype or out.shape != shape or not out.is_contiguous() or out.device != device:
+    if (not isinstance(out, torch.Tensor) or out.dtype != dtype or out.shape != shape or not out.is_contiguous()
+            or out.device != device):
         _fail(f"{name} must be a contiguous {tuple(shape)} tensor of {dtype} on {device}")
+    if out.requires_grad:
+        _fail(f"{name} must not require grad: it is written without a record of it")
     return out
 
 

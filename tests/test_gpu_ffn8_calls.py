@@ -201,3 +201,29 @@ def test_workspaces_that_are_none_of_the_weight_only_products():
                 f(bad)
                 pytest.fail(f"workspace {i} was taken")
         assert torch.equal(f(torch.zeros(need, dtype=torch.uint8, device="cuda")), want)
+
+
+# ---- outputs -----------------------------------------------------------------------------
+
+def test_outputs_that_are_none():
+    """Outputs that require grad (a leaf, or what autograd has a history of) and what is no tensor
+    are refused by every operator that takes one."""
+    Q, g, M, N, K = _Q(), _gen(3), 5, 32, 64
+    w, s = _codes(g, N, K), _scales(g, N)
+    cw, gw = Q.pack_channel(w, s), Q.pack_gated(w, s, w, s)
+    x, xs, dy, raw = _codes(g, M, K), _scales(g, M), _bf(g, (M, N)), _bf(g, (M, 2 * N))
+    r, one = _bf(g, (M, K)), torch.ones(K, device="cuda")
+    calls = [(N, lambda o: Q.linear_i8(x, xs, cw, out=o)), (N, lambda o: Q.gated_i8(x, xs, gw, out=o)),
+             (2 * N, lambda o: Q.gated_i8(x, xs, gw, raw=o)), (K, lambda o: Q.linear_i8_backward(dy, cw, out=o)),
+             (K, lambda o: Q.gated_i8_backward(dy, raw, gw, out=o)),
+             (2 * N, lambda o: Q.gated_i8_backward(dy, raw, gw, draw=o)),
+             (K, lambda o: Q.block_norm(r, pre_weight=one, residual_out=o))]
+    for i, (width, f) in enumerate(calls):
+        good = torch.zeros((M, width), dtype=torch.bfloat16, device="cuda")
+        f(good)
+        leaf = torch.zeros((M, width), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+        for bad in (leaf, leaf * 2, good.tolist(), 7):
+            with pytest.raises(Q.QLinearError):
+                f(bad)
+                pytest.fail(f"output {i} was taken")
+        assert bool((leaf == 0).all())
