@@ -231,8 +231,11 @@ def _activations(codes, scales, pw):
     if not shape or shape[-1] != pw.K:
         _fail(f"codes must be [..., {pw.K}]")
     M = codes.numel() // pw.K
-    _need(scales.numel() == M, "scales must hold one value a token")
-    return shape[:-1], M, _aligned(codes), scales.contiguous()
+    lead, given = shape[:-1], scales.shape
+    # one value a token, in the tokens' shape or in a row; another shape would reorder them
+    if given != lead and given != (M,) and given != (*lead, 1):
+        _fail(f"scales must be {tuple(lead)}")
+    return lead, M, _aligned(codes), scales.contiguous()
 
 
 def _bias(bias, n, pw):
@@ -249,7 +252,8 @@ def linear_i8(codes: torch.Tensor, scales: torch.Tensor, pw: ChannelWeight, bias
               workspace: torch.Tensor | None = None) -> torch.Tensor:
     """y[..., N] = (codes . q^T) * scales * channel scales + bias, summed exactly in int32.
 
-    codes int8 [..., K], scales float32 [...], bias bf16 [N]; out_dtype bf16 or float32."""
+    codes int8 [..., K], scales float32 [...] (or one row of them), bias bf16 [N]; out_dtype bf16
+    or float32."""
     _need(isinstance(pw, ChannelWeight), "pw must be a ChannelWeight")
     _need(out_dtype in _DTYPES, "out_dtype must be bfloat16 or float32")
     lead, M, codes, scales = _activations(codes, scales, pw)

@@ -227,3 +227,26 @@ def test_outputs_that_are_none():
                 f(bad)
                 pytest.fail(f"output {i} was taken")
         assert bool((leaf == 0).all())
+
+
+# ---- scales ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_scales_have_the_shape_of_the_tokens(gated):
+    """Scales of the tokens' shape, with a last dimension of one, or in a row; those of another
+    shape with as many values belong to other tokens."""
+    Q, g, N, K = _Q(), _gen(5), 48, 64
+    w, s = _codes(g, N, K), _scales(g, N)
+    pw = Q.pack_gated(w, s, w, s) if gated else Q.pack_channel(w, s)
+    f = Q.gated_i8 if gated else Q.linear_i8
+    x, xs = _codes(g, 6, K), _scales(g, 6, 1.0)
+    want = f(x, xs, pw)
+    shaped = x.view(2, 3, K)
+    for good in (xs.view(2, 3), xs.view(2, 3, 1), xs, xs.view(2, 3).t().contiguous().t()):
+        assert torch.equal(f(shaped, good, pw), want.view(2, 3, N))
+    assert torch.equal(f(x, xs[:, None], pw), want)
+    assert torch.equal(f(x[0], xs[0], pw), want[0]) and torch.equal(f(x[0], xs[:1], pw), want[0])
+    for bad in (xs.view(3, 2), xs.view(3, 2, 1), xs.view(1, 6), xs.view(6, 1), xs[:5], xs.view(2, 3)[:, :2]):
+        with pytest.raises(Q.QLinearError):
+            f(shaped, bad, pw)
+            pytest.fail(f"scales {tuple(bad.shape)} were taken")
