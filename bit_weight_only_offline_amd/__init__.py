@@ -9,6 +9,7 @@ GPU is present, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 
@@ -527,16 +528,19 @@ def grouped_linear(x: torch.Tensor, pe: PackedExperts, tokens_per_expert: torch.
 # ---- INT8-compute path (W4A8 / W8A8): dynamic per-row activation quantisation ----------
 
 def quantize_activations(x: torch.Tensor):
-    """Per-row symmetric INT8 quantisation of bf16 activations [M, K]:
-    -> (codes int8 [M, K], scales float32 [M]), s = amax / 127, q = rint(x / s)."""
+    """Per-row symmetric INT8 quantisation of bf16 activations [..., K]:
+    -> (codes int8 [..., K], scales float32 [...]), s = amax / 127, q = rint(x / s)."""
     if x.requires_grad:
         raise QLinearError("inference-only operator: inputs must not require grad")
-    if x.device.type != "cuda" or x.dtype != torch.bfloat16 or x.dim() != 2:
-        raise QLinearError("x must be a bf16 [M, K] device tensor")
+    if x.device.type != "cuda" or x.dtype != torch.bfloat16 or x.dim() == 0:
+        raise QLinearError("x must be a bf16 [..., K] device tensor")
     x = x.contiguous()
-    M, K = x.shape
-    codes = torch.empty((M, K), dtype=torch.int8, device=x.device)
-    scales = torch.empty((M,), dtype=torch.float32, device=x.device)
+    if x.data_ptr() % 16:
+        x = x.clone()                      # a view may start anywhere
+    K = x.shape[-1]
+    M = math.prod(x.shape[:-1])
+    codes = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     _check(lib().qlinear_quantize_activations(_ptr(x), M, K, _ptr(codes), _ptr(scales), _stream(x.device)),
            "qlinear_quantize_activations")
     return codes, scales

@@ -250,3 +250,35 @@ def test_scales_have_the_shape_of_the_tokens(gated):
         with pytest.raises(Q.QLinearError):
             f(shaped, bad, pw)
             pytest.fail(f"scales {tuple(bad.shape)} were taken")
+
+
+# ---- the chain ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("lead", [(), (1,), (7,), (2, 3), (2, 1, 4), (0,), (2, 0)])
+def test_activations_of_any_shape_through_a_layer(lead):
+    """norm -> gated -> quantisation -> linear -> norm for tokens of any leading shape, and from
+    views: what the same tokens give in a row."""
+    Q, g, C, N = _Q(), _gen(6), 64, 96
+    gw = Q.pack_gated(_codes(g, N, C), _scales(g, N), _codes(g, N, C), _scales(g, N))
+    dw = Q.pack_channel(_codes(g, C, N), _scales(g, C))
+    pre = torch.rand(C, generator=g, device="cuda") + 0.5
+
+    def layer(r):
+        r, (q, s) = Q.block_norm(r, pre_weight=pre, int8=True)
+        h = Q.gated_i8(q, s, gw)
+        codes, scales = Q.quantize_activations(h)
+        y = Q.linear_i8(codes, scales, dw)
+        return (h, codes, scales, y, *Q.block_norm(r, y, pre_weight=pre))
+    r = _bf(g, (*lead, C))
+    M = r.numel() // C
+    got, want = layer(r), layer(r.reshape(M, C))
+    for a, b, width in zip(got, want, ((N,), (N,), (), (C,), (C,), (C,))):
+        assert a.shape == (*lead, *width) and torch.equal(a.reshape(M, *width), b)
+    h = got[0]
+    room = torch.zeros(h.numel() + 3, dtype=torch.bfloat16, device="cuda")
+    room[3:] = h.reshape(-1)
+    wide = torch.zeros((*lead, N + 5), dtype=torch.bfloat16, device="cuda")
+    wide[..., 2:2 + N] = h
+    for view in (room[3:].view(h.shape), wide[..., 2:2 + N]):
+        codes, scales = Q.quantize_activations(view)
+        assert torch.equal(codes, got[1]) and torch.equal(scales, got[2])
