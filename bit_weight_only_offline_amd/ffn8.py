@@ -362,14 +362,15 @@ def _norm_args(residual, y, post_weight, pre_weight, gate, eps):
         if dtype is None:
             dtype = p.dtype
             allowed = (dtype,)
-        if p is gate:
-            gates = 1 if p.dim() == 1 else p.shape[0]
-            if p.dim() not in (1, 2) or p.shape[-1] != C:
-                _fail("gate must be [C] or [B, C]")
-            if gates == 0 or R % gates:
-                _fail("the rows must divide evenly among the gates")
-        elif p.dim() != 1 or len(p) != C:
+    for p in (post_weight, pre_weight):
+        if p is not None and p.shape != (C,):
             _fail("a norm weight must be [C]")
+    if gate is not None:
+        if gate.dim() not in (1, 2) or gate.shape[-1] != C:
+            _fail("gate must be [C] or [B, C]")
+        gates = 1 if gate.dim() == 1 else gate.shape[0]
+        if gates == 0 or R % gates:
+            _fail("the rows must divide evenly among the gates")
     if not eps > 0.0:
         _fail("eps must be positive")
     return R, C, gates, 1 if dtype is None else _DTYPES[dtype]

@@ -282,3 +282,26 @@ def test_activations_of_any_shape_through_a_layer(lead):
     for view in (room[3:].view(h.shape), wide[..., 2:2 + N]):
         codes, scales = Q.quantize_activations(view)
         assert torch.equal(codes, got[1]) and torch.equal(scales, got[2])
+
+
+# ---- norm parameters ---------------------------------------------------------------------
+
+def test_one_tensor_as_gate_and_weight():
+    """One tensor [C] may be several parameters at once; one [B, C] is a gate, and no norm weight
+    even where it is given as the gate too.  Scalars are neither."""
+    Q, g, R, C = _Q(), _gen(7), 6, 32
+    r, y, dx = _bf(g, (R, C)), _bf(g, (R, C)), _bf(g, (R, C))
+    w, both, one = torch.rand(C, device="cuda"), torch.rand((2, C), device="cuda"), torch.tensor(1.0, device="cuda")
+    kw = {"post_weight": w, "pre_weight": w, "gate": w}
+    for a, b in zip(Q.block_norm(r, y, **kw), Q.block_norm(r, y, **{k: v.clone() for k, v in kw.items()})):
+        assert torch.equal(a, b)
+    grads = Q.block_norm_backward(dx, None, r, y, **kw)
+    for a, b in zip(grads, Q.block_norm_backward(dx, None, r, y, **{k: v.clone() for k, v in kw.items()})):
+        assert torch.equal(a, b)
+    for change in ({"post_weight": both, "gate": both}, {"pre_weight": both, "gate": both}, {"post_weight": both},
+                   {"gate": one}, {"post_weight": one}, {"pre_weight": one, "gate": one}, {"gate": both[None]}):
+        bad = {**kw, **change}
+        for f in (lambda: Q.block_norm(r, y, **bad), lambda: Q.block_norm_backward(dx, None, r, y, **bad)):
+            with pytest.raises(Q.QLinearError):
+                f()
+                pytest.fail(f"{sorted(change)} was taken")
