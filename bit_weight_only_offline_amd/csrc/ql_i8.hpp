@@ -22,6 +22,13 @@ namespace ql {
 
 constexpr int I8_CHUNK = 64;
 constexpr int64_t I8_K_MAX = 131071;   // 128 * 128 * K < 2^31: the int32 sums cannot wrap
+// A launch may have fewer than 2^32 threads in a dimension.  Elementwise passes walk their data
+// with a grid of at most 2^30; products refuse the shapes whose tiles no schedule can launch.
+constexpr int64_t LAUNCH_THREADS_MAX = (int64_t(1) << 32) - 1;
+inline dim3 elementwise_grid(int64_t n) {
+    const int64_t blocks = ceil_div(n, 256), most = int64_t(1) << 22;
+    return dim3(unsigned(blocks < most ? blocks : most));
+}
 
 struct I8Layout {
     int64_t N = 0, K = 0;
@@ -56,6 +63,7 @@ struct I8Plan {
     int cfg = 0;
     int mtiles = 1, nblocks = 1;
     int ks = 1, cps = 0;         // splits of the input dimension, chunks per split
+    int64_t threads = 0;         // of the product's grid along x
     size_t ws_bytes = 0;         // int32 partial sums of a split [ks][M][16 ntiles]
 };
 
@@ -105,6 +113,7 @@ struct I8BackArgs {
 struct I8BackPlan {
     int cfg = 0, mtiles = 1, nblocks = 1;
     int ks = 1, nps = 0;
+    int64_t threads = 0;                      // of the product's grid along x
     int64_t Np = 0;                           // N rounded up to eight (gated: to a tile)
     size_t operand_bytes = 0, ex_bytes = 0, ws_bytes = 0;   // the operand, its exponents, partial sums
 };

@@ -17,7 +17,6 @@ ql_status from_hip(hipError_t e) { return e == hipSuccess ? QL_OK : QL_E_HIP; }
 
 // channels past 2^20 would pass the 31-bit row offsets of the backward product
 constexpr int64_t N_MAX = int64_t(1) << 20;
-constexpr int64_t WGS_MAX = (int64_t(1) << 31) - 1;
 
 ql_status check_weight(int64_t N, int64_t K, int gated) {
     if (gated != 0 && gated != 1) return QL_E_ARG;
@@ -42,7 +41,7 @@ ql_status forward(const void *codes, const float *scales, int64_t M, int64_t N, 
     if (!aligned(scales, 4) || !aligned(bias, 2) || !aligned(out, es) || !aligned(raw, 2)) return QL_E_ALIGN;
     const I8Layout L = make_i8_layout(N, K, gated != 0);
     const I8Plan p = make_i8_plan(L, M);
-    if (int64_t(p.mtiles) * p.nblocks > WGS_MAX) return QL_E_SHAPE;
+    if (p.threads > LAUNCH_THREADS_MAX || int64_t(p.mtiles) * p.nblocks > INT32_MAX) return QL_E_SHAPE;
     if (p.ws_bytes) {
         if (!workspace || workspace_bytes < p.ws_bytes) return QL_E_WORKSPACE;
         if (!aligned(workspace, 256)) return QL_E_ALIGN;
@@ -77,7 +76,7 @@ ql_status backward(const void *dy, const void *raw, int64_t M, int64_t N, int64_
         return QL_E_ALIGN;
     const I8Layout L = make_i8_layout(N, K, gated != 0);
     const I8BackPlan p = make_i8_back_plan(L, M);
-    if (int64_t(p.mtiles) * p.nblocks > WGS_MAX || ceil_div(M * p.Np, 256) > WGS_MAX) return QL_E_SHAPE;
+    if (p.threads > LAUNCH_THREADS_MAX || int64_t(p.mtiles) * p.nblocks > INT32_MAX) return QL_E_SHAPE;
     if (p.ws_bytes) {
         if (!workspace || workspace_bytes < p.ws_bytes) return QL_E_WORKSPACE;
         if (!aligned(workspace, 256)) return QL_E_ALIGN;
@@ -92,7 +91,7 @@ bool known_act(ql_gate_act act) { return act == QL_GATE_SILU || act == QL_GATE_G
 ql_status check_norm(int64_t R, int64_t C, int64_t gates, float residual_scale, float eps, ql_dtype r_dtype,
                      ql_dtype p_dtype) {
     if (R < 0 || R >= (int64_t(1) << 31) || C <= 0 || C > NORM_C_MAX) return QL_E_SHAPE;
-    if (gates < 0 || (gates > 1 && R % gates != 0)) return QL_E_SHAPE;
+    if (gates < 0 || gates >= (int64_t(1) << 31) || (gates > 1 && R % gates != 0)) return QL_E_SHAPE;
     if (!isfinite(residual_scale) || !isfinite(eps) || !(eps > 0.0f)) return QL_E_ARG;
     if ((r_dtype != QL_BF16 && r_dtype != QL_F32) || (p_dtype != QL_BF16 && p_dtype != QL_F32)) return QL_E_ARG;
     return QL_OK;

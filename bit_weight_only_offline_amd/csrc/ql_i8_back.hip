@@ -330,17 +330,17 @@ __global__ void __launch_bounds__(64 * BACK_WAVES) i8_back_kernel(I8BackArgs a) 
     }
 }
 
-// Adds the splits' float32 sums in split order and rounds: one thread per four inputs.
+// Adds the splits' float32 sums in split order and rounds: a thread takes four inputs at a time.
 __global__ void __launch_bounds__(256) i8_back_join_kernel(const float *__restrict__ part, uint16_t *__restrict__ dx,
                                                            int64_t n4, int ks) {
-    const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (e >= n4) return;
-    f32x4 t{0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < ks; ++k) {
-        const f32x4 p = reinterpret_cast<const f32x4 *>(part)[int64_t(k) * n4 + e];
-        t += p;
+    for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < n4; e += int64_t(gridDim.x) * 256) {
+        f32x4 t{0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < ks; ++k) {
+            const f32x4 p = reinterpret_cast<const f32x4 *>(part)[int64_t(k) * n4 + e];
+            t += p;
+        }
+        reinterpret_cast<u32x2 *>(dx)[e] = u32x2{pack_bf16(t[0], t[1]), pack_bf16(t[2], t[3])};
     }
-    reinterpret_cast<u32x2 *>(dx)[e] = u32x2{pack_bf16(t[0], t[1]), pack_bf16(t[2], t[3])};
 }
 
 // ---- the operand -----------------------------------------------------------------------
@@ -591,7 +591,7 @@ hipError_t launch_back(const I8BackArgs &a, hipStream_t st) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t n4 = int64_t(a.M) * a.K / 4;
-    hipLaunchKernelGGL(i8_back_join_kernel, dim3(unsigned(ceil_div(n4, 256))), dim3(256), 0, st, a.part, a.dx, n4, a.ks);
+    hipLaunchKernelGGL(i8_back_join_kernel, elementwise_grid(n4), dim3(256), 0, st, a.part, a.dx, n4, a.ks);
     return hipGetLastError();
 }
 
@@ -616,7 +616,8 @@ I8BackPlan make_i8_back_plan(const I8Layout &L, int64_t M) {
     p.nblocks = int(kblocks);
     float best = 0.0f;
     for (int c = 0; c < NUM_BACK_CFGS; ++c) {
-        const int64_t mtiles = ceil_div(M, back_rows(BACK_CFGS[c]));
+        const int64_t mtiles = ceil_div(M, back_rows(BACK_CFGS[c])), threads = mtiles * kblocks * 64 * BACK_WAVES;
+        if (c > 0 && threads > LAUNCH_THREADS_MAX) continue;
         for (int ks : {1, 2, 3, 4, 6, 8, 12, 16}) {
             const int64_t nps = ceil_div(ceil_div(steps, ks), 4) * 4;      // whole groups of four
             if (ks > 1 && (nps < 8 || ceil_div(steps, nps) < ks)) break;
@@ -626,6 +627,7 @@ I8BackPlan make_i8_back_plan(const I8Layout &L, int64_t M) {
                 best = us;
                 p.cfg = c;
                 p.mtiles = int(mtiles);
+                p.threads = threads;
                 p.ks = ks;
                 p.nps = int(nps);
             }

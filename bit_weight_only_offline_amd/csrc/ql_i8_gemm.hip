@@ -653,20 +653,20 @@ __global__ void __launch_bounds__(64 * WM * WN) i8_wide_kernel(I8Args a) {
     }
 }
 
-// Adds the splits' int32 sums and finishes: one thread per four channels of one token.
+// Adds the splits' int32 sums and finishes: a thread takes four channels of one token at a time.
 template <bool GATED>
 __global__ void __launch_bounds__(256) i8_join_kernel(I8Args a) {
     const int per_row = (GATED ? a.ntiles / 2 : a.ntiles) * 4;
-    const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (e >= int64_t(a.M) * per_row) return;
-    const int m = int(e / per_row), q = int(e % per_row), tile = q >> 2, at = 4 * (q & 3);
     const int64_t width = int64_t(a.ntiles) * TILE_N;
-    emit<GATED>(a, m, tile, at, [&](int t) {
-        i32x4 s{0, 0, 0, 0};
-        for (int k = 0; k < a.ks; ++k)
-            s += *reinterpret_cast<const i32x4 *>(a.part + (int64_t(k) * a.M + m) * width + int64_t(t) * TILE_N + at);
-        return s;
-    });
+    for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < int64_t(a.M) * per_row; e += int64_t(gridDim.x) * 256) {
+        const int m = int(e / per_row), q = int(e % per_row), tile = q >> 2, at = 4 * (q & 3);
+        emit<GATED>(a, m, tile, at, [&](int t) {
+            i32x4 s{0, 0, 0, 0};
+            for (int k = 0; k < a.ks; ++k)
+                s += *reinterpret_cast<const i32x4 *>(a.part + (int64_t(k) * a.M + m) * width + int64_t(t) * TILE_N + at);
+            return s;
+        });
+    }
 }
 
 constexpr I8Cfg CFGS[] = {
@@ -711,7 +711,7 @@ hipError_t launch_rows(const I8Args &a, hipStream_t st) {
 template <bool GATED>
 hipError_t launch_join(const I8Args &a, hipStream_t st) {
     const int64_t units = int64_t(a.M) * (GATED ? a.ntiles / 2 : a.ntiles) * 4;
-    hipLaunchKernelGGL(i8_join_kernel<GATED>, dim3(unsigned(ceil_div(units, 256))), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(i8_join_kernel<GATED>, elementwise_grid(units), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
@@ -788,6 +788,10 @@ I8Plan make_i8_plan(const I8Layout &L, int64_t M) {
         mt = ceil_div(M, 16 * t.MT * t.WM);
         nb = ceil_div(L.ntiles, t.NT * t.WN);
     };
+    auto threads = [](int c, int64_t mt, int64_t nb) {
+        const I8Cfg &t = CFGS[c];
+        return (t.kind == 2 ? std::min<int64_t>(mt * nb, WIDE_WGS) : t.kind == 0 ? nb : mt * nb) * 64 * t.WK * t.WM * t.WN;
+    };
     int64_t mt, nb;
     if (M <= 16) {
         p.cfg = !L.gated && L.ntiles <= 512 ? 0 : 1;
@@ -795,6 +799,7 @@ I8Plan make_i8_plan(const I8Layout &L, int64_t M) {
         float best = 0.0f;
         for (int c = M <= 32 ? 1 : WIDE; c < NUM_CFGS; ++c) {
             blocks(c, mt, nb);
+            if (threads(c, mt, nb) > LAUNCH_THREADS_MAX) continue;       // the large tiles always fit
             const int step = 2 * CFGS[c].WK;                             // chunks of a stage
             for (int ks : {1, 2, 3, 4, 6, 8}) {
                 const int64_t cps = ks == 1 ? L.kchunks : ceil_div(ceil_div(L.kchunks, ks), step) * step;
@@ -817,6 +822,7 @@ I8Plan make_i8_plan(const I8Layout &L, int64_t M) {
     blocks(p.cfg, mt, nb);
     p.mtiles = int(mt);
     p.nblocks = int(nb);
+    p.threads = threads(p.cfg, mt, nb);
     if (p.ks > 1) p.ws_bytes = round256(size_t(p.ks) * size_t(M) * size_t(L.ntiles) * TILE_N * 4);
     return p;
 }

@@ -406,20 +406,22 @@ __global__ void __launch_bounds__(TMAX, NV <= (V == 8 ? 1 : 4) ? 4 : 1) block_no
 __global__ void __launch_bounds__(1024) column_sum_kernel(ColumnSums a) {
     __shared__ float red[16][64];
     const int q = blockIdx.z, lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
-    if (blockIdx.y >= unsigned(a.outs[q])) return;
     const int64_t c = int64_t(blockIdx.x) * 64 + lane;
-    const float *p = a.part[q] + int64_t(blockIdx.y) * a.count[q] * a.C;
-    float s = 0.0f;
-    if (c < a.C)
+    for (int64_t b = blockIdx.y; b < a.outs[q]; b += gridDim.y) {
+        const float *p = a.part[q] + b * a.count[q] * a.C;
+        float s = 0.0f;
+        if (c < a.C)
 #pragma unroll 8
-        for (int g = grp; g < a.count[q]; g += 16) s += p[int64_t(g) * a.C + c];
-    red[grp][lane] = s;
-    __syncthreads();
-    if (grp == 0 && c < a.C) {
-        float t = red[0][lane];
+            for (int g = grp; g < a.count[q]; g += 16) s += p[int64_t(g) * a.C + c];
+        red[grp][lane] = s;
+        __syncthreads();
+        if (grp == 0 && c < a.C) {
+            float t = red[0][lane];
 #pragma unroll
-        for (int g = 1; g < 16; ++g) t += red[g][lane];
-        a.out[q][int64_t(blockIdx.y) * a.C + c] = t;
+            for (int g = 1; g < 16; ++g) t += red[g][lane];
+            a.out[q][b * a.C + c] = t;
+        }
+        __syncthreads();
     }
 }
 
@@ -541,7 +543,7 @@ hipError_t launch_block_norm_back(const NormBackArgs &args, const NormBackPlan &
     if (has_gate && p.cpb != 1) add(dgate, a.part_gate, p.cpb, gates);
     if (n == 0) return hipSuccess;
     c.C = a.C;
-    hipLaunchKernelGGL(column_sum_kernel, dim3(unsigned(ceil_div(a.C, 64)), unsigned(outs), unsigned(n)), dim3(1024), 0,
+    hipLaunchKernelGGL(column_sum_kernel, dim3(unsigned(ceil_div(a.C, 64)), unsigned(std::min(outs, 65535)), unsigned(n)), dim3(1024), 0,
                        st, c);
     return hipGetLastError();
 }

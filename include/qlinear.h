@@ -387,7 +387,9 @@ ql_status qlinear_grouped_forward(const void *x, int64_t T, const int32_t *token
  * 8-bit feed-forward operators.  Activations are int8 codes [M, K] with one float32 scale a
  * token (qlinear_quantize_activations() and qlinear_block_norm() make them), weights int8
  * codes [N, K] with one float32 scale a channel, K a multiple of 32 and at most 131071 (so
- * that the int32 sums are exact for all codes in -128 .. 127), N at most 2^20.
+ * that the int32 sums are exact for all codes in -128 .. 127), N at most 2^20.  M below 2^31;
+ * QL_E_SHAPE also where no grid holds a product's tiles (256 rows by 256 inputs each, 2^23 of
+ * them, for the backward products).
  *
  * qlinear_i8_pack() lays a weight out once for every product below; a gated weight holds
  * two weights of the same shape, up (codes, scales) and gate (gate_codes, gate_scales),
