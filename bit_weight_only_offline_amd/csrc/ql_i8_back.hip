@@ -39,6 +39,7 @@
 #include "ql_gemm_lds.hpp"
 #include "ql_i8.hpp"
 #include "ql_launch.hpp"
+#include "ql_lds_limit.hpp"
 
 namespace ql {
 namespace {
@@ -577,18 +578,18 @@ hipError_t launch_back(const I8BackArgs &a, hipStream_t st) {
     const dim3 grid(unsigned(a.mtiles * a.nblocks), unsigned(a.ks)), block(64 * BACK_WAVES);
     if (a.ks == 1) {
         auto kern = i8_back_kernel<t.WM, t.WN, t.MT, t.NT, false>;
-        static const hipError_t set =
-            hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (set != hipSuccess) return set;
+        static LdsLimit limit;
+        const hipError_t e = limit.raise((const void *)kern, lds);
+        if (e != hipSuccess) return e;
         hipLaunchKernelGGL(kern, grid, block, lds, st, a);
         return hipGetLastError();
     }
     auto kern = i8_back_kernel<t.WM, t.WN, t.MT, t.NT, true>;
-    static const hipError_t set =
-        hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    if (set != hipSuccess) return set;
+    static LdsLimit limit;
+    hipError_t e = limit.raise((const void *)kern, lds);
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, grid, block, lds, st, a);
-    const hipError_t e = hipGetLastError();
+    e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t n4 = int64_t(a.M) * a.K / 4;
     hipLaunchKernelGGL(i8_back_join_kernel, elementwise_grid(n4), dim3(256), 0, st, a.part, a.dx, n4, a.ks);

@@ -19,6 +19,7 @@
 #include "ql_gemm_lds.hpp"
 #include "ql_i8.hpp"
 #include "ql_launch.hpp"
+#include "ql_lds_limit.hpp"
 
 namespace ql {
 namespace {
@@ -692,18 +693,14 @@ constexpr float JOIN_US = 5.0f, JOIN_BYTES_PER_US = 4.0e6f;
 constexpr int ROWS_U = 4;
 constexpr int WIDE_WGS = 256;    // workgroups that walk the large tiles: one a compute unit
 
-template <typename F>
-hipError_t allow_lds(F kern, size_t lds) {
-    return hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
-}
-
 template <int I, bool GATED>
 hipError_t launch_rows(const I8Args &a, hipStream_t st) {
     constexpr I8Cfg t = CFGS[I];
     constexpr size_t lds = size_t(t.WK) * t.NT * t.MT * 1024;
     auto kern = i8_rows_kernel<t.MT, t.NT, t.WK, ROWS_U, GATED>;
-    static const hipError_t set = allow_lds(kern, lds);
-    if (set != hipSuccess) return set;
+    static LdsLimit limit;
+    const hipError_t e = limit.raise((const void *)kern, int(lds));
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, dim3(unsigned(a.nblocks), unsigned(a.mtiles)), dim3(64 * t.WK), lds, st, a);
     return hipGetLastError();
 }
@@ -724,8 +721,9 @@ hipError_t launch_wide(const I8Args &a, hipStream_t st) {
     constexpr int MT = GATED ? t.MT / 2 : t.MT, NT = GATED ? 2 * t.NT : t.NT;
     constexpr size_t lds = wide_lds<WM, WN, MT, NT, GATED>();
     auto kern = i8_wide_kernel<WM, WN, MT, NT, GATED>;
-    static const hipError_t set = allow_lds(kern, lds);
-    if (set != hipSuccess) return set;
+    static LdsLimit limit;
+    const hipError_t e = limit.raise((const void *)kern, int(lds));
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, dim3(unsigned(std::min<int64_t>(int64_t(a.mtiles) * a.nblocks, WIDE_WGS))),
                        dim3(64 * WM * WN), lds, st, a);
     return hipGetLastError();
@@ -738,8 +736,9 @@ hipError_t launch_tiles_of(const I8Args &a, hipStream_t st) {
     constexpr int NT = GATED && t.NT == 1 ? 2 : t.NT, WN = t.WN * t.NT / NT;
     constexpr size_t lds = tile_lds<WN, t.WK, t.MT, NT, t.S, GATED>();
     auto kern = i8_tile_kernel<WN, t.WK, t.MT, NT, t.S, GATED, SPLIT>;
-    static const hipError_t set = allow_lds(kern, lds);
-    if (set != hipSuccess) return set;
+    static LdsLimit limit;
+    const hipError_t e = limit.raise((const void *)kern, int(lds));
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, dim3(unsigned(a.mtiles * a.nblocks), unsigned(a.ks)), dim3(64 * WN * t.WK), lds, st, a);
     return hipGetLastError();
 }
