@@ -136,6 +136,23 @@ ql_status qlinear_i8_unpack(int64_t N, int64_t K, const void *packed_w, const vo
                                      scales, static_cast<int8_t *>(gate_codes), gate_scales, (hipStream_t)stream));
 }
 
+ql_status qlinear_i8_default_schedule(int64_t M, int64_t N, int64_t K, int gated, int backward, ql_schedule *out) {
+    if (!out || (backward != 0 && backward != 1)) return QL_E_ARG;
+    ql_status st = check_weight(N, K, gated);
+    if (st == QL_OK) st = check_rows(M);
+    if (st != QL_OK) return st;
+    if (M == 0) return QL_E_SHAPE;
+    const I8Layout L = make_i8_layout(N, K, gated != 0);
+    if (backward) {
+        const I8BackPlan p = make_i8_back_plan(L, M);
+        *out = ql_schedule{p.cfg, p.ks};
+    } else {
+        const I8Plan p = make_i8_plan(L, M);
+        *out = ql_schedule{p.cfg, p.ks};
+    }
+    return QL_OK;
+}
+
 ql_status qlinear_i8_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated, size_t *bytes) {
     if (!bytes) return QL_E_ARG;
     ql_status st = check_weight(N, K, gated);

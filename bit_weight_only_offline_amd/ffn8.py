@@ -24,7 +24,7 @@ import bit_weight_only_offline_amd as _Q
 
 __all__ = [
     "ChannelWeight", "GatedWeight", "pack_channel", "unpack_channel", "pack_gated", "unpack_gated", "GATE_ACTS",
-    "i8_packed_bytes", "i8_workspace_bytes", "i8_backward_workspace_bytes", "linear_i8", "linear_i8_backward",
+    "i8_packed_bytes", "i8_default_schedule", "i8_workspace_bytes", "i8_backward_workspace_bytes", "linear_i8", "linear_i8_backward",
     "gated_i8", "gated_i8_backward", "block_norm_backward_workspace_bytes", "block_norm", "block_norm_backward",
 ]
 
@@ -40,6 +40,7 @@ def bind(L: ctypes.CDLL) -> None:
         "qlinear_i8_packed_bytes": [i64, i64, ci, psz, psz],
         "qlinear_i8_pack": [i64, i64, vp, vp, vp, vp, vp, vp, vp],
         "qlinear_i8_unpack": [i64, i64, vp, vp, vp, vp, vp, vp, vp],
+        "qlinear_i8_default_schedule": [i64, i64, i64, ci, ci, ctypes.POINTER(_Q.Schedule)],
         "qlinear_i8_workspace_bytes": [i64, i64, i64, ci, psz],
         "qlinear_i8_backward_workspace_bytes": [i64, i64, i64, ci, psz],
         "qlinear_i8_forward": [vp, vp, i64, i64, i64, vp, vp, vp, vp, ci, vp, sz, vp],
@@ -130,6 +131,14 @@ def i8_packed_bytes(N: int, K: int, gated: bool = False):
     _Q._check(_Q.lib().qlinear_i8_packed_bytes(N, K, int(gated), ctypes.byref(w), ctypes.byref(s)),
               "qlinear_i8_packed_bytes")
     return w.value, s.value
+
+
+def i8_default_schedule(M: int, N: int, K: int, gated: bool = False, backward: bool = False):
+    """The Schedule (tile, splits) that a product, or its backward pass, takes at these sizes."""
+    s = _Q.Schedule()
+    _Q._check(_Q.lib().qlinear_i8_default_schedule(M, N, K, int(gated), int(backward), ctypes.byref(s)),
+              "qlinear_i8_default_schedule")
+    return s
 
 
 def i8_workspace_bytes(M: int, N: int, K: int, gated: bool = False) -> int:

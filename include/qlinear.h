@@ -404,6 +404,15 @@ ql_status qlinear_i8_unpack(int64_t N, int64_t K, const void *packed_w, const vo
                             float *scales, void *gate_codes, float *gate_scales, void *stream);
 
 /*
+ * The schedule of a product below (host-only): backward 0 or 1, splits of the dimension that is
+ * summed over, and tile (rows x outputs of a workgroup):
+ *   forward   0: 16 x 16, 1: 16 x 32, 2: 256 x 256, 3: 128 x 256, 4: 128 x 128, 5: 64 x 128,
+ *             6: 64 x 64, 7: 32 x 64 (gated: half as many outputs, and never 0)
+ *   backward  0: 256, 1: 128, 2: 64, 3: 16 rows, all x 256
+ */
+ql_status qlinear_i8_default_schedule(int64_t M, int64_t N, int64_t K, int gated, int backward, ql_schedule *out);
+
+/*
  * y[m, n] = scales[m] s[n] sum_k codes[m, k] q[n, k] + bias[n]
  *   codes      int8 [M, K] row-major, 16-byte aligned     scales  float32 [M]
  *   bias       bf16 [N] or NULL                           out     [M, N] bf16 or float32

@@ -46,3 +46,22 @@ def test_no_schedule_past_the_limit(L, gated):
         for N in (1, 16, 40, 300):
             for f in (L.qlinear_i8_workspace_bytes, L.qlinear_i8_backward_workspace_bytes):
                 assert f(M, N, 32, gated, ctypes.byref(n)) == OK
+
+
+def test_default_schedule(L):
+    import bit_weight_only_offline_amd as Q
+    s = Q.i8_default_schedule(1, 4096, 14336)
+    assert (s.tile, s.splits) == (0, 1)
+    assert Q.i8_default_schedule(4, 14336, 4096, gated=True).tile == 1
+    s = Q.i8_default_schedule(2048, 14336, 4096, gated=True, backward=True)
+    assert (s.tile, s.splits) == (0, 2)
+    out = Q.Schedule()
+    f = L.qlinear_i8_default_schedule
+    assert f(4, 64, 64, 0, 2, ctypes.byref(out)) == ARG and f(4, 64, 64, 2, 0, ctypes.byref(out)) == ARG
+    assert f(4, 64, 64, 0, 0, None) == ARG
+    assert f(0, 64, 64, 0, 0, ctypes.byref(out)) == SHAPE and f(4, 64, 40, 0, 1, ctypes.byref(out)) == SHAPE
+    for gated in (0, 1):
+        for M in (1, 16, 17, 100, 3000):                      # a workspace exactly where the forward splits
+            n = ctypes.c_size_t()
+            assert L.qlinear_i8_workspace_bytes(M, 4099, 12000, gated, ctypes.byref(n)) == OK
+            assert f(M, 4099, 12000, gated, 0, ctypes.byref(out)) == OK and (n.value > 0) == (out.splits > 1)

@@ -184,3 +184,35 @@ def test_rows_of_every_length(gated, M, N, K):
     else:
         dx, dv = Q.linear_i8_backward(dy, pw), dy.to(D)
     assert torch.equal(dx, torch.mm(dv, w).float().bfloat16())
+
+
+# Each schedule (tile, split or whole), at row counts off every tile and odd channel counts;
+# besides the shortest of each, contractions of a hundred steps and more.
+SCHEDULES = [
+    (False, 533, 617, 13088, 0, False), (False, 2047, 4093, 14336, 0, False), (False, 131, 4023, 10816, 0, True),
+    (False, 2741, 601, 1312, 1, False), (False, 333, 4099, 4096, 1, True), (False, 1031, 4091, 4096, 1, False),
+    (False, 2699, 1283, 64, 1, True), (False, 2081, 601, 288, 2, False), (False, 1035, 769, 64, 2, True),
+    (False, 3, 601, 64, 3, False), (False, 1, 641, 64, 3, True), (False, 13, 4091, 14336, 3, True),
+    (True, 661, 603, 10880, 0, False), (True, 2047, 14331, 4096, 0, True), (True, 2711, 4935, 64, 0, True),
+    (True, 3301, 603, 1056, 1, False), (True, 2691, 645, 64, 1, True), (True, 205, 603, 4928, 2, False),
+    (True, 673, 653, 64, 2, True), (True, 3647, 605, 96, 3, False), (True, 1, 601, 64, 3, True),
+    (True, 77, 5003, 2080, 1, True)]
+
+
+@pytest.mark.parametrize("gated,M,N,K,tile,split", SCHEDULES)
+def test_every_schedule(gated, M, N, K, tile, split):
+    Q, g = _Q(), _gen(M + N)
+    s = Q.i8_default_schedule(M, N, K, gated, backward=True)
+    assert (s.tile, s.splits > 1) == (tile, split)
+    pw, w = _weights(g, N, K, gated, _eleven_bits, -8, 8)
+    dy = _signs(g, (M, N))
+    print("backward, schedule", gated, M, N, K, s.tile, s.splits, flush=True)
+    if gated:
+        raw = torch.full((M, 2 * N), 32.0, dtype=torch.bfloat16, device="cuda")
+        raw[:, :N] *= _signs(g, (M, N))
+        dx, draw = Q.gated_i8_backward(dy, raw, pw)
+        dv = torch.cat([32 * dy.to(D), dy.to(D) * raw[:, :N].to(D)], 1)
+        assert torch.equal(draw.to(D), dv)
+    else:
+        dx, dv = Q.linear_i8_backward(dy, pw), dy.to(D)
+    assert torch.equal(dx, torch.mm(dv, w).float().bfloat16())
