@@ -19,8 +19,9 @@ enum : int { GATE_SILU = 0, GATE_GELU = 1 };
 constexpr float GELU_A = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float GELU_B = 0.044715f;
 
-// 1 / (1 + exp(-z)): the hardware exponential and reciprocal, each within about 1 ulp
-// (the results are rounded to bf16, or compared at float32 tolerances far above that)
+// 1 / (1 + exp(-z)): the hardware's exponential of two and reciprocal, each within about 1 ulp.
+// The exponent z log2(e) is rounded, which for negative z is |z| 2^-24 of the result; the roundings
+// of z itself, from the float32 sum and scales, come to as much and more whatever the exponential.
 __device__ inline float logistic(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
 __device__ inline float gate_clamp(float g) { return g > 1e4f ? 1e4f : (g < -1e4f ? -1e4f : g); }

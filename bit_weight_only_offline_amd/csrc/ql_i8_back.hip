@@ -23,13 +23,13 @@
 // multiplication and a rounding for every code in the inner loop, where decoding is what
 // keeps the matrix cores waiting.)
 //
-// From memory, 2048 x 4096 x 14336 takes 216 us: 10 for the operand and 206 for the product,
-// 1.17 PFLOP/s on 448 tiles, 1.75 rounds of the 256 compute units.  Gated 2048 x 14336 x 4096
-// takes 475: 77 for du, dg and the operand (411 MB, memory-bound), 385 for the product, 1.25
-// PFLOP/s in two splits on all compute units at once, 13 to join them.  The matrix cores are
-// busy for 63% of the cycles, at 2.18 GHz; power bounds them rather than decoding, which takes 6
-// instructions for four codes (11 for bf16, at the same times): with all codes zero the call
-// takes 188 us where it takes 207 with random ones.
+// From memory, 2048 x 4096 x 14336 takes 208 to 217 us between cards: 10 for the operand and 198
+// to 206 for the product, 1.17 to 1.21 PFLOP/s on 448 tiles, 1.75 rounds of the 256 compute units.
+// Gated 2048 x 14336 x 4096 takes 467 to 476: 77 for du, dg and the operand (411 MB, memory-bound),
+// 376 to 385 for the product, 1.25 to 1.28 PFLOP/s in two splits on all compute units at once, 13 to
+// join them.  The matrix cores are busy for 63% of the cycles, at 2.18 GHz; power bounds them rather
+// than decoding, which takes 6 instructions for four codes (11 for bf16, at the same times): with
+// all codes zero the call takes 188 us where it takes 201 to 207 with random ones.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

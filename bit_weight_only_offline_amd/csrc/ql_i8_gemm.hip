@@ -778,7 +778,8 @@ hipError_t launch_any(int cfg, const I8Args &a, hipStream_t st) {
 // 32 to 128 x 8192 x 8192, 333 x 5008 x 4128, 1500 x 3008 x 2048, 2000 x 8192 x 256, 8192 x 1024 x
 // 512 and 2100 x 4200 x 224, and gated at 20 to 4096 x 14336 x 4096, 77 x 5003 x 2080, 100 and 700
 // x 2000 x 4096, 1000 x 8192 x 2048 and 1500 x 3000 x 2048, its choice was the fastest or within
-// 8% of it.
+// 8% of it.  The rates are of weights that do not wait for memory: for 17 to 32 rows of wide weights
+// (28672 channels) the estimates are below the time of reading the weight once.
 I8Plan make_i8_plan(const I8Layout &L, int64_t M) {
     I8Plan p;
     p.cps = int(L.kchunks);
