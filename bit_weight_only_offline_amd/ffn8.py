@@ -241,9 +241,12 @@ def _activations(codes, scales, pw):
         _fail(f"codes must be [..., {pw.K}]")
     M = codes.numel() // pw.K
     lead, given = shape[:-1], scales.shape
-    # one value a token, in the tokens' shape or in a row; another shape would reorder them
-    if given != lead and given != (M,) and given != (*lead, 1):
-        _fail(f"scales must be {tuple(lead)}")
+    # one value a token, in the tokens' shape or in a row, ones aside; another shape as large holds
+    # them in another order
+    if given != lead:
+        long = [d for d in given if d != 1]
+        if long != [d for d in lead if d != 1] and long != ([M] if M != 1 else []):
+            _fail(f"scales must be {tuple(lead)}")
     return lead, M, _aligned(codes), scales.contiguous()
 
 

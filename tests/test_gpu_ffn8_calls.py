@@ -233,7 +233,7 @@ def test_outputs_that_are_none():
 
 @pytest.mark.parametrize("gated", [False, True])
 def test_scales_have_the_shape_of_the_tokens(gated):
-    """Scales of the tokens' shape, with a last dimension of one, or in a row; those of another
+    """Scales of the tokens' shape or in a row, with dimensions of one anywhere; those of another
     shape with as many values belong to other tokens."""
     Q, g, N, K = _Q(), _gen(5), 48, 64
     w, s = _codes(g, N, K), _scales(g, N)
@@ -242,11 +242,14 @@ def test_scales_have_the_shape_of_the_tokens(gated):
     x, xs = _codes(g, 6, K), _scales(g, 6, 1.0)
     want = f(x, xs, pw)
     shaped = x.view(2, 3, K)
-    for good in (xs.view(2, 3), xs.view(2, 3, 1), xs, xs.view(2, 3).t().contiguous().t()):
+    for good in (xs.view(2, 3), xs.view(2, 3, 1), xs, xs.view(2, 3).t().contiguous().t(), xs.view(1, 6), xs.view(6, 1),
+                 xs.view(2, 1, 3)):
         assert torch.equal(f(shaped, good, pw), want.view(2, 3, N))
     assert torch.equal(f(x, xs[:, None], pw), want)
     assert torch.equal(f(x[0], xs[0], pw), want[0]) and torch.equal(f(x[0], xs[:1], pw), want[0])
-    for bad in (xs.view(3, 2), xs.view(3, 2, 1), xs.view(1, 6), xs.view(6, 1), xs[:5], xs.view(2, 3)[:, :2]):
+    assert torch.equal(f(x[:1], xs[0], pw), want[:1]) and f(x[:0], xs[:0], pw).shape == (0, N)
+    assert f(x[:0].view(2, 0, K), xs[:0], pw).shape == (2, 0, N)
+    for bad in (xs.view(3, 2), xs.view(3, 2, 1), xs.view(1, 3, 2), xs[:5], xs[:1], xs[0], xs.view(2, 3)[:, :2]):
         with pytest.raises(Q.QLinearError):
             f(shaped, bad, pw)
             pytest.fail(f"scales {tuple(bad.shape)} were taken")
