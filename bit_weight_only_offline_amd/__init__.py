@@ -100,6 +100,7 @@ def lib() -> ctypes.CDLL:
         L.qlinear_forward_ex.argtypes = [vp, i64, i64, i64, vp, vp, vp, ci, ci, ci, vp, ci, vp, ci, vp, sz,
                                          ctypes.POINTER(Schedule), vp]
         ffn8.bind(L)
+        moe8.bind(L)
         _lib = L
     return _lib
 
@@ -602,3 +603,11 @@ from . import ffn8  # noqa: E402
 from .ffn8 import *  # noqa: E402,F401,F403
 
 __all__ += ffn8.__all__
+
+
+# ---- mixture-of-experts layers in 8-bit floating point -----------------------------------
+
+from . import moe8  # noqa: E402
+from .moe8 import *  # noqa: E402,F401,F403
+
+__all__ += moe8.__all__

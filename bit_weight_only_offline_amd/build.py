@@ -34,6 +34,11 @@ SOURCES = [   # slowest first, so the parallel build starts them first
     "ql_norm.hip",
     "ql_i8_pack.hip",
     "ql_i8_api.hip",
+    "ql_f8_gemm.hip",
+    "ql_f8_back.hip",
+    "ql_f8_quant.hip",
+    "ql_experts.hip",
+    "ql_f8_api.hip",
 ]
 
 ARCH = "gfx950"
@@ -57,6 +62,7 @@ FLAGS = [
 # bf16 tile kernels measured the same or slower with it, so they keep the default.
 SOURCE_FLAGS = {
     "ql_gemm_a8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "ql_f8_back.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

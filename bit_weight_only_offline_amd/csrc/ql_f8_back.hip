@@ -1,0 +1,367 @@
+// Backward products through frozen block-scaled e4m3 weights, plain or over experts.
+//
+//   dx[m, k] = sum over channel blocks b of ws[b, k / 128] (sum over n in b of dy[m, n] w[n, k])
+//
+// dy is bf16, and an e4m3 code is exact in bf16: the products go through the bf16 matrix cores without
+// rounding either, and float32 holds the sums.  The scale of a block multiplies what 128 channels have summed
+// to.  Rather than a second set of sums, which registers have no room for, the running sums are kept in
+// units of the current block's scale: between two blocks they are multiplied by the ratio of the scales, and
+// at the end by the last.  Powers of two go into the codes' conversion, exactly, so the ratios lie
+// between 1/2 and 2 and cannot overflow.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "ql_f8_device.hpp"
+#include "ql_gemm_lds.hpp"
+#include "ql_launch.hpp"
+#include "ql_lds_limit.hpp"
+
+namespace ql {
+namespace {
+
+constexpr uint32_t OUT_OF_RANGE = 0x80000000u;
+
+__device__ inline f32x4 mma(const u32x4 &a, const u32x4 &b, const f32x4 &c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// A block's scale as mantissa and power of two.  Scales below float32's normal range keep the
+// least power and a smaller mantissa; NaN and infinity are mantissas.
+struct Scale {
+    float mantissa, power;
+};
+__device__ inline Scale split_scale(float s) {
+    const uint32_t b = __float_as_uint(s), e = (b >> 23) & 0xFFu;
+    if (e == 0xFFu) return Scale{s, 1.0f};
+    if (e == 0u) return Scale{s * 8.507059173023462e37f, 1.1754943508222875e-38f};          // 2^126, 2^-126
+    return Scale{__uint_as_float((b & 0x807FFFFFu) | 0x3F800000u), __uint_as_float(e << 23)};
+}
+
+// Two codes as bf16 times a power of two.
+template <bool HI>
+__device__ inline uint32_t widen2(uint32_t codes, float power) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, power, HI));
+}
+
+// Workgroup: WM x WN wavefronts, each 16 MT tokens x 64 inputs; S stages of 64 channels in LDS.
+//
+// Weight.  The operand of inputs (the A operand) needs eight channels of one input in a lane, packed tiles
+// hold sixteen inputs of one channel.  A stage's 64 x 64 codes of a wavefront column lie in LDS as rows of 64
+// bytes, the row of channel 8 p + q of a step of 32 at 4 q + p, so that lane (c, g) reads inputs 4 c .. 4 c +
+// 3 of channel 8 g + q in one word, 64 words in a row over the lanes: no bank is hit twice.  Eight such words are
+// four operands, of inputs 4 c + j for j = 0 .. 3, after eight byte permutes and sixteen conversions.  Their sums
+// leave a lane with sixteen consecutive inputs of a token, 32 bytes of bf16, which are stored as they are.
+//
+// Gradients.  128-byte runs of the rows, their 16-byte pieces swizzled; the B operand.
+template <int WM, int WN, int MT, int S>
+constexpr int back_lds() { return S * (16 * MT * WM * 128 + WN * 4096) + (2 * MT * WM < WM * WN ? 1024 : 0); }
+
+template <int WM, int WN, int MT, int S, bool SPLIT>
+__global__ void __launch_bounds__(64 * WM * WN) f8_back_kernel(F8BackArgs a) {
+    constexpr int W = WM * WN, MP = 16 * MT * WM, KP = 64 * WN;
+    constexpr int X_BYTES = MP * 128, STAGE = X_BYTES + WN * 4096;
+    constexpr int XL = MP / 8, WL = 4 * WN;                // 1 KiB loads of a stage
+    constexpr int XLW = (XL + W - 1) / W, WLW = WL / W, LOADS = XLW + WLW;
+    static_assert(WL % W == 0 && (XL % W == 0 || XL < W), "every wavefront issues the same loads");
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wv / WN, wn = wv % WN;
+    const int g = lane >> 4, c = lane & 15;
+
+    // as in the forward product: runs of the tile order to each XCD, bands of eight row blocks
+    RowBlock rb;
+    int mtiles = a.mtiles;
+    if (a.r.counts) find_rows(a.r, MP, -1, lane, rb, mtiles);
+    const int tiles = mtiles * a.nblocks;
+    const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
+    const int q8 = tiles >> 3, r8 = tiles & 7;
+    if (idx >= q8 + (xcd < r8 ? 1 : 0)) return;
+    const int lin = xcd * q8 + min(xcd, r8) + idx;
+    const int band = lin / (8 * a.nblocks), in_band = lin - band * 8 * a.nblocks;
+    const int band_rows = min(8, mtiles - 8 * band);
+    find_rows(a.r, MP, 8 * band + in_band % band_rows, lane, rb, mtiles);
+    const int k0 = in_band / band_rows * KP;               // first input of the workgroup
+
+    // channels nb0 * 128 .. in stages of 64
+    const int nb0 = SPLIT ? int(blockIdx.y) * a.bps : 0;
+    const int nbs = SPLIT ? min(a.nbs - nb0, a.bps) : a.nbs;
+    const int n_end = min(a.N, (nb0 + nbs) * F8_BLOCK);
+    const int nst = (n_end - nb0 * F8_BLOCK + 63) / 64;
+
+    const __amdgpu_buffer_rsrc_t xr =
+        make_uniform_rsrc(a.dy + int64_t(rb.first) * a.ldy, uint32_t(rb.count) * uint32_t(a.ldy) * 2u);
+    const uint8_t *const w = a.w + uint64_t(rb.expert) * a.w_stride;
+    const float *const ws = a.ws + (int64_t(rb.expert) * a.nbs + nb0) * a.kblocks;
+    const int kb = min((k0 + 64 * wn) / F8_BLOCK, a.kblocks - 1);
+
+    uint32_t x_off[XLW];
+    int x_left[XLW];                                       // channels from the piece to the row's end
+#pragma unroll
+    for (int q = 0; q < XLW; ++q) {
+        const int row = (wv + W * q) * 8 + (lane >> 3), piece = (lane & 7) ^ ((row >> 1) & 7);
+        x_off[q] = row < rb.count ? uint32_t(row) * uint32_t(a.ldy) * 2u + uint32_t(nb0) * (2 * F8_BLOCK) + 16u * uint32_t(piece) : OUT_OF_RANGE;
+        x_left[q] = int(a.ldy) - nb0 * F8_BLOCK - 8 * piece;
+    }
+    // Load q of a wavefront: a quarter of the codes of wavefront column `col`, step `h`, rows 16 r ..  The
+    // four channel tiles of a stage are kblocks tiles apart each.
+    uint32_t w_off[WLW];
+    const uint32_t tile_step = uint32_t(a.kblocks) * F8_TILE_BYTES;
+    const int tiles_here = min(a.ntiles - nb0 * 8, nbs * 8);
+#pragma unroll
+    for (int q = 0; q < WLW; ++q) {
+        const int unit = wv + W * q, col = unit >> 2, h = (unit >> 1) & 1, r = unit & 1;
+        const int n = 8 * ((lane >> 2) & 3) + 4 * r + (lane >> 4);          // channel of the step
+        const int k = k0 + 64 * col + 16 * (lane & 3);
+        w_off[q] = k < a.K ? uint32_t(2 * h + (n >> 4)) * tile_step + uint32_t(k / F8_BLOCK) * F8_TILE_BYTES +
+                                 uint32_t((k >> 6) & 1) * 1024u + uint32_t(16 * (lane & 3) + (n & 15)) * 16u
+                           : OUT_OF_RANGE;
+    }
+    auto load = [&](int st, int u) {
+        uint8_t *const base = lds + u * STAGE;
+#pragma unroll
+        for (int q = 0; q < XLW; ++q) {
+            if (XL < W && wv >= XL) {                      // nothing left to load: zeros to a place of their own
+                ld128_lds(xr, OUT_OF_RANGE, lds + S * STAGE);
+                continue;
+            }
+            ld128_lds(xr, st < nst && st * 64 < x_left[q] ? x_off[q] + uint32_t(st) * 128u : OUT_OF_RANGE, base + (wv + W * q) * 1024);
+        }
+        // four tiles a stage, those past the last read as zero
+        const int left = min(4, tiles_here - 4 * st);
+        const __amdgpu_buffer_rsrc_t wr =
+            make_uniform_rsrc(w + int64_t(nb0 * 8 + (left > 0 ? 4 * st : 0)) * tile_step, left > 0 ? uint32_t(left) * tile_step : 0u);
+#pragma unroll
+        for (int q = 0; q < WLW; ++q) ld128_lds(wr, w_off[q], base + X_BYTES + (wv + W * q) * 1024);
+    };
+
+    f32x4 acc[4][MT];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const uint8_t *const x_at[2] = {lds + (wm * MT * 16 + c) * 128 + ((g ^ (c >> 1)) * 16),
+                                    lds + (wm * MT * 16 + c) * 128 + (((4 + g) ^ (c >> 1)) * 16)};
+    const uint8_t *const w_at = lds + X_BYTES + wn * 4096 + g * 64 + c * 4;
+    struct Codes {
+        uint32_t v[8];
+    };
+    auto read_w = [&](Codes &o, int u, int h) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) o.v[q] = *reinterpret_cast<const uint32_t *>(w_at + u * STAGE + h * 2048 + q * 256);
+    };
+    auto decode = [&](const Codes &o, float power, u32x4 (&op)[4]) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const uint32_t lo = __builtin_amdgcn_perm(o.v[2 * p + 1], o.v[2 * p], 0x05010400u);   // inputs 0 and 1 of two channels
+            const uint32_t hi = __builtin_amdgcn_perm(o.v[2 * p + 1], o.v[2 * p], 0x07030602u);
+            op[0][p] = widen2<false>(lo, power);
+            op[1][p] = widen2<true>(lo, power);
+            op[2][p] = widen2<false>(hi, power);
+            op[3][p] = widen2<true>(hi, power);
+        }
+    };
+
+#pragma unroll
+    for (int u = 0; u < S - 1; ++u) load(u, u);
+    Scale scale{1.0f, 1.0f};
+    bool some = false;                                     // whether a block with another scale than 0 came before
+    bool on = false;                                       // whether this block's scale is another than 0
+    float s_next = ws[kb];
+    int u = 0;
+    for (int st = 0; st < nst; ++st) {
+        wait_vmcnt<(S - 2) * LOADS>();
+        ring_barrier();
+        load(st + S - 1, u == 0 ? S - 1 : u - 1);
+        if ((st & 1) == 0) {
+            const float s = s_next;
+            if (st + 2 < nst) s_next = ws[int64_t((st >> 1) + 1) * a.kblocks + kb];
+            on = s != 0.0f;
+            if (on) {
+                const Scale next = split_scale(s);
+                if (some) {
+                    const float ratio = scale.mantissa / next.mantissa;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) acc[j][i] *= ratio;
+                }
+                scale = next;
+                some = true;
+            }
+        }
+        if (on) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                Codes codes;
+                u32x4 op[4];
+                read_w(codes, u, h);
+                decode(codes, scale.power, op);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const u32x4 x = *reinterpret_cast<const u32x4 *>(x_at[h] + u * STAGE + i * 2048);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[j][i] = mma(op[j], x, acc[j][i]);
+                }
+            }
+        }
+        u = u + 1 == S ? 0 : u + 1;
+    }
+
+    // A lane holds inputs 16 g .. of the wavefront's 64, element j of each four in acc[j].
+    const float last = scale.mantissa;
+    const int k = k0 + 64 * wn + 16 * g;
+    if (k >= a.K) return;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int row = (wm * MT + i) * 16 + c;
+        if (row >= rb.count) continue;
+        const int64_t at = int64_t(rb.first + row) * a.K + k;
+        float v[16];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * r + j] = acc[j][i][r] * last;
+        if constexpr (SPLIT) {
+            float *const to = a.part + int64_t(blockIdx.y) * a.r.rows * a.K + at;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *reinterpret_cast<f32x4 *>(to + 4 * r) = f32x4{v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]};
+        } else {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                *reinterpret_cast<u32x4 *>(a.dx + at + 8 * r) =
+                    u32x4{pack_bf16(v[8 * r], v[8 * r + 1]), pack_bf16(v[8 * r + 2], v[8 * r + 3]),
+                          pack_bf16(v[8 * r + 4], v[8 * r + 5]), pack_bf16(v[8 * r + 6], v[8 * r + 7])};
+        }
+    }
+}
+
+// Adds the splits' sums in their order.
+__global__ void __launch_bounds__(256) f8_back_join_kernel(const float *part, uint16_t *dx, int64_t n, int ks) {
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n / 4; i += int64_t(gridDim.x) * 256) {
+        f32x4 s = *reinterpret_cast<const f32x4 *>(part + 4 * i);
+        for (int k = 1; k < ks; ++k) s += *reinterpret_cast<const f32x4 *>(part + k * n + 4 * i);
+        *reinterpret_cast<u32x2 *>(dx + 4 * i) = u32x2{pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3])};
+    }
+}
+
+// Rows of N channels in rows of ldy, a multiple of eight, zeros behind: loads into LDS need rows on 16 bytes.
+__global__ void __launch_bounds__(256) f8_back_copy_kernel(const uint16_t *dy, uint16_t *to, int64_t M, int N, int64_t ldy) {
+    const int64_t per_row = ldy / 8;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < M * per_row; i += int64_t(gridDim.x) * 256) {
+        const int64_t m = i / per_row, n = (i - m * per_row) * 8;
+        const uint16_t *from = dy + m * N + n;
+        u32x4 v{0u, 0u, 0u, 0u};
+        if (n + 8 <= N) {
+            const u32x4_any p = *reinterpret_cast<const u32x4_any *>(from);
+            v = u32x4{p[0], p[1], p[2], p[3]};
+        } else {
+            for (int j = 0; n + j < N; ++j) v[j >> 1] |= uint32_t(from[j]) << (16 * (j & 1));
+        }
+        *reinterpret_cast<u32x4 *>(to + m * ldy + n) = v;
+    }
+}
+
+struct BackCfg { int WM, WN, MT, S; };
+constexpr BackCfg CFGS[] = {
+    {2, 4, 8, 3},      // 256 x 256
+    {1, 4, 8, 2},      // 128 x 256
+    {1, 4, 4, 3},      // 64 x 256
+    {1, 4, 1, 4},      // 16 x 256
+};
+constexpr int NUM_CFGS = 4;
+
+template <int I, bool SPLIT>
+hipError_t launch_of(const F8BackArgs &a, hipStream_t st) {
+    constexpr BackCfg t = CFGS[I];
+    constexpr size_t lds = back_lds<t.WM, t.WN, t.MT, t.S>();
+    static_assert(lds <= LDS_BYTES_MAX, "fits");
+    auto kern = f8_back_kernel<t.WM, t.WN, t.MT, t.S, SPLIT>;
+    static LdsLimit limit;
+    const hipError_t e = limit.raise((const void *)kern, int(lds));
+    if (e != hipSuccess) return e;
+    const unsigned grid = unsigned(ceil_div(int64_t(a.mtiles) * a.nblocks, 8) * 8);
+    hipLaunchKernelGGL(kern, dim3(grid, unsigned(a.ks)), dim3(64 * t.WM * t.WN), lds, st, a);
+    return hipGetLastError();
+}
+
+template <int I>
+hipError_t launch(const F8BackArgs &a, hipStream_t st) {
+    if (a.ks == 1) return launch_of<I, false>(a, st);
+    const hipError_t e = launch_of<I, true>(a, st);
+    if (e != hipSuccess) return e;
+    const int64_t n = int64_t(a.r.rows) * a.K;
+    hipLaunchKernelGGL(f8_back_join_kernel, elementwise_grid(n / 4), dim3(256), 0, st, a.part, a.dx, n, a.ks);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// The tallest tiles that still give every compute unit one; fewer than that, and the channels are split.
+F8BackPlan make_f8_back_plan(const F8Layout &L, int64_t M, bool grouped) {
+    F8BackPlan p;
+    p.ldy = ceil_div(L.N, 8) * 8;
+    p.bps = int(L.nblocks);
+    auto blocks = [&](int c, int64_t &mt, int64_t &nb) {
+        const BackCfg &t = CFGS[c];
+        mt = most_row_blocks(M, L.E, grouped, 16 * t.MT * t.WM);
+        nb = ceil_div(L.K, 64 * t.WN);
+    };
+    const int64_t each = ceil_div(M, grouped ? std::min(L.E, M) : 1);
+    int64_t mt, nb;
+    p.cfg = NUM_CFGS - 1;
+    for (int c = 0; c < NUM_CFGS; ++c) {
+        blocks(c, mt, nb);
+        if (each > 16 && mt * nb >= 256) { p.cfg = c; break; }
+    }
+    if (each > 16 && p.cfg == NUM_CFGS - 1) p.cfg = 2;
+    blocks(p.cfg, mt, nb);
+    if (!grouped && mt * nb < 256) {
+        const int64_t want = std::min<int64_t>(8, ceil_div(256, mt * nb));
+        p.bps = int(ceil_div(L.nblocks, std::min<int64_t>(want, ceil_div(L.nblocks, 4))));
+        p.ks = int(ceil_div(L.nblocks, p.bps));
+    }
+    p.mtiles = mt;
+    p.nblocks = nb;
+    p.threads = ceil_div(mt * nb, 8) * 8 * 64 * CFGS[p.cfg].WM * CFGS[p.cfg].WN;
+    p.operand_bytes = L.N % 8 != 0 ? round256(size_t(M) * size_t(p.ldy) * 2) : 0;
+    p.ws_bytes = p.operand_bytes + (p.ks > 1 ? round256(size_t(p.ks) * size_t(M) * size_t(L.K) * 4) : 0);
+    return p;
+}
+
+hipError_t launch_f8_backward(const F8Layout &L, const F8BackPlan &p, const F8BackArgs &args, void *workspace, hipStream_t st) {
+    F8BackArgs a = args;
+    a.w_stride = L.w_bytes;
+    a.N = int(L.N);
+    a.K = int(L.K);
+    a.ntiles = int(L.ntiles);
+    a.kblocks = int(L.kblocks);
+    a.nbs = int(L.nblocks);
+    a.mtiles = int(p.mtiles);
+    a.nblocks = int(p.nblocks);
+    a.ks = p.ks;
+    a.bps = p.bps;
+    a.ldy = p.ldy;
+    uint8_t *const space = static_cast<uint8_t *>(workspace);
+    a.part = p.ks > 1 ? reinterpret_cast<float *>(space + p.operand_bytes) : nullptr;
+    if (p.operand_bytes) {
+        uint16_t *const to = reinterpret_cast<uint16_t *>(space);
+        hipLaunchKernelGGL(f8_back_copy_kernel, elementwise_grid(int64_t(a.r.rows) * (p.ldy / 8)), dim3(256), 0, st, a.dy, to,
+                           int64_t(a.r.rows), a.N, p.ldy);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        a.dy = to;
+    }
+    switch (p.cfg) {
+        case 0: return launch<0>(a, st);
+        case 1: return launch<1>(a, st);
+        case 2: return launch<2>(a, st);
+        default: return launch<3>(a, st);
+    }
+}
+
+}  // namespace ql

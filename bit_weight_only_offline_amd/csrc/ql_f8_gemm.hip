@@ -1,0 +1,581 @@
+// Forward products of block-scaled e4m3 activations and weights on the 8-bit matrix cores, plain or
+// over experts.
+//
+//   y[m, n] = sum over blocks b of (sum over k in b of x[m, k] w[n, k]) xs[m, b] ws[n / 128, b] + bias[n]
+//
+// A block of 128 inputs is the contraction of one v_mfma_f32_16x16x128_f8f6f4, so a block's sum is one
+// instruction from zero, and joining it to the running float32 sum under its scale four fused
+// multiply-adds a lane; the two kinds of units work side by side.  The weight is the A
+// operand and the activations the B operand: a lane ends up with four consecutive channels of one token,
+// so the activation scale is one value a lane and 16 x 16 tile and the weight's one a wavefront, whose
+// channels lie in one block of 128.
+//
+// What that instruction rounds.  It aligns the products of eight inputs (a lane's bytes 8 i .. 8 i + 7) to
+// the largest of them and drops what lies below 2^-13 of it, then adds the groups in float32 (measured with
+// one large and one small product, place by place).  For normal values its sums are 1.5e-5 off, relative to their size:
+// a hundredth of what rounding to bf16 (1.7e-3) does, so products with a bf16 result take it.  Results in float32
+// are to be as exact as their type: there the codes, exact in bf16, go through v_mfma_f32_16x16x32_bf16, which sums
+// in float32 throughout (1e-7), at half the rate.  So do products of few rows, whose time is
+// the weight's way from memory whatever the instruction.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "ql_f8_device.hpp"
+#include "ql_gemm_lds.hpp"
+#include "ql_launch.hpp"
+#include "ql_lds_limit.hpp"
+
+namespace ql {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr uint32_t OUT_OF_RANGE = 0x80000000u;   // a buffer offset that reads as zero
+
+struct Operand {
+    u32x4 lo, hi;                                // inputs 16 g .. of the block's first and second half
+};
+
+// One block's sums of 16 channels x 16 tokens.
+__device__ inline f32x4 block_product(const Operand &w, const Operand &x) {
+    const i32x8 a{int(w.lo[0]), int(w.lo[1]), int(w.lo[2]), int(w.lo[3]), int(w.hi[0]), int(w.hi[1]), int(w.hi[2]), int(w.hi[3])};
+    const i32x8 b{int(x.lo[0]), int(x.lo[1]), int(x.lo[2]), int(x.lo[3]), int(x.hi[0]), int(x.hi[1]), int(x.hi[2]), int(x.hi[3])};
+    // e4m3 both, no scales of the instruction's own
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+}
+// The codes as bf16: the operand slices of four v_mfma_f32_16x16x32_bf16, eight inputs each.
+struct Wide {
+    u32x4 part[4];
+};
+__device__ inline Wide widen(const Operand &o) {
+    Wide w;
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t v = (p < 2 ? o.lo : o.hi)[2 * (p & 1) + h];
+            w.part[p][2 * h] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, false));
+            w.part[p][2 * h + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, true));
+        }
+    return w;
+}
+__device__ inline f32x4 block_product(const Wide &w, const Wide &x) {
+    f32x4 s{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+        s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w.part[p]), __builtin_bit_cast(bf16x8, x.part[p]), s, 0, 0, 0);
+    return s;
+}
+__device__ inline void join(f32x4 &acc, const f32x4 &sum, float scale) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[r] = fmaf(sum[r], scale, acc[r]);
+}
+
+// Channels n .. n + 3 of token m.
+__device__ inline void emit(const F8Args &a, int expert, int m, int n, const f32x4 &sum) {
+    const int count = a.N - n;
+    if (count <= 0) return;
+    float v[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        v[r] = sum[r] + (a.bias && r < count ? bf16_bits_to_f32(a.bias[int64_t(expert) * a.N + n + r]) : 0.0f);
+    const int64_t i = int64_t(m) * a.N + n;
+    if (a.out_f32) store4_f32(static_cast<float *>(a.out), i, v, count);
+    else store4_bf16(static_cast<uint16_t *>(a.out), i, v, count);
+}
+
+// ---- few rows: the weight streams through registers ----------------------------------
+// One workgroup owns NT column tiles over the whole input dimension.  Its WK wavefronts take the
+// blocks in turn (block i goes to wavefront i mod WK), so together they read one contiguous run per
+// tile; U blocks are in flight while the U before them are multiplied.  The wavefronts' sums meet
+// in LDS and are added in a fixed order.
+template <int NT, int WK, int U>
+__global__ void __launch_bounds__(64 * WK) f8_rows_kernel(F8Args a) {
+    extern __shared__ __attribute__((aligned(16))) f32x4 red[];      // [WK][NT][64]
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, c = lane & 15;
+    RowBlock rb;
+    int blocks;
+    if (!find_rows(a.r, 16, blockIdx.y, lane, rb, blocks)) return;
+    const int nt0 = blockIdx.x * NT, nt_here = min(NT, a.ntiles - nt0);
+
+    const __amdgpu_buffer_rsrc_t wr = make_uniform_rsrc(
+        a.w + uint64_t(rb.expert) * a.w_stride + int64_t(nt0) * a.kblocks * F8_TILE_BYTES,
+        uint32_t(nt_here) * uint32_t(a.kblocks) * F8_TILE_BYTES);
+    const __amdgpu_buffer_rsrc_t xr = make_uniform_rsrc(a.x + int64_t(rb.first) * a.K, uint32_t(rb.count) * uint32_t(a.K));
+    const __amdgpu_buffer_rsrc_t sr = make_uniform_rsrc(a.xs + int64_t(rb.first) * a.kblocks, uint32_t(rb.count) * uint32_t(a.kblocks) * 4u);
+    const __amdgpu_buffer_rsrc_t vr = make_uniform_rsrc(
+        a.ws + (int64_t(rb.expert) * a.nbs + nt0 * TILE_N / F8_BLOCK) * a.kblocks, uint32_t(a.kblocks) * 4u);
+
+    uint32_t w_off[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+        w_off[j] = j < nt_here ? uint32_t(j) * uint32_t(a.kblocks) * F8_TILE_BYTES + 16u * lane : OUT_OF_RANGE;
+    const uint32_t x_off = c < rb.count ? uint32_t(c) * uint32_t(a.K) + 16u * g : OUT_OF_RANGE;
+    const uint32_t s_off = c < rb.count ? uint32_t(c) * uint32_t(a.kblocks) * 4u : OUT_OF_RANGE;
+
+    f32x4 acc[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    struct Batch {
+        Operand w[U][NT], x[U];
+        uint32_t xs[U], ws[U];
+    };
+    auto load = [&](int it, Batch &b) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kb = (it * U + u) * WK + wv;
+            const uint32_t past = kb < a.kblocks ? 0u : OUT_OF_RANGE;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                b.w[u][j].lo = ld128(wr, (w_off[j] + uint32_t(kb) * F8_TILE_BYTES) | past);
+                b.w[u][j].hi = ld128(wr, (w_off[j] + uint32_t(kb) * F8_TILE_BYTES + 1024u) | past);
+            }
+            // the next row's codes behind the last input might be NaN: they are not read
+            const int k = kb * F8_BLOCK + 16 * g;
+            b.x[u].lo = ld128(xr, k < a.K ? x_off + uint32_t(kb) * F8_BLOCK : OUT_OF_RANGE);
+            b.x[u].hi = ld128(xr, k + 64 < a.K ? x_off + uint32_t(kb) * F8_BLOCK + 64u : OUT_OF_RANGE);
+            b.xs[u] = ld32(sr, (s_off + uint32_t(kb) * 4u) | past);
+            b.ws[u] = ld32(vr, uint32_t(kb) * 4u | past);
+        }
+    };
+    auto multiply = [&](const Batch &b) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float f = __uint_as_float(b.xs[u]) * __uint_as_float(b.ws[u]);
+            const Wide x = widen(b.x[u]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) join(acc[j], block_product(widen(b.w[u][j]), x), f);
+        }
+    };
+    const int its = (a.kblocks + WK * U - 1) / (WK * U);
+    Batch b0, b1;
+    load(0, b0);
+    for (int it = 0; it < its; it += 2) {
+        if (it + 1 < its) load(it + 1, b1);
+        multiply(b0);
+        if (it + 1 < its) {
+            if (it + 2 < its) load(it + 2, b0);
+            multiply(b1);
+        }
+    }
+
+#pragma unroll
+    for (int j = 0; j < NT; ++j) red[(wv * NT + j) * 64 + lane] = acc[j];
+    __syncthreads();
+    for (int e = tid; e < NT * 64; e += 64 * WK) {
+        const int l = e & 63, j = e >> 6;
+        if ((l & 15) >= rb.count || j >= nt_here) continue;
+        f32x4 t = red[j * 64 + l];
+#pragma unroll
+        for (int w = 1; w < WK; ++w) t += red[(w * NT + j) * 64 + l];
+        emit(a, rb.expert, rb.first + (l & 15), (nt0 + j) * TILE_N + 4 * (l >> 4), t);
+    }
+}
+
+// ---- tiles: activations through LDS, the weight straight to registers ------------------
+// WN wavefronts, each all 16 MT tokens x its own NT column tiles, WK times on alternate stages (their
+// sums meet in LDS at the end).  No two wavefronts of a group read the same weight tile: packed in operand
+// order it goes from memory to the registers it is multiplied from, S stages ahead, and LDS holds and
+// serves the activations and their scales.
+//
+// A stage is one block of 128 inputs: 128-byte runs of the rows, whose 16-byte pieces are swizzled so
+// that sixteen rows' pieces spread over all banks, and the rows' scales, in the order that gives each
+// lane its MT consecutive words.  Operands are read P tiles ahead.  One barrier a stage, P tiles
+// before its end: by then every wavefront has read all of the stage's operands and the next stage has
+// arrived, so the rows of the stage S on go to this one's place.
+template <int MT>
+constexpr int ahead() { return MT >= 8 ? 3 : (MT >= 4 ? 2 : 1); }
+template <int MT>
+constexpr int x_bytes() { return 16 * MT * F8_BLOCK; }
+constexpr int SCALE_BYTES = 1024;                       // a stage's: 128 tokens' words and 64 of the weight's
+template <int NT>
+constexpr int out_stride() { return NT * 32 + 16; }
+template <int WN, int WK, int MT, int NT, int S>
+constexpr int tile_lds() {
+    const int ring = S * WK * (x_bytes<MT>() + SCALE_BYTES), rows = (WK - 1) * WN * MT * NT * 1024 + WN * 16 * out_stride<NT>();
+    return ring > rows ? ring : rows;
+}
+
+// Outputs of a wavefront's MT x NT tiles.  A lane holds four channels of a token, eight bytes of
+// bf16; sixteen tokens of the wavefront's columns go through LDS (its own part, `mine`), so that the
+// stores are whole 16-byte pieces of contiguous runs, which memory takes at any address; element by
+// element only where a row ends.
+template <int MT, int NT>
+__device__ inline void store_tiles(const F8Args &a, const RowBlock &rb, int ct0, const f32x4 (&acc)[NT][MT], uint8_t *mine,
+                                   int lane) {
+    constexpr int PIECES = 2 * NT, STRIDE = out_stride<NT>(), ROWS = 64 / PIECES < 16 ? 64 / PIECES : 16;
+    const int g = lane >> 4, c = lane & 15;
+    const int p_row = lane / PIECES, n_mine = ct0 * TILE_N + 8 * (lane % PIECES);
+    const int last = rb.first + rb.count;
+    f32x4 b[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int n = (ct0 + j) * TILE_N + 4 * g + r;
+            b[j][r] = a.bias && n < a.N ? bf16_bits_to_f32(a.bias[int64_t(rb.expert) * a.N + n]) : 0.0f;
+        }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int mi = rb.first + i * 16;
+        if (mi >= last) break;
+        float v[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[j][r] = acc[j][i][r] + b[j][r];
+        if (a.out_f32) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int n = (ct0 + j) * TILE_N + 4 * g;
+                if (mi + c < last && n < a.N) store4_f32(static_cast<float *>(a.out), int64_t(mi + c) * a.N + n, v[j], a.N - n);
+            }
+            continue;
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            *reinterpret_cast<u32x2 *>(mine + c * STRIDE + j * 32 + g * 8) = u32x2{pack_bf16(v[j][0], v[j][1]), pack_bf16(v[j][2], v[j][3])};
+#pragma unroll
+        for (int r0 = 0; r0 < 16; r0 += ROWS) {
+            const int row = r0 + p_row, m = mi + row;
+            const uint8_t *const from = mine + (row & 15) * STRIDE + (lane % PIECES) * 16;
+            const u32x4 piece = *reinterpret_cast<const u32x4 *>(from);
+            if (p_row < ROWS && m < last && n_mine < a.N) {
+                uint16_t *const to = static_cast<uint16_t *>(a.out) + int64_t(m) * a.N + n_mine;
+                if (n_mine + 8 > a.N) {
+#pragma unroll 1
+                    for (int e = 0; n_mine + e < a.N; ++e) to[e] = reinterpret_cast<const uint16_t *>(from)[e];
+                } else {
+                    *reinterpret_cast<u32x4_any *>(to) = piece;
+                }
+            }
+        }
+    }
+}
+
+// EXACT: through the bf16 matrix cores.
+template <int WN, int WK, int MT, int NT, int S, bool SPLIT, bool EXACT>
+__global__ void __launch_bounds__(64 * WN * WK) f8_tile_kernel(F8Args a) {
+    constexpr int MP = 16 * MT, NTT = NT * WN;
+    constexpr int XL = MP / 8 / WN;                        // 1 KiB loads of rows a wavefront and stage
+    constexpr int PER_STAGE = XL + 1 + 2 * NT;
+    constexpr int P = ahead<MT>(), XB = MT >= 4 ? 4 : 2;   // operands read ahead, and buffers for them
+    static_assert(XL * WN * 8 == MP && XL >= 1, "loads divide evenly");
+    static_assert((S * MT) % XB == 0 && P < XB && P < MT, "buffers come round");
+    static_assert(F8_BLOCK % (16 * NT) == 0 && WN * 64 > MP && MP <= 128, "one weight scale a wavefront; one load of scales each");
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wk = wv / WN, wn = wv % WN;
+    const int g = lane >> 4, c = lane & 15;
+
+    // Block b runs on XCD b mod 8: give each XCD one contiguous run of the tile order, and order the
+    // tiles in bands of eight row blocks, so that the workgroups an XCD runs together share rows and
+    // columns in its L2.  A grouped product has at most a.mtiles row blocks; the counts say how many.
+    RowBlock rb;
+    int mtiles = a.mtiles;
+    if (a.r.counts) find_rows(a.r, MP, -1, lane, rb, mtiles);
+    const int tiles = mtiles * a.nblocks;
+    const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
+    const int q8 = tiles >> 3, r8 = tiles & 7;
+    if (idx >= q8 + (xcd < r8 ? 1 : 0)) return;
+    const int lin = xcd * q8 + min(xcd, r8) + idx;
+    const int band = lin / (8 * a.nblocks), in_band = lin - band * 8 * a.nblocks;
+    const int band_rows = min(8, mtiles - 8 * band);
+    find_rows(a.r, MP, 8 * band + in_band % band_rows, lane, rb, mtiles);
+    const int nt0 = in_band / band_rows * NTT, nt_here = min(NTT, a.ntiles - nt0);
+
+    const int kb0 = SPLIT ? int(blockIdx.y) * a.bps : 0;
+    const int nkb = SPLIT ? min(a.kblocks - kb0, a.bps) : a.kblocks;
+    const int nst = (nkb + WK - 1) / WK;
+
+    const __amdgpu_buffer_rsrc_t wr = make_uniform_rsrc(
+        a.w + uint64_t(rb.expert) * a.w_stride + int64_t(nt0) * a.kblocks * F8_TILE_BYTES,
+        uint32_t(nt_here) * uint32_t(a.kblocks) * F8_TILE_BYTES);
+    const __amdgpu_buffer_rsrc_t xr = make_uniform_rsrc(a.x + int64_t(rb.first) * a.K, uint32_t(rb.count) * uint32_t(a.K));
+    // this wavefront's load of scales: 64 tokens', or the weight's
+    constexpr int SW = MP < 64 ? 1 : MP / 64;             // wavefronts that load tokens' scales
+    const int nb0 = nt0 * TILE_N / F8_BLOCK, nb_here = min((NTT * TILE_N + F8_BLOCK - 1) / F8_BLOCK, a.nbs - nb0);
+    const bool tokens = wn < SW;
+    const __amdgpu_buffer_rsrc_t sr = make_uniform_rsrc(
+        tokens ? a.xs + int64_t(rb.first) * a.kblocks : a.ws + (int64_t(rb.expert) * a.nbs + nb0) * a.kblocks,
+        uint32_t(tokens ? rb.count : nb_here) * uint32_t(a.kblocks) * 4u);
+
+    uint32_t x_off[XL], s_off, w_off[NT];
+    int x_left[XL];                                        // inputs from the piece to the row's end
+#pragma unroll
+    for (int q = 0; q < XL; ++q) {
+        const int row = (wn + WN * q) * 8 + (lane >> 3), piece = (lane & 7) ^ ((row >> 1) & 7);
+        x_off[q] = row < rb.count ? uint32_t(row) * uint32_t(a.K) + uint32_t(kb0 + wk) * F8_BLOCK + 16u * uint32_t(piece) : OUT_OF_RANGE;
+        x_left[q] = a.K - (kb0 + wk) * F8_BLOCK - 16 * piece;
+    }
+    {
+        // word p of a stage's scales is token 16 (p mod MT) + p / MT; the weight's follow
+        const int p = wn * 64 + lane, row = tokens ? 16 * (p % MT) + p / MT : lane;
+        const bool real = tokens ? p < MP && row < rb.count : wn == SW && lane < nb_here;
+        s_off = real ? (uint32_t(row) * uint32_t(a.kblocks) + uint32_t(kb0 + wk)) * 4u : OUT_OF_RANGE;
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int tile = wn * NT + j;
+        w_off[j] = tile < nt_here ? (uint32_t(tile) * uint32_t(a.kblocks) + uint32_t(kb0 + wk)) * F8_TILE_BYTES + 16u * lane : OUT_OF_RANGE;
+    }
+    constexpr int STAGE = x_bytes<MT>() + SCALE_BYTES;
+    uint8_t *const ring = lds + wk * (S * STAGE);
+    auto load_x = [&](int st, int u) {
+        const bool real = st * WK + wk < nkb;
+#pragma unroll
+        for (int q = 0; q < XL; ++q)
+            ld128_lds(xr, real && st * WK * F8_BLOCK < x_left[q] ? x_off[q] + uint32_t(st) * (WK * F8_BLOCK) : OUT_OF_RANGE,
+                      ring + u * STAGE + (wn + WN * q) * 1024);
+        // past the last stage the scales are zero, the products of zero weights with them too
+        ld32_lds(sr, real ? s_off + uint32_t(st) * (WK * 4) : OUT_OF_RANGE,
+                 ring + u * STAGE + x_bytes<MT>() + (wn < SW ? wn * 256 : (wn == SW ? 512 : 768)));
+    };
+    Operand w[S][NT], x[XB];
+    auto load_w = [&](int st, int u) {
+        const uint32_t past = st * WK + wk < nkb ? 0u : OUT_OF_RANGE;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            w[u][j].lo = ld128(wr, (w_off[j] + uint32_t(st) * (WK * F8_TILE_BYTES)) | past);
+            w[u][j].hi = ld128(wr, (w_off[j] + uint32_t(st) * (WK * F8_TILE_BYTES) + 1024u) | past);
+        }
+    };
+    const uint8_t *const x_at[2] = {ring + c * 128 + ((g ^ (c >> 1)) * 16), ring + c * 128 + (((4 + g) ^ (c >> 1)) * 16)};
+    const uint8_t *const s_at = ring + x_bytes<MT>() + c * (MT * 4);
+    const uint8_t *const v_at = ring + x_bytes<MT>() + 512 + ((nt0 + wn * NT) * TILE_N / F8_BLOCK - nb0) * 4;
+    auto read_x = [&](Operand &o, int u, int i) {
+        o.lo = *reinterpret_cast<const u32x4 *>(x_at[0] + u * STAGE + i * 2048);
+        o.hi = *reinterpret_cast<const u32x4 *>(x_at[1] + u * STAGE + i * 2048);
+    };
+    float f[MT], v;                                        // the tokens' scales, the weight's
+    auto read_scales = [&](int u) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) f[i] = *reinterpret_cast<const float *>(s_at + u * STAGE + 4 * i);
+        v = *reinterpret_cast<const float *>(v_at + u * STAGE);
+    };
+
+    f32x4 acc[NT][MT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+#pragma unroll
+    for (int u = 0; u < S; ++u) {
+        load_x(u, u);
+        __builtin_amdgcn_sched_barrier(0);                 // the waits count loads in this order
+        load_w(u, u);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    wait_vmcnt<(S - 1) * PER_STAGE>();
+    ring_barrier();
+#pragma unroll
+    for (int i = 0; i < P; ++i) read_x(x[i], 0, i);
+    read_scales(0);
+
+    // Stage st in place u.  A tile's sums are joined while the next tile's instructions run.
+    auto stage = [&](int st, int u, bool more) {
+        float s[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) s[i] = f[i] * v;
+        f32x4 sum[2][NT];
+        Wide wide[EXACT ? NT : 1];
+        if constexpr (EXACT)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) wide[j] = widen(w[u][j]);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            if (i == MT - P) {
+                if (more) wait_vmcnt<(S - 2) * PER_STAGE>();
+                ring_barrier();
+                if (more) load_x(st + S, u);
+                __builtin_amdgcn_sched_barrier(0);
+                read_scales((u + 1) % S);
+            }
+            if constexpr (EXACT) {
+                const Wide xw = widen(x[(u * MT + i) % XB]);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) sum[i & 1][j] = block_product(wide[j], xw);
+            } else {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) sum[i & 1][j] = block_product(w[u][j], x[(u * MT + i) % XB]);
+            }
+            read_x(x[(u * MT + i + P) % XB], i + P < MT ? u : (u + 1) % S, (i + P) % MT);
+            if (i > 0)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) join(acc[j][i - 1], sum[(i - 1) & 1][j], s[i - 1]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) join(acc[j][MT - 1], sum[(MT - 1) & 1][j], s[MT - 1]);
+        if (more) load_w(st + S, u);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    int st = 0;
+    for (; st + S <= nst; st += S) {
+#pragma unroll
+        for (int u = 0; u < S; ++u) stage(st + u, u, true);
+    }
+    // what is left has been loaded
+    wait_vmcnt<0>();
+#pragma unroll
+    for (int u = 0; u < S - 1; ++u)
+        if (st + u < nst) stage(st + u, u, false);
+    ring_barrier();                                        // the ring is free for what follows
+    if constexpr (WK > 1) {
+        // the later groups hand their sums to the first: 1 KiB a tile, 16 bytes a lane
+        f32x4 *const at = reinterpret_cast<f32x4 *>(lds) + wn * (MT * NT) * 64 + lane;
+        constexpr int GROUP = WN * MT * NT * 64;
+        if (wk > 0) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) at[(wk - 1) * GROUP + (j * MT + i) * 64] = acc[j][i];
+        }
+        ring_barrier();
+        if (wk > 0) return;                                // no barrier follows
+#pragma unroll
+        for (int k = 0; k < WK - 1; ++k)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) acc[j][i] += at[k * GROUP + (j * MT + i) * 64];
+    }
+    const int ct0 = nt0 + wn * NT;
+    if constexpr (SPLIT) {
+        const int64_t width = int64_t(a.ntiles) * TILE_N;
+        float *const part = a.part + int64_t(blockIdx.y) * a.r.rows * width;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            if (16 * i + c >= rb.count) continue;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                if (wn * NT + j < nt_here)
+                    *reinterpret_cast<f32x4 *>(part + int64_t(rb.first + 16 * i + c) * width + (ct0 + j) * TILE_N + 4 * g) = acc[j][i];
+        }
+    } else {
+        constexpr int SUMS = (WK - 1) * WN * MT * NT * 1024;   // sums of the other groups may still be read
+        store_tiles<MT, NT>(a, rb, ct0, acc, lds + SUMS + wn * 16 * out_stride<NT>(), lane);
+    }
+}
+
+// Adds the splits' sums in their order and finishes: a thread takes four channels of one token at a time.
+__global__ void __launch_bounds__(256) f8_join_kernel(F8Args a) {
+    const int per_row = a.ntiles * 4;
+    const int64_t width = int64_t(a.ntiles) * TILE_N, all = int64_t(a.r.rows) * width;
+    for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < int64_t(a.r.rows) * per_row; e += int64_t(gridDim.x) * 256) {
+        const int m = int(e / per_row), n = int(e % per_row) * 4;
+        const float *const p = a.part + int64_t(m) * width + n;
+        f32x4 s = *reinterpret_cast<const f32x4 *>(p);
+        for (int k = 1; k < a.ks; ++k) s += *reinterpret_cast<const f32x4 *>(p + k * all);
+        emit(a, 0, m, n, s);
+    }
+}
+
+// Schedules.  kind 0 (few rows): NT column tiles a workgroup, WK wavefronts on alternate blocks; kind
+// 1 (tiles): WN wavefronts of MT x NT tiles, WK times on alternate stages, a ring of S stages.
+struct F8Cfg { int kind, MT, NT, WK, WN, S; };
+constexpr F8Cfg CFGS[] = {
+    {0, 1, 1, 8, 1, 0}, {0, 1, 2, 8, 1, 0},
+    {1, 8, 2, 1, 8, 3},      // 128 x 256
+    {1, 8, 1, 1, 8, 4},      // 128 x 128
+    {1, 4, 2, 1, 4, 4},      // 64 x 128
+    {1, 4, 1, 2, 4, 4},      // 64 x 64, two groups
+    {1, 2, 1, 2, 4, 6},      // 32 x 64, two groups
+};
+constexpr int NUM_CFGS = 7, FIRST_TILE = 2;
+constexpr int ROWS_U = 2;
+
+template <int I>
+hipError_t launch_rows(const F8Args &a, hipStream_t st) {
+    constexpr F8Cfg t = CFGS[I];
+    constexpr size_t lds = size_t(t.WK) * t.NT * 1024;
+    hipLaunchKernelGGL((f8_rows_kernel<t.NT, t.WK, ROWS_U>), dim3(unsigned(a.nblocks), unsigned(a.mtiles)), dim3(64 * t.WK), lds, st, a);
+    return hipGetLastError();
+}
+
+template <int I, bool SPLIT, bool EXACT>
+hipError_t launch_tiles_of(const F8Args &a, hipStream_t st) {
+    constexpr F8Cfg t = CFGS[I];
+    constexpr size_t lds = tile_lds<t.WN, t.WK, t.MT, t.NT, t.S>();
+    static_assert(lds <= LDS_BYTES_MAX, "fits");
+    auto kern = f8_tile_kernel<t.WN, t.WK, t.MT, t.NT, t.S, SPLIT, EXACT>;
+    static LdsLimit limit;
+    const hipError_t e = limit.raise((const void *)kern, int(lds));
+    if (e != hipSuccess) return e;
+    // each XCD takes one of eight runs of equal length: whole eights of workgroups
+    const unsigned grid = unsigned(ceil_div(int64_t(a.mtiles) * a.nblocks, 8) * 8);
+    hipLaunchKernelGGL(kern, dim3(grid, unsigned(a.ks)), dim3(64 * t.WN * t.WK), lds, st, a);
+    return hipGetLastError();
+}
+
+template <int I>
+hipError_t launch_tiles(const F8Args &a, hipStream_t st) {
+    if (a.ks == 1) return a.out_f32 ? launch_tiles_of<I, false, true>(a, st) : launch_tiles_of<I, false, false>(a, st);
+    const hipError_t e = a.out_f32 ? launch_tiles_of<I, true, true>(a, st) : launch_tiles_of<I, true, false>(a, st);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(f8_join_kernel, elementwise_grid(int64_t(a.r.rows) * a.ntiles * 4), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+F8Plan make_f8_plan(const F8Layout &L, int64_t M, bool grouped) {
+    F8Plan p;
+    p.bps = int(L.kblocks);
+    auto blocks = [&](int c, int64_t &mt, int64_t &nb) {
+        const F8Cfg &t = CFGS[c];
+        mt = most_row_blocks(M, L.E, grouped, 16 * t.MT);
+        nb = ceil_div(L.ntiles, t.NT * t.WN);
+    };
+    const int64_t used = grouped ? std::min(L.E, M) : 1;
+    const int64_t each = ceil_div(M, used);
+    int64_t mt, nb;
+    if (each <= 16 && most_row_blocks(M, L.E, grouped, 16) <= 65535) {
+        p.cfg = L.ntiles <= 512 ? 0 : 1;
+    } else {
+        p.cfg = NUM_CFGS - 1;
+        for (int c = FIRST_TILE; c < NUM_CFGS; ++c) {
+            blocks(c, mt, nb);
+            if (mt * nb >= 256) { p.cfg = c; break; }
+        }
+    }
+    blocks(p.cfg, mt, nb);
+    p.mtiles = mt;
+    p.nblocks = nb;
+    const F8Cfg &t = CFGS[p.cfg];
+    p.threads = (t.kind == 0 ? nb : ceil_div(mt * nb, 8) * 8) * 64 * t.WK * t.WN;
+    if (p.ks > 1) p.ws_bytes = round256(size_t(p.ks) * size_t(M) * size_t(L.ntiles) * TILE_N * 4);
+    return p;
+}
+
+hipError_t launch_f8_forward(const F8Layout &L, const F8Plan &p, const F8Args &args, hipStream_t st) {
+    F8Args a = args;
+    a.w_stride = L.w_bytes;
+    a.N = int(L.N);
+    a.K = int(L.K);
+    a.ntiles = int(L.ntiles);
+    a.kblocks = int(L.kblocks);
+    a.nbs = int(L.nblocks);
+    a.mtiles = int(p.mtiles);
+    a.nblocks = int(p.nblocks);
+    a.ks = p.ks;
+    a.bps = p.bps;
+    switch (p.cfg) {
+        case 0: return launch_rows<0>(a, st);
+        case 1: return launch_rows<1>(a, st);
+        case 2: return launch_tiles<2>(a, st);
+        case 3: return launch_tiles<3>(a, st);
+        case 4: return launch_tiles<4>(a, st);
+        case 5: return launch_tiles<5>(a, st);
+        default: return launch_tiles<6>(a, st);
+    }
+}
+
+}  // namespace ql

@@ -1,0 +1,413 @@
+"""Mixture-of-experts layers in 8-bit floating point: block-scaled e4m3 products, plain and over experts, the
+quantiser that makes their inputs, and the tokens' way into expert order and back, each with its backward pass.
+
+Activations are e4m3 codes [..., K] with one float32 scale for each 128 inputs, as quantize_f8() and
+dispatch_tokens(f8=True) return them; weights are packed once by pack_f8() from codes and one scale for each
+128 x 128 block (quantize_weight_f8() makes both).  One layer, forward, for expert choices `ids` [T, k] and their
+weights [T, k]:
+
+    order = expert_order(ids, E)
+    x, s = dispatch_tokens(x, order, f8=True)
+    raw = grouped_linear_f8(x, s, up_gate, order.counts)             # [up | gate]
+    h, s = quantize_f8(raw, act="swiglu")
+    y = combine_tokens(grouped_linear_f8(h, s, down, order.counts), order, weights)
+
+and backward, through the frozen weights:
+
+    dh, dweights = combine_tokens_backward(dy, h_out, order, weights)  # h_out: what combine_tokens() took
+    dh = grouped_linear_f8_backward(dh, down, order.counts)
+    draw = quantize_f8_backward(dh, raw)
+    dx = dispatch_tokens_backward(grouped_linear_f8_backward(draw, up_gate, order.counts), order)
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+import bit_weight_only_offline_amd as _Q
+
+from .ffn8 import _DTYPES, _FLOATS, _aligned, _bias, _c, _call, _fail, _need, _out, _p, _sizes, _space, _tensor
+
+__all__ = [
+    "F8_BLOCK", "quantize_f8", "quantize_f8_backward", "dequantize_f8", "quantize_weight_f8", "BlockWeight", "pack_f8",
+    "unpack_f8", "f8_default_schedule", "f8_workspace_bytes", "f8_backward_workspace_bytes", "linear_f8",
+    "linear_f8_backward", "grouped_linear_f8", "grouped_linear_f8_backward", "ExpertOrder",
+    "expert_order_workspace_bytes", "expert_order", "dispatch_tokens", "dispatch_tokens_backward", "combine_tokens",
+    "combine_tokens_backward",
+]
+
+F8_BLOCK = 128
+_CODES = (torch.float8_e4m3fn,)
+_QUANT_ACTS = {None: 0, "none": 0, "swiglu": 1}
+
+
+def bind(L: ctypes.CDLL) -> None:
+    """Argument types of the entry points this module calls."""
+    i64, sz, vp, ci = ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int
+    psz = ctypes.POINTER(sz)
+    for name, args in {
+        "qlinear_f8_quantize": [vp, ci, ci, i64, i64, vp, vp, vp],
+        "qlinear_f8_quantize_backward": [vp, vp, i64, i64, vp, vp],
+        "qlinear_f8_dequantize": [vp, vp, i64, i64, vp, ci, vp],
+        "qlinear_f8_quantize_weight": [vp, ci, i64, i64, i64, vp, vp, vp],
+        "qlinear_f8_packed_bytes": [i64, i64, i64, psz],
+        "qlinear_f8_pack": [i64, i64, i64, vp, vp, vp],
+        "qlinear_f8_unpack": [i64, i64, i64, vp, vp, vp],
+        "qlinear_f8_default_schedule": [i64, i64, i64, i64, ci, ci, ctypes.POINTER(_Q.Schedule)],
+        "qlinear_f8_workspace_bytes": [i64, i64, i64, i64, ci, psz],
+        "qlinear_f8_forward": [vp, vp, i64, vp, i64, i64, i64, vp, vp, vp, vp, ci, vp, sz, vp],
+        "qlinear_f8_backward_workspace_bytes": [i64, i64, i64, i64, ci, psz],
+        "qlinear_f8_backward": [vp, i64, vp, i64, i64, i64, vp, vp, vp, vp, sz, vp],
+        "qlinear_expert_order_workspace_bytes": [i64, i64, psz],
+        "qlinear_expert_order": [vp, ci, i64, i64, vp, vp, vp, vp, sz, vp],
+        "qlinear_dispatch": [vp, ci, vp, i64, i64, i64, vp, vp, vp, vp],
+        "qlinear_combine": [vp, ci, vp, vp, i64, i64, i64, vp, vp],
+        "qlinear_combine_backward": [vp, vp, ci, vp, vp, i64, i64, i64, vp, vp, vp],
+    }.items():
+        f = getattr(L, name)
+        f.restype = ci
+        f.argtypes = args
+
+
+def _blocks(n: int) -> int:
+    return -(-n // F8_BLOCK)
+
+
+# ---- quantisation ------------------------------------------------------------------------
+
+def quantize_f8(x: torch.Tensor, act: str | None = None):
+    """Codes float8_e4m3fn [..., K] and scales float32 [..., ceil(K / 128)] of x [..., K], bf16 or float32:
+    s = max|x| / 448 of each block, each code the nearest to x / s.  act="swiglu": x is [..., 2K] = [up | gate],
+    and up * silu(gate) is quantised.  K a multiple of 32."""
+    _tensor(x, "x", _FLOATS)
+    if act not in _QUANT_ACTS:
+        _fail("act must be None or 'swiglu'")
+    swiglu = _QUANT_ACTS[act]
+    wide = x.shape[-1] if x.dim() else 0
+    K = wide // 2 if swiglu else wide
+    if K == 0 or K % 32 or (swiglu and wide % 2):
+        _fail("x must be [..., K], or [..., 2K] with a SwiGLU, K a multiple of 32")
+    x = _aligned(x)
+    lead, R = x.shape[:-1], x.numel() // wide
+    codes = torch.empty(*lead, K, dtype=torch.float8_e4m3fn, device=x.device)
+    scales = torch.empty(*lead, _blocks(K), dtype=torch.float32, device=x.device)
+    _call("qlinear_f8_quantize", x.device, x.data_ptr(), _DTYPES[x.dtype], swiglu, R, K, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def quantize_f8_backward(dh: torch.Tensor, raw: torch.Tensor, act: str = "swiglu", out: torch.Tensor | None = None):
+    """draw bf16 [..., 2K], the gradient of the raw [up | gate] that quantize_f8(act="swiglu") took, for dh bf16
+    [..., K], the gradient of the dequantised result.  (Without an activation the gradient of x is dh itself.)"""
+    _need(act == "swiglu", "act must be 'swiglu'")
+    _tensor(dh, "dh", (torch.bfloat16,))
+    _tensor(raw, "raw", (torch.bfloat16,), dh.device)
+    if not dh.shape or dh.shape[-1] == 0 or dh.shape[-1] % 32:
+        _fail("dh must be [..., K], K a multiple of 32")
+    K, lead = dh.shape[-1], dh.shape[:-1]
+    if raw.shape != (*lead, 2 * K):
+        _fail(f"raw must be {(*lead, 2 * K)}")
+    dh, raw = _aligned(dh), _aligned(raw)
+    out = _out(out, (*lead, 2 * K), torch.bfloat16, dh.device)
+    _call("qlinear_f8_quantize_backward", dh.device, dh.data_ptr(), raw.data_ptr(), dh.numel() // K, K, out.data_ptr())
+    return out
+
+
+def _rows(codes, scales, K=None, device=None):
+    """Checked codes [..., K] and their scales: (leading shape, rows, both contiguous)."""
+    _tensor(codes, "codes", _CODES, device)
+    _tensor(scales, "scales", (torch.float32,), codes.device)
+    shape = codes.shape
+    if not shape or shape[-1] == 0 or shape[-1] % 32 or (K is not None and shape[-1] != K):
+        _fail(f"codes must be [..., {'K, a multiple of 32' if K is None else K}]")
+    if scales.shape != (*shape[:-1], _blocks(shape[-1])):
+        _fail(f"scales must be {(*shape[:-1], _blocks(shape[-1]))}")
+    return shape[:-1], codes.numel() // shape[-1], _aligned(codes), _c(scales)
+
+
+def dequantize_f8(codes: torch.Tensor, scales: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """code * scale, bf16 or float32, of what quantize_f8() or dispatch_tokens(f8=True) returned."""
+    _need(out_dtype in _DTYPES, "out_dtype must be bfloat16 or float32")
+    lead, R, codes, scales = _rows(codes, scales)
+    K = codes.shape[-1]
+    out = _out(out, (*lead, K), out_dtype, codes.device)
+    _call("qlinear_f8_dequantize", codes.device, codes.data_ptr(), scales.data_ptr(), R, K, out.data_ptr(), _DTYPES[out_dtype])
+    return out
+
+
+def quantize_weight_f8(w: torch.Tensor):
+    """Codes float8_e4m3fn and scales float32, one for each block of 128 channels by 128 inputs, of a weight [N, K]
+    or of experts' weights [E, N, K], bf16 or float32: what pack_f8() takes."""
+    _tensor(w, "w", _FLOATS)
+    _need(w.dim() in (2, 3) and w.numel() > 0 and w.shape[-1] % 32 == 0, "w must be [N, K] or [E, N, K], K a multiple of 32")
+    w = _aligned(w)
+    *lead, N, K = w.shape
+    codes = torch.empty(*w.shape, dtype=torch.float8_e4m3fn, device=w.device)
+    scales = torch.empty(*lead, _blocks(N), _blocks(K), dtype=torch.float32, device=w.device)
+    _call("qlinear_f8_quantize_weight", w.device, w.data_ptr(), _DTYPES[w.dtype], lead[0] if lead else 1, N, K,
+          codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+# ---- products ----------------------------------------------------------------------------
+
+@dataclass
+class BlockWeight:
+    """An e4m3 weight [N, K], or those of E experts, in operand order, with its block scales."""
+    E: int
+    N: int
+    K: int
+    w: torch.Tensor
+    s: torch.Tensor
+    experts: bool
+
+    def __post_init__(self):
+        self.device = self.w.device
+
+
+def pack_f8(codes: torch.Tensor, scales: torch.Tensor) -> BlockWeight:
+    """Pack codes float8_e4m3fn [N, K] and scales float32 [ceil(N / 128), ceil(K / 128)], or those of experts [E, N, K]
+    and [E, ..., ...], once.  The scales are copied."""
+    _tensor(codes, "codes", _CODES)
+    _tensor(scales, "scales", (torch.float32,), codes.device)
+    _need(codes.dim() in (2, 3) and codes.numel() > 0, "codes must be [N, K] or [E, N, K]")
+    *lead, N, K = codes.shape
+    _need(scales.shape == (*lead, _blocks(N), _blocks(K)), f"scales must be {(*lead, _blocks(N), _blocks(K))}")
+    E = lead[0] if lead else 1
+    n = ctypes.c_size_t()
+    _Q._check(_Q.lib().qlinear_f8_packed_bytes(E, N, K, ctypes.byref(n)), "qlinear_f8_packed_bytes")
+    codes = _aligned(codes)
+    w = torch.empty(n.value, dtype=torch.uint8, device=codes.device)
+    _call("qlinear_f8_pack", codes.device, E, N, K, codes.data_ptr(), w.data_ptr())
+    return BlockWeight(E, N, K, w, scales.clone(memory_format=torch.contiguous_format), bool(lead))
+
+
+def unpack_f8(pw: BlockWeight):
+    """(codes, scales), exactly as packed."""
+    _need(isinstance(pw, BlockWeight), "a BlockWeight is needed")
+    lead = (pw.E,) if pw.experts else ()
+    codes = torch.empty(*lead, pw.N, pw.K, dtype=torch.float8_e4m3fn, device=pw.device)
+    _call("qlinear_f8_unpack", pw.device, pw.E, pw.N, pw.K, pw.w.data_ptr(), codes.data_ptr())
+    return codes, pw.s.clone()
+
+
+def f8_default_schedule(M: int, N: int, K: int, E: int | None = None, backward: bool = False):
+    """The Schedule (tile, splits) that a product of M rows, or its backward pass, takes; E: over that many experts."""
+    s = _Q.Schedule()
+    _Q._check(_Q.lib().qlinear_f8_default_schedule(M, 1 if E is None else E, N, K, int(E is not None), int(backward),
+                                                   ctypes.byref(s)), "qlinear_f8_default_schedule")
+    return s
+
+
+def f8_workspace_bytes(M: int, N: int, K: int, E: int | None = None) -> int:
+    return _sizes("qlinear_f8_workspace_bytes", M, 1 if E is None else E, N, K, int(E is not None))
+
+
+def f8_backward_workspace_bytes(M: int, N: int, K: int, E: int | None = None) -> int:
+    return _sizes("qlinear_f8_backward_workspace_bytes", M, 1 if E is None else E, N, K, int(E is not None))
+
+
+def _weight(pw, experts: bool):
+    if not isinstance(pw, BlockWeight) or pw.experts != experts:
+        _fail("pw must be a BlockWeight of experts [E, N, K]" if experts else "pw must be a BlockWeight of one weight [N, K]")
+    return pw.E if experts else None
+
+
+def _counts(tokens_per_expert, pw):
+    _tensor(tokens_per_expert, "tokens_per_expert", (torch.int32,), pw.device)
+    if tokens_per_expert.shape != (pw.E,):
+        _fail(f"tokens_per_expert must be ({pw.E},)")
+    return _c(tokens_per_expert)
+
+
+def _forward(codes, scales, pw, counts, bias, out_dtype, out, workspace):
+    E = None if counts is None else pw.E
+    _need(out_dtype in _DTYPES, "out_dtype must be bfloat16 or float32")
+    lead, M, codes, scales = _rows(codes, scales, pw.K, pw.device)
+    bias = _bias(bias, pw.E * pw.N, pw)
+    out = _out(out, (*lead, pw.N), out_dtype, pw.device)
+    need = f8_workspace_bytes(M, pw.N, pw.K, E)
+    ws = _space(workspace, need, pw.device)
+    _call("qlinear_f8_forward", pw.device, codes.data_ptr(), scales.data_ptr(), M, _p(counts), pw.E, pw.N, pw.K,
+          pw.w.data_ptr(), pw.s.data_ptr(), _p(bias), out.data_ptr(), _DTYPES[out_dtype], _p(ws), need)
+    return out
+
+
+def _backward(dy, pw, counts, out, workspace):
+    E = None if counts is None else pw.E
+    _tensor(dy, "dy", (torch.bfloat16,), pw.device)
+    if not dy.shape or dy.shape[-1] != pw.N:
+        _fail(f"dy must be [..., {pw.N}]")
+    dy = _aligned(dy)
+    M = dy.numel() // pw.N
+    out = _out(out, (*dy.shape[:-1], pw.K), torch.bfloat16, pw.device)
+    need = f8_backward_workspace_bytes(M, pw.N, pw.K, E)
+    ws = _space(workspace, need, pw.device)
+    _call("qlinear_f8_backward", pw.device, dy.data_ptr(), M, _p(counts), pw.E, pw.N, pw.K, pw.w.data_ptr(), pw.s.data_ptr(),
+          out.data_ptr(), _p(ws), need)
+    return out
+
+
+def linear_f8(codes: torch.Tensor, scales: torch.Tensor, pw: BlockWeight, bias: torch.Tensor | None = None,
+              out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y[..., N] = sum over blocks of 128 inputs of (codes . w^T) * scales * weight scales, plus bias.
+
+    codes float8_e4m3fn [..., K], scales float32 [..., ceil(K / 128)], bias bf16 [N]; out_dtype bf16 or float32."""
+    _weight(pw, False)
+    return _forward(codes, scales, pw, None, bias, out_dtype, out, workspace)
+
+
+def linear_f8_backward(dy: torch.Tensor, pw: BlockWeight, out: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """dx bf16 [..., K] for dy bf16 [..., N]: the gradient of the dequantised activations.  The gradient of a
+    bias is dy summed over the tokens."""
+    _weight(pw, False)
+    return _backward(dy, pw, None, out, workspace)
+
+
+def grouped_linear_f8(codes: torch.Tensor, scales: torch.Tensor, pw: BlockWeight, tokens_per_expert: torch.Tensor,
+                      bias: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """linear_f8() of rows [T, K] in expert order, each with its own expert's weight: expert e owns the next
+    tokens_per_expert[e] rows, an int32 device tensor [E]; bias bf16 [E, N].  Rows past the sum of the counts are left
+    as they are in `out` (uninitialised when allocated)."""
+    _weight(pw, True)
+    _tensor(codes, "codes", _CODES, pw.device)
+    _need(codes.dim() == 2, f"codes must be [T, {pw.K}]")
+    return _forward(codes, scales, pw, _counts(tokens_per_expert, pw), bias, out_dtype, out, workspace)
+
+
+def grouped_linear_f8_backward(dy: torch.Tensor, pw: BlockWeight, tokens_per_expert: torch.Tensor,
+                               out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """dx bf16 [T, K] for dy bf16 [T, N], rows in expert order; rows past the sum of the counts are left as they
+    are in `out` (uninitialised when allocated)."""
+    _weight(pw, True)
+    _tensor(dy, "dy", (torch.bfloat16,), pw.device)
+    _need(dy.dim() == 2, f"dy must be [T, {pw.N}]")
+    return _backward(dy, pw, _counts(tokens_per_expert, pw), out, workspace)
+
+
+# ---- expert order ------------------------------------------------------------------------
+
+@dataclass
+class ExpertOrder:
+    """Slots (token, choice) in expert order: counts int32 [E], rows int32 [..., k] (each slot's place, -1 for none),
+    source int32 [slots] (the slot at each place, -1 behind the last)."""
+    counts: torch.Tensor
+    rows: torch.Tensor
+    source: torch.Tensor
+
+    @property
+    def device(self) -> torch.device:
+        return self.rows.device
+
+
+def expert_order_workspace_bytes(slots: int, E: int) -> int:
+    return _sizes("qlinear_expert_order_workspace_bytes", slots, E)
+
+
+def expert_order(ids: torch.Tensor, E: int, workspace: torch.Tensor | None = None) -> ExpertOrder:
+    """Sort the slots of ids [..., k], int32 or int64 (as torch.topk() returns them), by their expert, in the order of
+    the slots within each; order.counts is what grouped_linear_f8() and grouped_linear() take.  An id outside 0 ..
+    E - 1 puts its slot nowhere.  E at most 1024."""
+    _tensor(ids, "ids", (torch.int32, torch.int64))
+    _need(ids.dim() > 0 and ids.shape[-1] > 0, "ids must be [..., k]")
+    ids = _c(ids)
+    n, dev = ids.numel(), ids.device
+    need = expert_order_workspace_bytes(n, E)
+    counts = torch.empty(E, dtype=torch.int32, device=dev)
+    rows = torch.empty(*ids.shape, dtype=torch.int32, device=dev)
+    source = torch.empty(n, dtype=torch.int32, device=dev)
+    ws = _space(workspace, need, dev)
+    _call("qlinear_expert_order", dev, ids.data_ptr(), ids.element_size(), n, E, counts.data_ptr(), rows.data_ptr(),
+          source.data_ptr(), _p(ws), need)
+    return ExpertOrder(counts, rows, source)
+
+
+def _order(order, device):
+    """(leading shape, tokens, choices) of a checked order on `device`, its rows contiguous."""
+    if not isinstance(order, ExpertOrder):
+        _fail("order must be an ExpertOrder")
+    rows = order.rows
+    _tensor(rows, "order.rows", (torch.int32,), device)
+    if not rows.is_contiguous() or rows.dim() == 0 or rows.shape[-1] == 0:
+        _fail("order.rows must be a contiguous [..., k]")
+    k = rows.shape[-1]
+    return rows.shape[:-1], rows.numel() // k, k
+
+
+def _sorted(y, name, order, dtypes=_FLOATS):
+    """A checked tensor [slots, D] in expert order."""
+    _tensor(y, name, dtypes)
+    lead, T, k = _order(order, y.device)
+    if y.dim() != 2 or y.shape[0] != T * k or y.shape[1] == 0:
+        _fail(f"{name} must be [{T * k}, D], a row for each slot")
+    return lead, T, k, _c(y)
+
+
+def dispatch_tokens(x: torch.Tensor, order: ExpertOrder, f8: bool = False, out: torch.Tensor | None = None):
+    """Rows [slots, D] in expert order of tokens x [..., D], bf16 or float32: every token's row once for each of its
+    choices.  f8=True: (codes, scales) in its place, as quantize_f8() of those rows.  Rows that no slot is
+    put to (slots without an expert leave as many at the end) are left as they are."""
+    _tensor(x, "x", _FLOATS)
+    lead, T, k = _order(order, x.device)
+    if x.shape[:-1] != lead or not x.shape or x.shape[-1] == 0:
+        _fail(f"x must be {(*lead, 'D')}")
+    D, x = x.shape[-1], _c(x)
+    codes = scales = None
+    if f8:
+        _need(out is None, "out is for rows that are not quantised")
+        _need(D % 32 == 0, "D must be a multiple of 32 for quantised rows")
+        codes = torch.empty(T * k, D, dtype=torch.float8_e4m3fn, device=x.device)
+        scales = torch.empty(T * k, _blocks(D), dtype=torch.float32, device=x.device)
+    else:
+        out = _out(out, (T * k, D), x.dtype, x.device)
+    _call("qlinear_dispatch", x.device, x.data_ptr(), _DTYPES[x.dtype], order.rows.data_ptr(), T, k, D, _p(out), _p(codes),
+          _p(scales))
+    return (codes, scales) if f8 else out
+
+
+def combine_tokens(y: torch.Tensor, order: ExpertOrder, weights: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """out[..., D] = sum over a token's choices of weights * its rows of y [slots, D], bf16 or float32, added in
+    float32 in the choices' order; weights float32 [..., k], or None for ones.  Slots without a place add nothing."""
+    lead, T, k, y = _sorted(y, "y", order)
+    if weights is not None:
+        _tensor(weights, "weights", (torch.float32,), y.device)
+        if weights.shape != order.rows.shape:
+            _fail(f"weights must be {tuple(order.rows.shape)}")
+        weights = _c(weights)
+    D = y.shape[1]
+    out = _out(out, (*lead, D), y.dtype, y.device)
+    _call("qlinear_combine", y.device, y.data_ptr(), _DTYPES[y.dtype], order.rows.data_ptr(), _p(weights), T, k, D, out.data_ptr())
+    return out
+
+
+def dispatch_tokens_backward(dsorted: torch.Tensor, order: ExpertOrder, out: torch.Tensor | None = None) -> torch.Tensor:
+    """dx [..., D] for the gradient [slots, D] of dispatch_tokens()'s rows (of the dequantised ones with f8=True): the
+    sum of each token's rows."""
+    return combine_tokens(dsorted, order, None, out)
+
+
+def combine_tokens_backward(dout: torch.Tensor, y: torch.Tensor, order: ExpertOrder, weights: torch.Tensor,
+                            out: torch.Tensor | None = None):
+    """(dy [slots, D], dweights float32 [..., k]) of combine_tokens() with weights, for dout [..., D] of y's type; rows
+    of dy that no slot names are left as they are in `out` (uninitialised when allocated).  (Without weights the gradient
+    of y is dispatch_tokens(dout, order).)"""
+    lead, T, k, y = _sorted(y, "y", order)
+    D = y.shape[1]
+    _tensor(dout, "dout", (y.dtype,), y.device)
+    _tensor(weights, "weights", (torch.float32,), y.device)
+    if dout.shape != (*lead, D):
+        _fail(f"dout must be {(*lead, D)}")
+    if weights.shape != order.rows.shape:
+        _fail(f"weights must be {tuple(order.rows.shape)}")
+    dout, weights = _c(dout), _c(weights)
+    dy = _out(out, (T * k, D), y.dtype, y.device)
+    dw = torch.empty(*weights.shape, dtype=torch.float32, device=y.device)
+    _call("qlinear_combine_backward", y.device, dout.data_ptr(), y.data_ptr(), _DTYPES[y.dtype], order.rows.data_ptr(),
+          weights.data_ptr(), T, k, D, dy.data_ptr(), dw.data_ptr())
+    return dy, dw

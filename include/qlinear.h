@@ -502,6 +502,105 @@ ql_status qlinear_block_norm_backward(const void *dx, const void *dresidual, con
                                       void *dy, float *dpost, float *dpre, float *dgate, void *workspace,
                                       size_t workspace_bytes, void *stream);
 
+/*
+ * Mixture-of-experts layers in 8-bit floating point.  Codes are e4m3 (OCP: sign, 4 exponent bits of bias 7,
+ * 3 mantissa bits, largest value 448, no infinities).  Activations carry one float32 scale for each block of
+ * 128 inputs of a row, weights one for each block of 128 channels by 128 inputs; a last block may be
+ * shorter.  K is a multiple of 32 and at most 131071, N at most 2^20, experts at most 65536, rows below
+ * 2^31.
+ *
+ * qlinear_f8_quantize: s = max|x| / 448 of each block in float32, code = the e4m3 value nearest to the exact
+ * quotient x / s, ties to even.  An all-zero block gets s = 0 and codes 0, a block with NaN or infinity s =
+ * NaN and codes 0.
+ *   x       [R, K] bf16 or float32, 16-byte aligned; with QL_ACT_SWIGLU [R, 2K] = [up | gate], and
+ *           up * silu(gate), formed in float32, is quantised
+ *   codes   out: [R, K] (8-byte aligned)     scales  out: float32 [R, ceil(K / 128)]
+ * qlinear_f8_quantize_backward: gradient through the SwiGLU, the quantisation passed straight through:
+ *   draw = [dh silu(gate) | dh up silu'(gate)]; dh bf16 [R, K], raw and draw bf16 [R, 2K], 16-byte aligned
+ * qlinear_f8_dequantize: out[r, k] = code * s, rounded once; [R, K] bf16 or float32
+ * qlinear_f8_quantize_weight: the same for weights [E, N, K] with scales [E, ceil(N / 128), ceil(K / 128)]
+ */
+ql_status qlinear_f8_quantize(const void *x, ql_dtype x_dtype, ql_act act, int64_t R, int64_t K, void *codes, float *scales,
+                              void *stream);
+ql_status qlinear_f8_quantize_backward(const void *dh, const void *raw, int64_t R, int64_t K, void *draw, void *stream);
+ql_status qlinear_f8_dequantize(const void *codes, const float *scales, int64_t R, int64_t K, void *out, ql_dtype out_dtype,
+                                void *stream);
+ql_status qlinear_f8_quantize_weight(const void *w, ql_dtype w_dtype, int64_t E, int64_t N, int64_t K, void *codes,
+                                     float *scales, void *stream);
+
+/*
+ * qlinear_f8_pack() lays the codes of a weight [E, N, K] (E = 1: a plain one) out once for the products
+ * below; scales are used as they are.  qlinear_f8_unpack() inverts it.  All pointers 16-byte aligned.
+ */
+ql_status qlinear_f8_packed_bytes(int64_t E, int64_t N, int64_t K, size_t *bytes);
+ql_status qlinear_f8_pack(int64_t E, int64_t N, int64_t K, const void *codes, void *packed, void *stream);
+ql_status qlinear_f8_unpack(int64_t E, int64_t N, int64_t K, const void *packed, void *codes, void *stream);
+
+/*
+ * y[m, n] = sum over blocks b (sum over k in b of x[m, k] w[n, k]) scales[m, b] w_scales[n / 128, b] + bias[n]
+ *   codes              [M, K] row-major, 16-byte aligned     scales  float32 [M, ceil(K / 128)]
+ *   tokens_per_expert  NULL: a plain product, E = 1.  Else int32 [E] (device): rows are in expert order, and
+ *                      expert e owns the next tokens_per_expert[e] of them.  It is read by the device.  A negative
+ *                      count counts as 0 and counts past M are clipped; rows past the sum of the counts are
+ *                      left untouched.
+ *   packed, w_scales   all experts' packed codes, and float32 [E, ceil(N / 128), ceil(K / 128)]
+ *   bias               bf16 [E, N] or NULL                   out     [M, N] bf16 or float32
+ *   workspace          qlinear_f8_workspace_bytes() bytes, 256-byte aligned (NULL if 0): float32 partial sums
+ *                      where the input dimension is split over workgroups
+ * Sums are float32 in an order that the schedule sets: repeated calls give the same bits.  One exception: where
+ * out is bf16 and an expert has more than 16 rows on average, the 8-bit matrix cores add products in groups of
+ * eight, of which what lies below 2^-13 of the group's largest is dropped (1.5e-5 of a sum of normal values; its
+ * rounding to bf16 is 1.7e-3).  M = 0 is a no-op.  QL_E_SHAPE where no grid holds the tiles.
+ *
+ * Backward: dx[m, k] = sum over channel blocks b of w_scales[b, k / 128] (sum over n in b of dy[m, n] w[n, k]),
+ * the gradient of the dequantised activations for frozen weights; dy bf16 [M, N], dx bf16 [M, K], both
+ * 16-byte aligned.  Neither dy nor the codes are rounded.  Its workspace holds partial sums of split channels,
+ * and a copy of dy where N is not a multiple of eight.
+ *
+ * qlinear_f8_default_schedule: tile (rows x outputs of a workgroup) and splits of the summed dimension:
+ *   forward   0: 16 x 16, 1: 16 x 32, 2: 128 x 256, 3: 128 x 128, 4: 64 x 128, 5: 64 x 64, 6: 32 x 64
+ *   backward  0: 256, 1: 128, 2: 64, 3: 16 rows, all x 256
+ */
+ql_status qlinear_f8_default_schedule(int64_t M, int64_t E, int64_t N, int64_t K, int grouped, int backward, ql_schedule *out);
+ql_status qlinear_f8_workspace_bytes(int64_t M, int64_t E, int64_t N, int64_t K, int grouped, size_t *bytes);
+ql_status qlinear_f8_forward(const void *codes, const float *scales, int64_t M, const int32_t *tokens_per_expert, int64_t E,
+                             int64_t N, int64_t K, const void *packed, const float *w_scales, const void *bias, void *out,
+                             ql_dtype out_dtype, void *workspace, size_t workspace_bytes, void *stream);
+ql_status qlinear_f8_backward_workspace_bytes(int64_t M, int64_t E, int64_t N, int64_t K, int grouped, size_t *bytes);
+ql_status qlinear_f8_backward(const void *dy, int64_t M, const int32_t *tokens_per_expert, int64_t E, int64_t N, int64_t K,
+                              const void *packed, const float *w_scales, void *dx, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/*
+ * Tokens into expert order and back.  Slot (t, j) = t k + j is choice j of token t.
+ *
+ * qlinear_expert_order: slots sorted by their expert, in the order of the slots within each.
+ *   ids      [n] int32 or int64 (id_bytes 4 or 8); an id outside 0 .. E-1 puts its slot nowhere
+ *   counts   out: int32 [E], slots of each expert
+ *   rows     out: int32 [n], each slot's place, -1 for none
+ *   source   out: int32 [n], the slot at each place, -1 behind the last
+ *   E at most 1024; workspace qlinear_expert_order_workspace_bytes() bytes, 256-byte aligned (NULL if 0)
+ *
+ * qlinear_dispatch: out[rows[t, j]] = x[t], x [T, D] and out [T k, D] of one type; or codes and scales in
+ *   place of out, quantised as by qlinear_f8_quantize() (D then as K there).  Its gradient is
+ *   qlinear_combine() without weights.
+ * qlinear_combine: out[t] = sum over j of weights[t, j] y[rows[t, j]], added in float32 in the order of j;
+ *   weights float32 [T, k], or NULL for ones
+ * qlinear_combine_backward: dy[rows[t, j]] = weights[t, j] dout[t],
+ *   dweights[t, j] = sum over d of dout[t, d] y[rows[t, j], d], 0 for a slot without a place
+ * Rows outside 0 .. T k - 1 are skipped; rows of out, codes, scales and dy that no slot names are left as they are.
+ * bf16 or float32, k at most 256, D at most 2^24, T k below 2^31.  T = 0 is a no-op.
+ */
+ql_status qlinear_expert_order_workspace_bytes(int64_t n, int64_t E, size_t *bytes);
+ql_status qlinear_expert_order(const void *ids, int id_bytes, int64_t n, int64_t E, int32_t *counts, int32_t *rows,
+                               int32_t *source, void *workspace, size_t workspace_bytes, void *stream);
+ql_status qlinear_dispatch(const void *x, ql_dtype dtype, const int32_t *rows, int64_t T, int64_t k, int64_t D, void *out,
+                           void *codes, float *scales, void *stream);
+ql_status qlinear_combine(const void *y, ql_dtype dtype, const int32_t *rows, const float *weights, int64_t T, int64_t k,
+                          int64_t D, void *out, void *stream);
+ql_status qlinear_combine_backward(const void *dout, const void *y, ql_dtype dtype, const int32_t *rows, const float *weights,
+                                   int64_t T, int64_t k, int64_t D, void *dy, float *dweights, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
