@@ -26,16 +26,26 @@ __device__ inline f32x4 mma(const u32x4 &a, const u32x4 &b, const f32x4 &c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// A block's scale as mantissa and power of two.  Scales below float32's normal range keep the
-// least power and a smaller mantissa; NaN and infinity are mantissas.
+// A block's scale as mantissa and power of two, the ratio of the sums' unit before to it, and how its codes are
+// taken apart.  Scales below float32's normal range keep the least power and a smaller mantissa; NaN and infinity are
+// mantissas.  A block with the scale 0 leaves the unit as it is, and its codes are taken as zeros.
 struct Scale {
-    float mantissa, power;
+    float mantissa, power, ratio;
+    uint32_t lo, hi;                                       // permutations: inputs 0 and 1, 2 and 3 of two channels
 };
-__device__ inline Scale split_scale(float s) {
+__device__ inline Scale split_scale(float s, float before) {
     const uint32_t b = __float_as_uint(s), e = (b >> 23) & 0xFFu;
-    if (e == 0xFFu) return Scale{s, 1.0f};
-    if (e == 0u) return Scale{s * 8.507059173023462e37f, 1.1754943508222875e-38f};          // 2^126, 2^-126
-    return Scale{__uint_as_float((b & 0x807FFFFFu) | 0x3F800000u), __uint_as_float(e << 23)};
+    Scale r{s, 1.0f, 1.0f, 0x05010400u, 0x07030602u};
+    if (e == 0u) {
+        r.mantissa = s * 8.507059173023462e37f;            // 2^126
+        r.power = 1.1754943508222875e-38f;                 // 2^-126
+    } else if (e != 0xFFu) {
+        r.mantissa = __uint_as_float((b & 0x807FFFFFu) | 0x3F800000u);
+        r.power = __uint_as_float(e << 23);
+    }
+    if (s == 0.0f) return Scale{before, 1.0f, 1.0f, 0x0C0C0C0Cu, 0x0C0C0C0Cu};
+    r.ratio = before / r.mantissa;
+    return r;
 }
 
 // Two codes as bf16 times a power of two.
@@ -44,7 +54,7 @@ __device__ inline uint32_t widen2(uint32_t codes, float power) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, power, HI));
 }
 
-// Workgroup: WM x WN wavefronts, each 16 MT tokens x 64 inputs; S stages of 64 channels in LDS.
+// Workgroup: WM x WN wavefronts, each 16 MT tokens x 64 inputs; three stages of 64 channels in LDS.
 //
 // Weight.  The operand of inputs (the A operand) needs eight channels of one input in a lane, packed tiles
 // hold sixteen inputs of one channel.  A stage's 64 x 64 codes of a wavefront column lie in LDS as rows of 64
@@ -53,13 +63,18 @@ __device__ inline uint32_t widen2(uint32_t codes, float power) {
 // four operands, of inputs 4 c + j for j = 0 .. 3, after eight byte permutes and sixteen conversions.  Their sums
 // leave a lane with sixteen consecutive inputs of a token, 32 bytes of bf16, which are stored as they are.
 //
-// Gradients.  128-byte runs of the rows, their 16-byte pieces swizzled; the B operand.
-template <int WM, int WN, int MT, int S>
-constexpr int back_lds() { return S * (16 * MT * WM * 128 + WN * 4096) + (2 * MT * WM < WM * WN ? 1024 : 0); }
+// Gradients.  128-byte runs of the rows, their 16-byte pieces swizzled; the B operand, read P tiles ahead.
+//
+// A stage is two steps of 32 channels.  During a step the next one's codes are read and turned into operands between
+// the matrix instructions.  A barrier before each step: the first of a stage frees the stage before it, whose place
+// takes the loads of the stage after next; the second waits for the next stage.
+template <int WM, int WN, int MT>
+constexpr int back_lds() { return 3 * (16 * MT * WM * 128 + WN * 4096) + (2 * MT * WM < WM * WN ? 1024 : 0); }
 
-template <int WM, int WN, int MT, int S, bool SPLIT>
-__global__ void __launch_bounds__(64 * WM * WN) f8_back_kernel(F8BackArgs a) {
-    constexpr int W = WM * WN, MP = 16 * MT * WM, KP = 64 * WN;
+template <int WM, int WN, int MT, bool SPLIT>
+__global__ void __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2))) f8_back_kernel(F8BackArgs a) {
+    constexpr int S = 3, W = WM * WN, MP = 16 * MT * WM, KP = 64 * WN;
+    constexpr int P = MT >= 4 ? 3 : 1, XB = MT >= 4 ? 4 : 2;
     constexpr int X_BYTES = MP * 128, STAGE = X_BYTES + WN * 4096;
     constexpr int XL = MP / 8, WL = 4 * WN;                // 1 KiB loads of a stage
     constexpr int XLW = (XL + W - 1) / W, WLW = WL / W, LOADS = XLW + WLW;
@@ -119,8 +134,8 @@ __global__ void __launch_bounds__(64 * WM * WN) f8_back_kernel(F8BackArgs a) {
                                  uint32_t((k >> 6) & 1) * 1024u + uint32_t(16 * (lane & 3) + (n & 15)) * 16u
                            : OUT_OF_RANGE;
     }
-    auto load = [&](int st, int u) {
-        uint8_t *const base = lds + u * STAGE;
+    auto load = [&](int st, int place) {
+        uint8_t *const base = lds + place;
 #pragma unroll
         for (int q = 0; q < XLW; ++q) {
             if (XL < W && wv >= XL) {                      // nothing left to load: zeros to a place of their own
@@ -149,70 +164,88 @@ __global__ void __launch_bounds__(64 * WM * WN) f8_back_kernel(F8BackArgs a) {
     struct Codes {
         uint32_t v[8];
     };
-    auto read_w = [&](Codes &o, int u, int h) {
+    auto read_w = [&](Codes &o, int stage, int h) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) o.v[q] = *reinterpret_cast<const uint32_t *>(w_at + u * STAGE + h * 2048 + q * 256);
+        for (int q = 0; q < 8; ++q) o.v[q] = *reinterpret_cast<const uint32_t *>(w_at + stage + h * 2048 + q * 256);
     };
-    auto decode = [&](const Codes &o, float power, u32x4 (&op)[4]) {
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const uint32_t lo = __builtin_amdgcn_perm(o.v[2 * p + 1], o.v[2 * p], 0x05010400u);   // inputs 0 and 1 of two channels
-            const uint32_t hi = __builtin_amdgcn_perm(o.v[2 * p + 1], o.v[2 * p], 0x07030602u);
-            op[0][p] = widen2<false>(lo, power);
-            op[1][p] = widen2<true>(lo, power);
-            op[2][p] = widen2<false>(hi, power);
-            op[3][p] = widen2<true>(hi, power);
-        }
+    // Channels 2 p and 2 p + 1 of each lane's eight.
+    auto decode = [&](const Codes &o, int p, const Scale &s, u32x4 (&op)[4]) {
+        const uint32_t lo = __builtin_amdgcn_perm(o.v[2 * p + 1], o.v[2 * p], s.lo);
+        const uint32_t hi = __builtin_amdgcn_perm(o.v[2 * p + 1], o.v[2 * p], s.hi);
+        op[0][p] = widen2<false>(lo, s.power);
+        op[1][p] = widen2<true>(lo, s.power);
+        op[2][p] = widen2<false>(hi, s.power);
+        op[3][p] = widen2<true>(hi, s.power);
+    };
+    u32x4 x[XB], op[2][4];
+    auto read_x = [&](int stage, int q) {                  // tile q of a stage's two steps
+        x[q % XB] = *reinterpret_cast<const u32x4 *>(x_at[q / MT] + stage + q % MT * 2048);
     };
 
-#pragma unroll
-    for (int u = 0; u < S - 1; ++u) load(u, u);
-    Scale scale{1.0f, 1.0f};
-    bool some = false;                                     // whether a block with another scale than 0 came before
-    bool on = false;                                       // whether this block's scale is another than 0
+    load(0, 0);
+    load(1, STAGE);
+    wait_vmcnt<LOADS>();
+    ring_barrier();
     float s_next = ws[kb];
-    int u = 0;
-    for (int st = 0; st < nst; ++st) {
-        wait_vmcnt<(S - 2) * LOADS>();
-        ring_barrier();
-        load(st + S - 1, u == 0 ? S - 1 : u - 1);
-        if ((st & 1) == 0) {
-            const float s = s_next;
-            if (st + 2 < nst) s_next = ws[int64_t((st >> 1) + 1) * a.kblocks + kb];
-            on = s != 0.0f;
-            if (on) {
-                const Scale next = split_scale(s);
-                if (some) {
-                    const float ratio = scale.mantissa / next.mantissa;
+    Scale now = split_scale(s_next, 1.0f), next = now;
+    if (nst > 2) s_next = ws[a.kblocks + kb];
+    {
+        Codes first;
+        read_w(first, 0, 0);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+        for (int q = 0; q < P; ++q) read_x(0, q);
 #pragma unroll
-                        for (int i = 0; i < MT; ++i) acc[j][i] *= ratio;
-                }
-                scale = next;
-                some = true;
-            }
-        }
-        if (on) {
+        for (int p = 0; p < 4; ++p) decode(first, p, now, op[0]);
+    }
+    int at = 0, after = STAGE;                             // places of this stage and of the next
+    for (int st = 0; st < nst; st += 2) {                  // a block of channels, its second stage maybe empty
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int free = after == (S - 1) * STAGE ? 0 : after + STAGE;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                if (h == 1) wait_vmcnt<LOADS>();
+                ring_barrier();
+                if (h == 0) load(st + e + 2, free);
+                if (e == 1 && h == 1) {
+                    next = st + 2 < nst ? split_scale(s_next, now.mantissa) : now;
+                    if (st + 2 >= nst) next.ratio = 1.0f;
+                    if (st + 4 < nst) s_next = ws[int64_t((st >> 1) + 2) * a.kblocks + kb];
+                }
                 Codes codes;
-                u32x4 op[4];
-                read_w(codes, u, h);
-                decode(codes, scale.power, op);
+                read_w(codes, h == 0 ? at : after, 1 - h);
+                __builtin_amdgcn_sched_barrier(0);
+                const Scale &s = e == 1 && h == 1 ? next : now;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
-                    const u32x4 x = *reinterpret_cast<const u32x4 *>(x_at[h] + u * STAGE + i * 2048);
+                    const int q = h * MT + i;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[j][i] = mma(op[j], x, acc[j][i]);
+                    for (int j = 0; j < 4; ++j) acc[j][i] = mma(op[h][j], x[q % XB], acc[j][i]);
+                    if (q + P < 2 * MT) read_x(at, q + P);
+                    else read_x(after, q + P - 2 * MT);
+                    // the next step's operands, and behind a block's last products its sums in units of the next scale
+                    if (MT >= 4 ? i >= MT - 4 : true)
+#pragma unroll
+                        for (int p = MT >= 4 ? i - (MT - 4) : 0; p < (MT >= 4 ? i - (MT - 4) + 1 : 4); ++p) decode(codes, p, s, op[1 - h]);
+                    if (e == 1 && h == 1 && i > 0)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[j][i - 1] *= next.ratio;
+                    __builtin_amdgcn_sched_barrier(0);
                 }
+                if (e == 1 && h == 1)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[j][MT - 1] *= next.ratio;
             }
+            at = after;
+            after = free;
         }
-        u = u + 1 == S ? 0 : u + 1;
+        if (st + 2 < nst) now = next;
     }
 
+    wait_vmcnt<0>();                                       // zeros of stages past the last, on their way into LDS
+
     // A lane holds inputs 16 g .. of the wavefront's 64, element j of each four in acc[j].
-    const float last = scale.mantissa;
+    const float last = now.mantissa;
     const int k = k0 + 64 * wn + 16 * g;
     if (k >= a.K) return;
 #pragma unroll
@@ -266,21 +299,21 @@ __global__ void __launch_bounds__(256) f8_back_copy_kernel(const uint16_t *dy, u
     }
 }
 
-struct BackCfg { int WM, WN, MT, S; };
+struct BackCfg { int WM, WN, MT; };
 constexpr BackCfg CFGS[] = {
-    {2, 4, 8, 3},      // 256 x 256
-    {1, 4, 8, 2},      // 128 x 256
-    {1, 4, 4, 3},      // 64 x 256
-    {1, 4, 1, 4},      // 16 x 256
+    {2, 4, 8},      // 256 x 256
+    {2, 4, 4},      // 128 x 256
+    {1, 4, 4},      // 64 x 256
+    {1, 4, 1},      // 16 x 256
 };
 constexpr int NUM_CFGS = 4;
 
 template <int I, bool SPLIT>
 hipError_t launch_of(const F8BackArgs &a, hipStream_t st) {
     constexpr BackCfg t = CFGS[I];
-    constexpr size_t lds = back_lds<t.WM, t.WN, t.MT, t.S>();
+    constexpr size_t lds = back_lds<t.WM, t.WN, t.MT>();
     static_assert(lds <= LDS_BYTES_MAX, "fits");
-    auto kern = f8_back_kernel<t.WM, t.WN, t.MT, t.S, SPLIT>;
+    auto kern = f8_back_kernel<t.WM, t.WN, t.MT, SPLIT>;
     static LdsLimit limit;
     const hipError_t e = limit.raise((const void *)kern, int(lds));
     if (e != hipSuccess) return e;

@@ -182,21 +182,26 @@ __global__ void __launch_bounds__(64 * WK) f8_rows_kernel(F8Args a) {
 // order it goes from memory to the registers it is multiplied from, S stages ahead, and LDS holds and
 // serves the activations and their scales.
 //
-// A stage is one block of 128 inputs: 128-byte runs of the rows, whose 16-byte pieces are swizzled so
-// that sixteen rows' pieces spread over all banks, and the rows' scales, in the order that gives each
-// lane its MT consecutive words.  Operands are read P tiles ahead.  One barrier a stage, P tiles
-// before its end: by then every wavefront has read all of the stage's operands and the next stage has
+// A stage is BS blocks of 128 inputs: 128-byte runs of the rows, whose 16-byte pieces are swizzled so
+// that sixteen rows' pieces spread over all banks.  Operands are read P tiles ahead.  One barrier a stage, P
+// tiles before its end: by then every wavefront has read all of the stage's operands and the next stage has
 // arrived, so the rows of the stage S on go to this one's place.
+//
+// Scales come in panels of 32 blocks, 128 bytes of a row (and of the weight's rows of scales), swizzled in the
+// same way, the next panel while one is in use.  Taken block by block instead, 64 lanes a load fetched 64 cache
+// lines for four bytes of each.
 template <int MT>
 constexpr int ahead() { return MT >= 8 ? 3 : (MT >= 4 ? 2 : 1); }
 template <int MT>
 constexpr int x_bytes() { return 16 * MT * F8_BLOCK; }
-constexpr int SCALE_BYTES = 1024;                       // a stage's: 128 tokens' words and 64 of the weight's
+constexpr int PANEL_BLOCKS = 32;
+template <int MT>
+constexpr int panel_bytes() { return (16 * MT + 8) * PANEL_BLOCKS * 4; }   // the tokens' rows, and eight of the weight's
 template <int NT>
 constexpr int out_stride() { return NT * 32 + 16; }
-template <int WN, int WK, int MT, int NT, int S>
+template <int WN, int WK, int MT, int NT, int BS, int S>
 constexpr int tile_lds() {
-    const int ring = S * WK * (x_bytes<MT>() + SCALE_BYTES), rows = (WK - 1) * WN * MT * NT * 1024 + WN * 16 * out_stride<NT>();
+    const int ring = S * WK * BS * x_bytes<MT>() + 2 * panel_bytes<MT>(), rows = (WK - 1) * WN * MT * NT * 1024 + WN * 16 * out_stride<NT>();
     return ring > rows ? ring : rows;
 }
 
@@ -258,15 +263,17 @@ __device__ inline void store_tiles(const F8Args &a, const RowBlock &rb, int ct0,
 }
 
 // EXACT: through the bf16 matrix cores.
-template <int WN, int WK, int MT, int NT, int S, bool SPLIT, bool EXACT>
-__global__ void __launch_bounds__(64 * WN * WK) f8_tile_kernel(F8Args a) {
+template <int WN, int WK, int MT, int NT, int BS, int S, bool SPLIT, bool EXACT>
+__global__ void __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_eu(2))) f8_tile_kernel(F8Args a) {
     constexpr int MP = 16 * MT, NTT = NT * WN;
-    constexpr int XL = MP / 8 / WN;                        // 1 KiB loads of rows a wavefront and stage
-    constexpr int PER_STAGE = XL + 1 + 2 * NT;
+    constexpr int XL = MP / 8 / WN;                        // 1 KiB loads of a block's rows a wavefront
+    constexpr int PER_STAGE = BS * (XL + 2 * NT);
+    constexpr int Q = BS * MT;                             // token tiles of a stage's blocks, one after another
     constexpr int P = ahead<MT>(), XB = MT >= 4 ? 4 : 2;   // operands read ahead, and buffers for them
     static_assert(XL * WN * 8 == MP && XL >= 1, "loads divide evenly");
-    static_assert((S * MT) % XB == 0 && P < XB && P < MT, "buffers come round");
-    static_assert(F8_BLOCK % (16 * NT) == 0 && WN * 64 > MP && MP <= 128, "one weight scale a wavefront; one load of scales each");
+    static_assert((S * Q) % XB == 0 && P < XB && P < MT, "buffers come round");
+    static_assert(F8_BLOCK % (16 * NT) == 0 && NTT * TILE_N <= 8 * F8_BLOCK, "one weight scale a wavefront and block, eight rows of them");
+    static_assert(PANEL_BLOCKS % (BS * WK) == 0 && PANEL_BLOCKS / (BS * WK) > 2 * S, "a panel lasts longer than a load takes");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -292,72 +299,91 @@ __global__ void __launch_bounds__(64 * WN * WK) f8_tile_kernel(F8Args a) {
 
     const int kb0 = SPLIT ? int(blockIdx.y) * a.bps : 0;
     const int nkb = SPLIT ? min(a.kblocks - kb0, a.bps) : a.kblocks;
-    const int nst = (nkb + WK - 1) / WK;
+    const int nst = (nkb + BS * WK - 1) / (BS * WK);
 
     const __amdgpu_buffer_rsrc_t wr = make_uniform_rsrc(
         a.w + uint64_t(rb.expert) * a.w_stride + int64_t(nt0) * a.kblocks * F8_TILE_BYTES,
         uint32_t(nt_here) * uint32_t(a.kblocks) * F8_TILE_BYTES);
     const __amdgpu_buffer_rsrc_t xr = make_uniform_rsrc(a.x + int64_t(rb.first) * a.K, uint32_t(rb.count) * uint32_t(a.K));
-    // this wavefront's load of scales: 64 tokens', or the weight's
-    constexpr int SW = MP < 64 ? 1 : MP / 64;             // wavefronts that load tokens' scales
+    const __amdgpu_buffer_rsrc_t sr = make_uniform_rsrc(a.xs + int64_t(rb.first) * a.kblocks, uint32_t(rb.count) * uint32_t(a.kblocks) * 4u);
     const int nb0 = nt0 * TILE_N / F8_BLOCK, nb_here = min((NTT * TILE_N + F8_BLOCK - 1) / F8_BLOCK, a.nbs - nb0);
-    const bool tokens = wn < SW;
-    const __amdgpu_buffer_rsrc_t sr = make_uniform_rsrc(
-        tokens ? a.xs + int64_t(rb.first) * a.kblocks : a.ws + (int64_t(rb.expert) * a.nbs + nb0) * a.kblocks,
-        uint32_t(tokens ? rb.count : nb_here) * uint32_t(a.kblocks) * 4u);
+    const __amdgpu_buffer_rsrc_t vr =
+        make_uniform_rsrc(a.ws + (int64_t(rb.expert) * a.nbs + nb0) * a.kblocks, uint32_t(nb_here) * uint32_t(a.kblocks) * 4u);
 
-    uint32_t x_off[XL], s_off, w_off[NT];
+    const int k_first = kb0 + wk * BS;                     // first block of the wavefront's first stage
+    uint32_t x_off[XL], w_off[NT];
     int x_left[XL];                                        // inputs from the piece to the row's end
 #pragma unroll
     for (int q = 0; q < XL; ++q) {
         const int row = (wn + WN * q) * 8 + (lane >> 3), piece = (lane & 7) ^ ((row >> 1) & 7);
-        x_off[q] = row < rb.count ? uint32_t(row) * uint32_t(a.K) + uint32_t(kb0 + wk) * F8_BLOCK + 16u * uint32_t(piece) : OUT_OF_RANGE;
-        x_left[q] = a.K - (kb0 + wk) * F8_BLOCK - 16 * piece;
-    }
-    {
-        // word p of a stage's scales is token 16 (p mod MT) + p / MT; the weight's follow
-        const int p = wn * 64 + lane, row = tokens ? 16 * (p % MT) + p / MT : lane;
-        const bool real = tokens ? p < MP && row < rb.count : wn == SW && lane < nb_here;
-        s_off = real ? (uint32_t(row) * uint32_t(a.kblocks) + uint32_t(kb0 + wk)) * 4u : OUT_OF_RANGE;
+        x_off[q] = row < rb.count ? uint32_t(row) * uint32_t(a.K) + uint32_t(k_first) * F8_BLOCK + 16u * uint32_t(piece) : OUT_OF_RANGE;
+        x_left[q] = a.K - k_first * F8_BLOCK - 16 * piece;
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
         const int tile = wn * NT + j;
-        w_off[j] = tile < nt_here ? (uint32_t(tile) * uint32_t(a.kblocks) + uint32_t(kb0 + wk)) * F8_TILE_BYTES + 16u * lane : OUT_OF_RANGE;
+        w_off[j] = tile < nt_here ? (uint32_t(tile) * uint32_t(a.kblocks) + uint32_t(k_first)) * F8_TILE_BYTES + 16u * lane : OUT_OF_RANGE;
     }
-    constexpr int STAGE = x_bytes<MT>() + SCALE_BYTES;
+    constexpr int BLOCK = x_bytes<MT>(), STAGE = BS * BLOCK;
     uint8_t *const ring = lds + wk * (S * STAGE);
+    auto past = [&](int st, int b) { return (st * WK + wk) * BS + b < nkb ? 0u : OUT_OF_RANGE; };
     auto load_x = [&](int st, int u) {
-        const bool real = st * WK + wk < nkb;
 #pragma unroll
-        for (int q = 0; q < XL; ++q)
-            ld128_lds(xr, real && st * WK * F8_BLOCK < x_left[q] ? x_off[q] + uint32_t(st) * (WK * F8_BLOCK) : OUT_OF_RANGE,
-                      ring + u * STAGE + (wn + WN * q) * 1024);
-        // past the last stage the scales are zero, the products of zero weights with them too
-        ld32_lds(sr, real ? s_off + uint32_t(st) * (WK * 4) : OUT_OF_RANGE,
-                 ring + u * STAGE + x_bytes<MT>() + (wn < SW ? wn * 256 : (wn == SW ? 512 : 768)));
+        for (int b = 0; b < BS; ++b) {
+            const int on = st * WK * BS + b;               // blocks after the first
+            uint8_t *const to = ring + u * STAGE + b * BLOCK;
+#pragma unroll
+            for (int q = 0; q < XL; ++q)
+                ld128_lds(xr, on * F8_BLOCK < x_left[q] ? (x_off[q] + uint32_t(on) * F8_BLOCK) | past(st, b) : OUT_OF_RANGE,
+                          to + (wn + WN * q) * 1024);
+        }
     };
-    Operand w[S][NT], x[XB];
-    auto load_w = [&](int st, int u) {
-        const uint32_t past = st * WK + wk < nkb ? 0u : OUT_OF_RANGE;
+    uint8_t *const panels = lds + WK * S * STAGE;
+    constexpr int PANEL = panel_bytes<MT>();
+    // a wavefront's loads of a panel: eight rows each, the last of all the weight's
+    constexpr int PL = (MP / 8 + WN * WK) / (WN * WK);
+    uint32_t p_off[PL];
+#pragma unroll
+    for (int q = 0; q < PL; ++q) {
+        const int unit = wv + q * WN * WK, row = 8 * unit + (lane >> 3), mine = unit < MP / 8 ? row : row - MP;
+        p_off[q] = mine < (unit < MP / 8 ? rb.count : nb_here)
+                       ? (uint32_t(mine) * uint32_t(a.kblocks) + uint32_t(kb0 + 4 * ((lane & 7) ^ (row & 7)))) * 4u
+                       : OUT_OF_RANGE;
+    }
+    auto load_panel = [&](int at) {                        // blocks 32 at .. of this split
+#pragma unroll
+        for (int q = 0; q < PL; ++q) {
+            const int unit = wv + q * WN * WK;
+            uint8_t *const to = panels + (at & 1) * PANEL + unit * 1024;
+            if (unit < MP / 8) ld128_lds(sr, p_off[q] + uint32_t(at) * (PANEL_BLOCKS * 4), to);
+            else if (unit == MP / 8) ld128_lds(vr, p_off[q] + uint32_t(at) * (PANEL_BLOCKS * 4), to);
+        }
+    };
+    Operand w[S][BS][NT], x[XB];
+    auto load_w = [&](int st, int u, int b) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            w[u][j].lo = ld128(wr, (w_off[j] + uint32_t(st) * (WK * F8_TILE_BYTES)) | past);
-            w[u][j].hi = ld128(wr, (w_off[j] + uint32_t(st) * (WK * F8_TILE_BYTES) + 1024u) | past);
+            const uint32_t off = w_off[j] + uint32_t(st * WK * BS + b) * F8_TILE_BYTES;
+            w[u][b][j].lo = ld128(wr, off | past(st, b));
+            w[u][b][j].hi = ld128(wr, (off + 1024u) | past(st, b));
         }
     };
     const uint8_t *const x_at[2] = {ring + c * 128 + ((g ^ (c >> 1)) * 16), ring + c * 128 + (((4 + g) ^ (c >> 1)) * 16)};
-    const uint8_t *const s_at = ring + x_bytes<MT>() + c * (MT * 4);
-    const uint8_t *const v_at = ring + x_bytes<MT>() + 512 + ((nt0 + wn * NT) * TILE_N / F8_BLOCK - nb0) * 4;
-    auto read_x = [&](Operand &o, int u, int i) {
-        o.lo = *reinterpret_cast<const u32x4 *>(x_at[0] + u * STAGE + i * 2048);
-        o.hi = *reinterpret_cast<const u32x4 *>(x_at[1] + u * STAGE + i * 2048);
+    // token tile q of the stage in place u, those past its last from the next place
+    auto read_x = [&](Operand &o, int u, int q) {
+        const int at = (q < Q ? u : (u + 1) % S) * STAGE + q % Q / MT * BLOCK + q % MT * 2048;
+        o.lo = *reinterpret_cast<const u32x4 *>(x_at[0] + at);
+        o.hi = *reinterpret_cast<const u32x4 *>(x_at[1] + at);
     };
-    float f[MT], v;                                        // the tokens' scales, the weight's
-    auto read_scales = [&](int u) {
+    float f[MT], v;                                        // the tokens' scales of a block, the weight's
+    const int v_row = (nt0 + wn * NT) * TILE_N / F8_BLOCK - nb0;
+    auto read_scales = [&](int st, int b) {
+        const int block = (st * WK + wk) * BS + b, word = block & (PANEL_BLOCKS - 1);
+        const uint8_t *const panel = panels + (block / PANEL_BLOCKS & 1) * PANEL + (word & 3) * 4;
+        const uint8_t *const at = panel + c * 128 + (((word >> 2) ^ (c & 7)) * 16);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) f[i] = *reinterpret_cast<const float *>(s_at + u * STAGE + 4 * i);
-        v = *reinterpret_cast<const float *>(v_at + u * STAGE);
+        for (int i = 0; i < MT; ++i) f[i] = *reinterpret_cast<const float *>(at + i * 2048);
+        v = *reinterpret_cast<const float *>(panel + (MP + v_row) * 128 + (((word >> 2) ^ v_row) * 16));
     };
 
     f32x4 acc[NT][MT];
@@ -366,59 +392,76 @@ __global__ void __launch_bounds__(64 * WN * WK) f8_tile_kernel(F8Args a) {
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
+    load_panel(0);
+    load_panel(1);
 #pragma unroll
     for (int u = 0; u < S; ++u) {
         load_x(u, u);
         __builtin_amdgcn_sched_barrier(0);                 // the waits count loads in this order
-        load_w(u, u);
+#pragma unroll
+        for (int b = 0; b < BS; ++b) load_w(u, u, b);
         __builtin_amdgcn_sched_barrier(0);
     }
     wait_vmcnt<(S - 1) * PER_STAGE>();
     ring_barrier();
 #pragma unroll
     for (int i = 0; i < P; ++i) read_x(x[i], 0, i);
-    read_scales(0);
+    read_scales(0, 0);
 
     // Stage st in place u.  A tile's sums are joined while the next tile's instructions run.
     auto stage = [&](int st, int u, bool more) {
-        float s[MT];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) s[i] = f[i] * v;
         f32x4 sum[2][NT];
-        Wide wide[EXACT ? NT : 1];
-        if constexpr (EXACT)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) wide[j] = widen(w[u][j]);
+        for (int b = 0; b < BS; ++b) {
+            float s[MT];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            if (i == MT - P) {
-                if (more) wait_vmcnt<(S - 2) * PER_STAGE>();
-                ring_barrier();
-                if (more) load_x(st + S, u);
+            for (int i = 0; i < MT; ++i) {
+                s[i] = f[i] * v;
+                // past the last block: weights that read as zero, but whatever scales lie there
+                if (BS * WK > 1 && past(st, b)) s[i] = 0.0f;
+            }
+            Wide wide[EXACT ? NT : 1];
+            if constexpr (EXACT)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) wide[j] = widen(w[u][b][j]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const int q = b * MT + i;
+                if (q == Q - P) {
+                    // weights of the stage S on that are under way already
+                    if (more) wait_vmcnt<(S - 2) * PER_STAGE + (BS - 1) * 2 * NT>();
+                    ring_barrier();
+                    if (more) load_x(st + S, u);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (i == MT - P) read_scales(b + 1 < BS ? st : st + 1, (b + 1) % BS);
+                if constexpr (EXACT) {
+                    const Wide xw = widen(x[(u * Q + q) % XB]);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) sum[i & 1][j] = block_product(wide[j], xw);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) sum[i & 1][j] = block_product(w[u][b][j], x[(u * Q + q) % XB]);
+                }
+                read_x(x[(u * Q + q + P) % XB], u, q + P);
+                __builtin_amdgcn_sched_barrier(0);         // joined first, the last sums would be waited for
+                if (i > 0)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) join(acc[j][i - 1], sum[(i - 1) & 1][j], s[i - 1]);
                 __builtin_amdgcn_sched_barrier(0);
-                read_scales((u + 1) % S);
             }
-            if constexpr (EXACT) {
-                const Wide xw = widen(x[(u * MT + i) % XB]);
-#pragma unroll
-                for (int j = 0; j < NT; ++j) sum[i & 1][j] = block_product(wide[j], xw);
-            } else {
-#pragma unroll
-                for (int j = 0; j < NT; ++j) sum[i & 1][j] = block_product(w[u][j], x[(u * MT + i) % XB]);
-            }
-            read_x(x[(u * MT + i + P) % XB], i + P < MT ? u : (u + 1) % S, (i + P) % MT);
-            if (i > 0)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) join(acc[j][i - 1], sum[(i - 1) & 1][j], s[i - 1]);
+            if (more) load_w(st + S, u, b);
             __builtin_amdgcn_sched_barrier(0);
-        }
 #pragma unroll
-        for (int j = 0; j < NT; ++j) join(acc[j][MT - 1], sum[(MT - 1) & 1][j], s[MT - 1]);
-        if (more) load_w(st + S, u);
-        __builtin_amdgcn_sched_barrier(0);
+            for (int j = 0; j < NT; ++j) join(acc[j][MT - 1], sum[(MT - 1) & 1][j], s[MT - 1]);
+        }
     };
-    int st = 0;
+    int st = 0, panel = 2;
     for (; st + S <= nst; st += S) {
+        // Every wavefront has read the scales of stage st - 1: the panel before its own is free.  The next is read C - S
+        // stages on at the earliest, and the waits, which count its loads as a stage's, have seen to them by then.
+        constexpr int C = PANEL_BLOCKS / (BS * WK);
+        if (st > (panel - 1) * C) load_panel(panel++);
 #pragma unroll
         for (int u = 0; u < S; ++u) stage(st + u, u, true);
     }
@@ -480,14 +523,17 @@ __global__ void __launch_bounds__(256) f8_join_kernel(F8Args a) {
 
 // Schedules.  kind 0 (few rows): NT column tiles a workgroup, WK wavefronts on alternate blocks; kind
 // 1 (tiles): WN wavefronts of MT x NT tiles, WK times on alternate stages, a ring of S stages.
-struct F8Cfg { int kind, MT, NT, WK, WN, S; };
+struct F8Cfg { int kind, MT, NT, WK, WN, BS, S; };
 constexpr F8Cfg CFGS[] = {
-    {0, 1, 1, 8, 1, 0}, {0, 1, 2, 8, 1, 0},
-    {1, 8, 2, 1, 8, 3},      // 128 x 256
-    {1, 8, 1, 1, 8, 4},      // 128 x 128
-    {1, 4, 2, 1, 4, 4},      // 64 x 128
-    {1, 4, 1, 2, 4, 4},      // 64 x 64, two groups
-    {1, 2, 1, 2, 4, 6},      // 32 x 64, two groups
+    {0, 1, 1, 8, 1, 1, 0}, {0, 1, 2, 8, 1, 1, 0},
+    {1, 8, 2, 1, 8, 1, 3},      // 128 x 256
+    {1, 8, 1, 1, 8, 1, 4},      // 128 x 128
+    {1, 4, 2, 1, 4, 1, 4},      // 64 x 128
+    {1, 4, 1, 2, 4, 1, 4},      // 64 x 64, two groups
+    {1, 2, 1, 2, 4, 1, 6},      // 32 x 64, two groups
+#ifdef EXTRA
+    EXTRA
+#endif
 };
 constexpr int NUM_CFGS = 7, FIRST_TILE = 2;
 constexpr int ROWS_U = 2;
@@ -503,9 +549,9 @@ hipError_t launch_rows(const F8Args &a, hipStream_t st) {
 template <int I, bool SPLIT, bool EXACT>
 hipError_t launch_tiles_of(const F8Args &a, hipStream_t st) {
     constexpr F8Cfg t = CFGS[I];
-    constexpr size_t lds = tile_lds<t.WN, t.WK, t.MT, t.NT, t.S>();
+    constexpr size_t lds = tile_lds<t.WN, t.WK, t.MT, t.NT, t.BS, t.S>();
     static_assert(lds <= LDS_BYTES_MAX, "fits");
-    auto kern = f8_tile_kernel<t.WN, t.WK, t.MT, t.NT, t.S, SPLIT, EXACT>;
+    auto kern = f8_tile_kernel<t.WN, t.WK, t.MT, t.NT, t.BS, t.S, SPLIT, EXACT>;
     static LdsLimit limit;
     const hipError_t e = limit.raise((const void *)kern, int(lds));
     if (e != hipSuccess) return e;
