@@ -34,17 +34,17 @@ struct Scale {
     uint32_t lo, hi;                                       // permutations: inputs 0 and 1, 2 and 3 of two channels
 };
 __device__ inline Scale split_scale(float s, float before) {
+    asm("" : "+v"(s));                                     // selections, where a uniform value would make branches
     const uint32_t b = __float_as_uint(s), e = (b >> 23) & 0xFFu;
-    Scale r{s, 1.0f, 1.0f, 0x05010400u, 0x07030602u};
-    if (e == 0u) {
-        r.mantissa = s * 8.507059173023462e37f;            // 2^126
-        r.power = 1.1754943508222875e-38f;                 // 2^-126
-    } else if (e != 0xFFu) {
-        r.mantissa = __uint_as_float((b & 0x807FFFFFu) | 0x3F800000u);
-        r.power = __uint_as_float(e << 23);
-    }
-    if (s == 0.0f) return Scale{before, 1.0f, 1.0f, 0x0C0C0C0Cu, 0x0C0C0C0Cu};
+    const bool none = s == 0.0f, tiny = e == 0u, special = e == 0xFFu;
+    Scale r;
+    r.mantissa = tiny ? s * 8.507059173023462e37f          // 2^126
+                      : special ? s : __uint_as_float((b & 0x807FFFFFu) | 0x3F800000u);
+    r.mantissa = none ? before : r.mantissa;
+    r.power = tiny ? 1.1754943508222875e-38f : special ? 1.0f : __uint_as_float(e << 23);   // 2^-126
     r.ratio = before / r.mantissa;
+    r.lo = none ? 0x0C0C0C0Cu : 0x05010400u;
+    r.hi = none ? 0x0C0C0C0Cu : 0x07030602u;
     return r;
 }
 
@@ -57,9 +57,11 @@ __device__ inline uint32_t widen2(uint32_t codes, float power) {
 // Workgroup: WM x WN wavefronts, each 16 MT tokens x 64 inputs; three stages of 64 channels in LDS.
 //
 // Weight.  The operand of inputs (the A operand) needs eight channels of one input in a lane, packed tiles
-// hold sixteen inputs of one channel.  A stage's 64 x 64 codes of a wavefront column lie in LDS as rows of 64
-// bytes, the row of channel 8 p + q of a step of 32 at 4 q + p, so that lane (c, g) reads inputs 4 c .. 4 c +
-// 3 of channel 8 g + q in one word, 64 words in a row over the lanes: no bank is hit twice.  Eight such words are
+// hold sixteen inputs of one channel.  A stage's 64 x 64 codes of a wavefront column lie in LDS as four planes of
+// sixteen inputs, 64 channels of 16 bytes each; channel 32 h + 8 g + 4 p + q of the stage at 32 h + 16 p + 4 g + q.  Lane (c,
+// g) reads inputs 4 c .. 4 c + 3 of channel 8 g + r of step h in one word, from plane c / 4; planes are 1040 bytes apart,
+// so that the 64 words lie in 64 banks.  Loaded in this order, four lanes fetch 64 bytes in a row (with channels
+// 8 apart beside each other, 16 bytes each, the loads took as long as all else).  Eight such words are
 // four operands, of inputs 4 c + j for j = 0 .. 3, after eight byte permutes and sixteen conversions.  Their sums
 // leave a lane with sixteen consecutive inputs of a token, 32 bytes of bf16, which are stored as they are.
 //
@@ -68,14 +70,15 @@ __device__ inline uint32_t widen2(uint32_t codes, float power) {
 // A stage is two steps of 32 channels.  During a step the next one's codes are read and turned into operands between
 // the matrix instructions.  A barrier before each step: the first of a stage frees the stage before it, whose place
 // takes the loads of the stage after next; the second waits for the next stage.
+constexpr int PLANE = 1040;
 template <int WM, int WN, int MT>
-constexpr int back_lds() { return 3 * (16 * MT * WM * 128 + WN * 4096) + (2 * MT * WM < WM * WN ? 1024 : 0); }
+constexpr int back_lds() { return 3 * (16 * MT * WM * 128 + WN * 4 * PLANE) + (2 * MT * WM < WM * WN ? 1024 : 0); }
 
 template <int WM, int WN, int MT, bool SPLIT>
 __global__ void __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2))) f8_back_kernel(F8BackArgs a) {
     constexpr int S = 3, W = WM * WN, MP = 16 * MT * WM, KP = 64 * WN;
     constexpr int P = MT >= 4 ? 3 : 1, XB = MT >= 4 ? 4 : 2;
-    constexpr int X_BYTES = MP * 128, STAGE = X_BYTES + WN * 4096;
+    constexpr int X_BYTES = MP * 128, STAGE = X_BYTES + WN * 4 * PLANE;
     constexpr int XL = MP / 8, WL = 4 * WN;                // 1 KiB loads of a stage
     constexpr int XLW = (XL + W - 1) / W, WLW = WL / W, LOADS = XLW + WLW;
     static_assert(WL % W == 0 && (XL % W == 0 || XL < W), "every wavefront issues the same loads");
@@ -112,44 +115,33 @@ __global__ void __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_
     const float *const ws = a.ws + (int64_t(rb.expert) * a.nbs + nb0) * a.kblocks;
     const int kb = min((k0 + 64 * wn) / F8_BLOCK, a.kblocks - 1);
 
-    uint32_t x_off[XLW];
-    int x_left[XLW];                                       // channels from the piece to the row's end
-#pragma unroll
-    for (int q = 0; q < XLW; ++q) {
-        const int row = (wv + W * q) * 8 + (lane >> 3), piece = (lane & 7) ^ ((row >> 1) & 7);
-        x_off[q] = row < rb.count ? uint32_t(row) * uint32_t(a.ldy) * 2u + uint32_t(nb0) * (2 * F8_BLOCK) + 16u * uint32_t(piece) : OUT_OF_RANGE;
-        x_left[q] = int(a.ldy) - nb0 * F8_BLOCK - 8 * piece;
-    }
-    // Load q of a wavefront: a quarter of the codes of wavefront column `col`, step `h`, rows 16 r ..  The
-    // four channel tiles of a stage are kblocks tiles apart each.
-    uint32_t w_off[WLW];
+    // A wavefront's first loads of a stage; the others lie a fixed distance on.  Rows past the last lie past the range.
+    // Inputs past the last are read from whatever lies there, and their sums are not stored.
+    const int row = wv * 8 + (lane >> 3), piece = (lane & 7) ^ ((row >> 1) & 7);
+    static_assert(W % 2 == 0, "a wavefront's rows have one swizzle");
+    const uint32_t x_off = uint32_t(row) * uint32_t(a.ldy) * 2u + uint32_t(nb0) * (2 * F8_BLOCK) + 16u * uint32_t(piece);
+    const uint32_t x_far = uint32_t(W * 8) * uint32_t(a.ldy) * 2u;
+    const int x_left = int(a.ldy) - nb0 * F8_BLOCK - 8 * piece;   // channels from the piece to the row's end
+    // a load takes one plane of a wavefront column; the four channel tiles of a stage are kblocks tiles apart each
     const uint32_t tile_step = uint32_t(a.kblocks) * F8_TILE_BYTES;
     const int tiles_here = min(a.ntiles - nb0 * 8, nbs * 8);
-#pragma unroll
-    for (int q = 0; q < WLW; ++q) {
-        const int unit = wv + W * q, col = unit >> 2, h = (unit >> 1) & 1, r = unit & 1;
-        const int n = 8 * ((lane >> 2) & 3) + 4 * r + (lane >> 4);          // channel of the step
-        const int k = k0 + 64 * col + 16 * (lane & 3);
-        w_off[q] = k < a.K ? uint32_t(2 * h + (n >> 4)) * tile_step + uint32_t(k / F8_BLOCK) * F8_TILE_BYTES +
-                                 uint32_t((k >> 6) & 1) * 1024u + uint32_t(16 * (lane & 3) + (n & 15)) * 16u
-                           : OUT_OF_RANGE;
-    }
+    const int channel = 32 * (lane >> 5) + 8 * ((lane >> 2) & 3) + 4 * ((lane >> 4) & 1) + (lane & 3);   // of the stage
+    const int k_load = k0 + 64 * (wv >> 2);
+    static_assert(W % 4 == 0 && F8_TILE_BYTES == 2048, "four planes; a column is 1 KiB after the one before");
+    const uint32_t w_off = uint32_t(channel >> 4) * tile_step + uint32_t(k_load >> 6) * 1024u + uint32_t(16 * (wv & 3) + (channel & 15)) * 16u;
     auto load = [&](int st, int place) {
         uint8_t *const base = lds + place;
+        const bool more = (st < nst) & (st * 64 < x_left);
 #pragma unroll
         for (int q = 0; q < XLW; ++q) {
-            if (XL < W && wv >= XL) {                      // nothing left to load: zeros to a place of their own
-                ld128_lds(xr, OUT_OF_RANGE, lds + S * STAGE);
-                continue;
-            }
-            ld128_lds(xr, st < nst && st * 64 < x_left[q] ? x_off[q] + uint32_t(st) * 128u : OUT_OF_RANGE, base + (wv + W * q) * 1024);
+            if (XL < W && wv >= XL) ld128_lds(xr, OUT_OF_RANGE, lds + S * STAGE);   // nothing left: zeros to a place of their own
+            else ld128_lds(xr, more ? x_off + uint32_t(q) * x_far + uint32_t(st) * 128u : OUT_OF_RANGE, base + (wv + W * q) * 1024);
         }
         // four tiles a stage, those past the last read as zero
-        const int left = min(4, tiles_here - 4 * st);
-        const __amdgpu_buffer_rsrc_t wr =
-            make_uniform_rsrc(w + int64_t(nb0 * 8 + (left > 0 ? 4 * st : 0)) * tile_step, left > 0 ? uint32_t(left) * tile_step : 0u);
+        const int left = max(0, min(4, tiles_here - 4 * st));
+        const __amdgpu_buffer_rsrc_t wr = make_uniform_rsrc(w + int64_t(nb0 * 8 + min(4 * st, tiles_here)) * tile_step, uint32_t(left) * tile_step);
 #pragma unroll
-        for (int q = 0; q < WLW; ++q) ld128_lds(wr, w_off[q], base + X_BYTES + (wv + W * q) * 1024);
+        for (int q = 0; q < WLW; ++q) ld128_lds(wr, w_off + uint32_t(q * (W / 4)) * 1024u, base + X_BYTES + (wv + W * q) * PLANE);
     };
 
     f32x4 acc[4][MT];
@@ -160,13 +152,13 @@ __global__ void __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_
 
     const uint8_t *const x_at[2] = {lds + (wm * MT * 16 + c) * 128 + ((g ^ (c >> 1)) * 16),
                                     lds + (wm * MT * 16 + c) * 128 + (((4 + g) ^ (c >> 1)) * 16)};
-    const uint8_t *const w_at = lds + X_BYTES + wn * 4096 + g * 64 + c * 4;
+    const uint8_t *const w_at = lds + X_BYTES + (4 * wn + (c >> 2)) * PLANE + g * 64 + (c & 3) * 4;
     struct Codes {
         uint32_t v[8];
     };
     auto read_w = [&](Codes &o, int stage, int h) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) o.v[q] = *reinterpret_cast<const uint32_t *>(w_at + stage + h * 2048 + q * 256);
+        for (int q = 0; q < 8; ++q) o.v[q] = *reinterpret_cast<const uint32_t *>(w_at + stage + h * 512 + (q >> 2) * 256 + (q & 3) * 16);
     };
     // Channels 2 p and 2 p + 1 of each lane's eight.
     auto decode = [&](const Codes &o, int p, const Scale &s, u32x4 (&op)[4]) {
@@ -188,7 +180,7 @@ __global__ void __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_
     ring_barrier();
     float s_next = ws[kb];
     Scale now = split_scale(s_next, 1.0f), next = now;
-    if (nst > 2) s_next = ws[a.kblocks + kb];
+    s_next = ws[int64_t(min(1, nbs - 1)) * a.kblocks + kb];
     {
         Codes first;
         read_w(first, 0, 0);
@@ -208,9 +200,10 @@ __global__ void __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_
                 ring_barrier();
                 if (h == 0) load(st + e + 2, free);
                 if (e == 1 && h == 1) {
-                    next = st + 2 < nst ? split_scale(s_next, now.mantissa) : now;
-                    if (st + 2 >= nst) next.ratio = 1.0f;
-                    if (st + 4 < nst) s_next = ws[int64_t((st >> 1) + 2) * a.kblocks + kb];
+                    next = split_scale(s_next, now.mantissa);
+                    next.ratio = st + 2 < nst ? next.ratio : 1.0f;
+                    next.mantissa = st + 2 < nst ? next.mantissa : now.mantissa;
+                    s_next = ws[int64_t(min((st >> 1) + 2, nbs - 1)) * a.kblocks + kb];
                 }
                 Codes codes;
                 read_w(codes, h == 0 ? at : after, 1 - h);
@@ -239,7 +232,7 @@ __global__ void __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_
             at = after;
             after = free;
         }
-        if (st + 2 < nst) now = next;
+        now = next;
     }
 
     wait_vmcnt<0>();                                       // zeros of stages past the last, on their way into LDS
