@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(1024) order_count_kernel(OrderArgs a) {
 // A run of slots a workgroup, a part of it to each wavefront in order.  A slot's place is the number of
 // slots of smaller experts, of its own in earlier workgroups and wavefronts, and of its own before it in this
 // wavefront: the first from the counts, the last from a comparison of ids over the lanes, 64 slots at a time.
-// One launch for up to 16384 slots; more have their runs counted by a launch before.
+// One launch for up to 4096 slots; more have their runs counted by a launch before.
 __global__ void __launch_bounds__(64 * ORDER_WAVES) order_place_kernel(OrderArgs a) {
     extern __shared__ int32_t hist[];                      // [ORDER_WAVES][E], then the next place of each
     __shared__ int32_t sums[ORDER_WAVES + 1];
@@ -273,13 +273,12 @@ __global__ void __launch_bounds__(256) combine_back_kernel(CombineArgs a) {
 
 }  // namespace
 
+// One workgroup takes up to 4096 slots, four steps of its wavefronts.  More slots are cut into runs of 1024, one step
+// each, after a launch that counts them (24594 slots: 12.0 us in runs of 4096, see the header for these), and into
+// longer ones past 64 runs, whose counts every workgroup reads.
 OrderPlan make_order_plan(int64_t n, int64_t E) {
     OrderPlan p;
-    p.per = 16384;
-    if (n > p.per) {
-        // more workgroups than 64 would read more counts than slots
-        p.per = std::max<int64_t>(4096, ceil_div(ceil_div(n, 64), 1024) * 1024);
-    }
+    p.per = n <= 4096 ? 4096 : std::max<int64_t>(1024, ceil_div(ceil_div(n, 64), 1024) * 1024);
     p.wgs = std::max<int64_t>(1, ceil_div(n, p.per));
     p.ws_bytes = p.wgs > 1 ? round256(size_t(p.wgs) * size_t(E) * 4) : 0;
     return p;

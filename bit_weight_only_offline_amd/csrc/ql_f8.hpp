@@ -82,7 +82,7 @@ struct F8Args {
     int out_f32;
 };
 
-F8Plan make_f8_plan(const F8Layout &L, int64_t M, bool grouped);
+F8Plan make_f8_plan(const F8Layout &L, int64_t M, bool grouped, bool f32);
 hipError_t launch_f8_forward(const F8Layout &L, const F8Plan &p, const F8Args &a, hipStream_t st);
 
 // Backward products  dx = sum over channel blocks of scale (dy . codes).

@@ -121,8 +121,9 @@ ql_status qlinear_f8_unpack(int64_t E, int64_t N, int64_t K, const void *packed,
                                      (hipStream_t)stream));
 }
 
-ql_status qlinear_f8_default_schedule(int64_t M, int64_t E, int64_t N, int64_t K, int grouped, int backward, ql_schedule *out) {
-    if (!out || (backward != 0 && backward != 1)) return QL_E_ARG;
+ql_status qlinear_f8_default_schedule(int64_t M, int64_t E, int64_t N, int64_t K, int grouped, int backward,
+                                      ql_dtype out_dtype, ql_schedule *out) {
+    if (!out || !known(out_dtype) || (backward != 0 && backward != 1)) return QL_E_ARG;
     const ql_status st = check_product(M, E, N, K, grouped);
     if (st != QL_OK) return st;
     if (M == 0) return QL_E_SHAPE;
@@ -131,17 +132,18 @@ ql_status qlinear_f8_default_schedule(int64_t M, int64_t E, int64_t N, int64_t K
         const F8BackPlan p = make_f8_back_plan(L, M, grouped != 0);
         *out = ql_schedule{p.cfg, p.ks};
     } else {
-        const F8Plan p = make_f8_plan(L, M, grouped != 0);
+        const F8Plan p = make_f8_plan(L, M, grouped != 0, out_dtype == QL_F32);
         *out = ql_schedule{p.cfg, p.ks};
     }
     return QL_OK;
 }
 
-ql_status qlinear_f8_workspace_bytes(int64_t M, int64_t E, int64_t N, int64_t K, int grouped, size_t *bytes) {
-    if (!bytes) return QL_E_ARG;
+ql_status qlinear_f8_workspace_bytes(int64_t M, int64_t E, int64_t N, int64_t K, int grouped, ql_dtype out_dtype,
+                                     size_t *bytes) {
+    if (!bytes || !known(out_dtype)) return QL_E_ARG;
     const ql_status st = check_product(M, E, N, K, grouped);
     if (st != QL_OK) return st;
-    *bytes = M ? make_f8_plan(make_f8_layout(E, N, K), M, grouped != 0).ws_bytes : 0;
+    *bytes = M ? make_f8_plan(make_f8_layout(E, N, K), M, grouped != 0, out_dtype == QL_F32).ws_bytes : 0;
     return QL_OK;
 }
 
@@ -158,7 +160,7 @@ ql_status qlinear_f8_forward(const void *codes, const float *scales, int64_t M, 
         !aligned(tokens_per_expert, 4) || !aligned(bias, 2) || !aligned(out, width(out_dtype)))
         return QL_E_ALIGN;
     const F8Layout L = make_f8_layout(E, N, K);
-    const F8Plan p = make_f8_plan(L, M, grouped != 0);
+    const F8Plan p = make_f8_plan(L, M, grouped != 0, out_dtype == QL_F32);
     if (!fits(p)) return QL_E_SHAPE;
     if (p.ws_bytes) {
         if (!workspace || workspace_bytes < p.ws_bytes) return QL_E_WORKSPACE;

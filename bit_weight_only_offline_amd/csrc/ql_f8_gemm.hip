@@ -522,21 +522,35 @@ __global__ void __launch_bounds__(256) f8_join_kernel(F8Args a) {
 }
 
 // Schedules.  kind 0 (few rows): NT column tiles a workgroup, WK wavefronts on alternate blocks; kind
-// 1 (tiles): WN wavefronts of MT x NT tiles, WK times on alternate stages, a ring of S stages.
+// 1 (tiles): WN wavefronts of MT x NT tiles, WK times on alternate stages of BS blocks, a ring of S stages.
 struct F8Cfg { int kind, MT, NT, WK, WN, BS, S; };
 constexpr F8Cfg CFGS[] = {
     {0, 1, 1, 8, 1, 1, 0}, {0, 1, 2, 8, 1, 1, 0},
     {1, 8, 2, 1, 8, 1, 3},      // 128 x 256
-    {1, 8, 1, 1, 8, 1, 4},      // 128 x 128
+    {1, 4, 2, 1, 8, 1, 4},      // 64 x 256
     {1, 4, 2, 1, 4, 1, 4},      // 64 x 128
     {1, 4, 1, 2, 4, 1, 4},      // 64 x 64, two groups
+    {1, 2, 2, 1, 4, 1, 6},      // 32 x 128
     {1, 2, 1, 2, 4, 1, 6},      // 32 x 64, two groups
 #ifdef EXTRA
     EXTRA
 #endif
 };
-constexpr int NUM_CFGS = 7, FIRST_TILE = 2;
+constexpr int NUM_CFGS = 8, FIRST_TILE = 2;
 constexpr int ROWS_U = 2;
+// Microseconds that a compute unit takes for one block of a workgroup's tile, and for the tile besides (start, first
+// loads, stores); and what a round of 256 workgroups after the first takes of either, less where several share a unit,
+// more where the operands of more workgroups pass through the caches.  For results in bf16 and, through the bf16 cores,
+// in float32.  Fitted to 60 sizes each, 20 to 8192 x 4096 x 14336, 14336 x 4096, 4096 x 4096, 5001 x 4128 and 2048 x
+// 2048, every schedule in one to eight splits; the choice was within 6% of the fastest at each.
+struct F8Rate { float block, tile, tile_more, block_more; };
+constexpr F8Rate RATES[2][NUM_CFGS] = {
+    {{0.105f, 5.1f, 0.18f, 1.11f}, {0.105f, 5.1f, 0.18f, 1.11f}, {0.80f, 6.6f, 0.24f, 1.31f}, {0.433f, 5.7f, 0.09f, 1.54f},
+     {0.296f, 5.6f, 0.0f, 1.05f}, {0.20f, 5.0f, 0.36f, 1.04f}, {0.20f, 5.0f, 0.0f, 1.09f}, {0.104f, 5.15f, 0.1f, 1.2f}},
+    {{0.086f, 6.3f, 0.01f, 1.49f}, {0.086f, 6.3f, 0.01f, 1.49f}, {1.195f, 18.1f, 0.84f, 1.2f}, {0.629f, 12.6f, 0.24f, 1.73f},
+     {0.421f, 7.3f, 0.63f, 0.79f}, {0.337f, 5.6f, 0.53f, 1.04f}, {0.312f, 6.5f, 0.17f, 0.93f}, {0.169f, 6.2f, 0.14f, 1.05f}},
+};
+constexpr float JOIN_US[2] = {4.0f, 3.1f}, JOIN_BYTES_PER_US[2] = {7.8e6f, 2.0e7f};
 
 template <int I>
 hipError_t launch_rows(const F8Args &a, hipStream_t st) {
@@ -563,8 +577,10 @@ hipError_t launch_tiles_of(const F8Args &a, hipStream_t st) {
 
 template <int I>
 hipError_t launch_tiles(const F8Args &a, hipStream_t st) {
-    if (a.ks == 1) return a.out_f32 ? launch_tiles_of<I, false, true>(a, st) : launch_tiles_of<I, false, false>(a, st);
-    const hipError_t e = a.out_f32 ? launch_tiles_of<I, true, true>(a, st) : launch_tiles_of<I, true, false>(a, st);
+    // the largest tiles are not split
+    if (I == FIRST_TILE || a.ks == 1) return a.out_f32 ? launch_tiles_of<I, false, true>(a, st) : launch_tiles_of<I, false, false>(a, st);
+    constexpr bool SPLIT = I != FIRST_TILE;
+    const hipError_t e = a.out_f32 ? launch_tiles_of<I, SPLIT, true>(a, st) : launch_tiles_of<I, SPLIT, false>(a, st);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(f8_join_kernel, elementwise_grid(int64_t(a.r.rows) * a.ntiles * 4), dim3(256), 0, st, a);
     return hipGetLastError();
@@ -572,31 +588,48 @@ hipError_t launch_tiles(const F8Args &a, hipStream_t st) {
 
 }  // namespace
 
-F8Plan make_f8_plan(const F8Layout &L, int64_t M, bool grouped) {
+// Up to 16 rows, an expert's on average, stream the weight through registers.  More take the schedule and the split of
+// the input dimension whose time is least by the measured rates.  A grouped product's row blocks are taken to
+// be half a block an expert more than its rows fill; it is not split.
+F8Plan make_f8_plan(const F8Layout &L, int64_t M, bool grouped, bool f32) {
     F8Plan p;
     p.bps = int(L.kblocks);
-    auto blocks = [&](int c, int64_t &mt, int64_t &nb) {
-        const F8Cfg &t = CFGS[c];
-        mt = most_row_blocks(M, L.E, grouped, 16 * t.MT);
-        nb = ceil_div(L.ntiles, t.NT * t.WN);
-    };
     const int64_t used = grouped ? std::min(L.E, M) : 1;
-    const int64_t each = ceil_div(M, used);
-    int64_t mt, nb;
-    if (each <= 16 && most_row_blocks(M, L.E, grouped, 16) <= 65535) {
+    auto columns = [&](const F8Cfg &t) { return ceil_div(L.ntiles, t.NT * t.WN); };
+    auto threads = [&](int c) {
+        const F8Cfg &t = CFGS[c];
+        const int64_t mt = most_row_blocks(M, L.E, grouped, 16 * t.MT);
+        return (t.kind == 0 ? columns(t) : ceil_div(mt * columns(t), 8) * 8) * 64 * t.WK * t.WN;
+    };
+    const bool rows_fit = most_row_blocks(M, L.E, grouped, 16) <= 65535;    // the grid dimension that holds them
+    if (M <= 16 * used && rows_fit) {
         p.cfg = L.ntiles <= 512 ? 0 : 1;
     } else {
-        p.cfg = NUM_CFGS - 1;
-        for (int c = FIRST_TILE; c < NUM_CFGS; ++c) {
-            blocks(c, mt, nb);
-            if (mt * nb >= 256) { p.cfg = c; break; }
+        float best = 0.0f;
+        for (int c = M <= 64 * used && rows_fit ? 1 : FIRST_TILE; c < NUM_CFGS; ++c) {
+            const F8Cfg &t = CFGS[c];
+            const F8Rate &rate = RATES[f32][c];
+            if (c > FIRST_TILE && threads(c) > LAUNCH_THREADS_MAX) continue;    // where the largest do not fit, none does
+            const int64_t block = 16 * t.MT, mt = grouped ? std::max(used, ceil_div(2 * M + used * block, 2 * block)) : ceil_div(M, block);
+            for (int ks : {1, 2, 4, 8}) {
+                const int64_t step = t.WK * t.BS, bps = ks == 1 ? L.kblocks : ceil_div(ceil_div(L.kblocks, ks), step) * step;
+                if (ks > 1 && (c <= FIRST_TILE || grouped || bps < 4 * step || ceil_div(L.kblocks, bps) < ks)) break;
+                const float more = float(ceil_div(mt * columns(t) * ks, 256) - 1);
+                float us = (1.0f + more * rate.block_more) * float(bps) * rate.block + (1.0f + more * rate.tile_more) * rate.tile;
+                if (ks > 1) us += JOIN_US[f32] + float(ks) * float(M) * float(L.ntiles) * TILE_N * 8.0f / JOIN_BYTES_PER_US[f32];
+                if (best == 0.0f || us < best) {
+                    best = us;
+                    p.cfg = c;
+                    p.ks = ks;
+                    p.bps = int(bps);
+                }
+            }
         }
     }
-    blocks(p.cfg, mt, nb);
-    p.mtiles = mt;
-    p.nblocks = nb;
     const F8Cfg &t = CFGS[p.cfg];
-    p.threads = (t.kind == 0 ? nb : ceil_div(mt * nb, 8) * 8) * 64 * t.WK * t.WN;
+    p.mtiles = most_row_blocks(M, L.E, grouped, 16 * t.MT);
+    p.nblocks = columns(t);
+    p.threads = threads(p.cfg);
     if (p.ks > 1) p.ws_bytes = round256(size_t(p.ks) * size_t(M) * size_t(L.ntiles) * TILE_N * 4);
     return p;
 }
@@ -620,7 +653,8 @@ hipError_t launch_f8_forward(const F8Layout &L, const F8Plan &p, const F8Args &a
         case 3: return launch_tiles<3>(a, st);
         case 4: return launch_tiles<4>(a, st);
         case 5: return launch_tiles<5>(a, st);
-        default: return launch_tiles<6>(a, st);
+        case 6: return launch_tiles<6>(a, st);
+        default: return launch_tiles<7>(a, st);
     }
 }
 

@@ -55,8 +55,8 @@ def bind(L: ctypes.CDLL) -> None:
         "qlinear_f8_packed_bytes": [i64, i64, i64, psz],
         "qlinear_f8_pack": [i64, i64, i64, vp, vp, vp],
         "qlinear_f8_unpack": [i64, i64, i64, vp, vp, vp],
-        "qlinear_f8_default_schedule": [i64, i64, i64, i64, ci, ci, ctypes.POINTER(_Q.Schedule)],
-        "qlinear_f8_workspace_bytes": [i64, i64, i64, i64, ci, psz],
+        "qlinear_f8_default_schedule": [i64, i64, i64, i64, ci, ci, ci, ctypes.POINTER(_Q.Schedule)],
+        "qlinear_f8_workspace_bytes": [i64, i64, i64, i64, ci, ci, psz],
         "qlinear_f8_forward": [vp, vp, i64, vp, i64, i64, i64, vp, vp, vp, vp, ci, vp, sz, vp],
         "qlinear_f8_backward_workspace_bytes": [i64, i64, i64, i64, ci, psz],
         "qlinear_f8_backward": [vp, i64, vp, i64, i64, i64, vp, vp, vp, vp, sz, vp],
@@ -193,16 +193,18 @@ def unpack_f8(pw: BlockWeight):
     return codes, pw.s.clone()
 
 
-def f8_default_schedule(M: int, N: int, K: int, E: int | None = None, backward: bool = False):
+def f8_default_schedule(M: int, N: int, K: int, E: int | None = None, backward: bool = False,
+                        out_dtype: torch.dtype = torch.bfloat16):
     """The Schedule (tile, splits) that a product of M rows, or its backward pass, takes; E: over that many experts."""
+    _need(out_dtype in _DTYPES, "out_dtype must be bfloat16 or float32")
     s = _Q.Schedule()
     _Q._check(_Q.lib().qlinear_f8_default_schedule(M, 1 if E is None else E, N, K, int(E is not None), int(backward),
-                                                   ctypes.byref(s)), "qlinear_f8_default_schedule")
+                                                   _DTYPES[out_dtype], ctypes.byref(s)), "qlinear_f8_default_schedule")
     return s
 
 
-def f8_workspace_bytes(M: int, N: int, K: int, E: int | None = None) -> int:
-    return _sizes("qlinear_f8_workspace_bytes", M, 1 if E is None else E, N, K, int(E is not None))
+def f8_workspace_bytes(M: int, N: int, K: int, E: int | None = None, out_dtype: torch.dtype = torch.bfloat16) -> int:
+    return _sizes("qlinear_f8_workspace_bytes", M, 1 if E is None else E, N, K, int(E is not None), _DTYPES[out_dtype])
 
 
 def f8_backward_workspace_bytes(M: int, N: int, K: int, E: int | None = None) -> int:
@@ -228,7 +230,7 @@ def _forward(codes, scales, pw, counts, bias, out_dtype, out, workspace):
     lead, M, codes, scales = _rows(codes, scales, pw.K, pw.device)
     bias = _bias(bias, pw.E * pw.N, pw)
     out = _out(out, (*lead, pw.N), out_dtype, pw.device)
-    need = f8_workspace_bytes(M, pw.N, pw.K, E)
+    need = f8_workspace_bytes(M, pw.N, pw.K, E, out_dtype)
     ws = _space(workspace, need, pw.device)
     _call("qlinear_f8_forward", pw.device, codes.data_ptr(), scales.data_ptr(), M, _p(counts), pw.E, pw.N, pw.K,
           pw.w.data_ptr(), pw.s.data_ptr(), _p(bias), out.data_ptr(), _DTYPES[out_dtype], _p(ws), need)

@@ -557,12 +557,15 @@ ql_status qlinear_f8_unpack(int64_t E, int64_t N, int64_t K, const void *packed,
  * 16-byte aligned.  Neither dy nor the codes are rounded.  Its workspace holds partial sums of split channels,
  * and a copy of dy where N is not a multiple of eight.
  *
- * qlinear_f8_default_schedule: tile (rows x outputs of a workgroup) and splits of the summed dimension:
- *   forward   0: 16 x 16, 1: 16 x 32, 2: 128 x 256, 3: 128 x 128, 4: 64 x 128, 5: 64 x 64, 6: 32 x 64
+ * qlinear_f8_default_schedule: tile (rows x outputs of a workgroup) and splits of the summed dimension (out_dtype is
+ * the forward product's, bf16 for the backward one):
+ *   forward   0: 16 x 16, 1: 16 x 32, 2: 128 x 256, 3: 64 x 256, 4: 64 x 128, 5: 64 x 64, 6: 32 x 128, 7: 32 x 64
  *   backward  0: 256, 1: 128, 2: 64, 3: 16 rows, all x 256
  */
-ql_status qlinear_f8_default_schedule(int64_t M, int64_t E, int64_t N, int64_t K, int grouped, int backward, ql_schedule *out);
-ql_status qlinear_f8_workspace_bytes(int64_t M, int64_t E, int64_t N, int64_t K, int grouped, size_t *bytes);
+ql_status qlinear_f8_default_schedule(int64_t M, int64_t E, int64_t N, int64_t K, int grouped, int backward,
+                                      ql_dtype out_dtype, ql_schedule *out);
+ql_status qlinear_f8_workspace_bytes(int64_t M, int64_t E, int64_t N, int64_t K, int grouped, ql_dtype out_dtype,
+                                     size_t *bytes);
 ql_status qlinear_f8_forward(const void *codes, const float *scales, int64_t M, const int32_t *tokens_per_expert, int64_t E,
                              int64_t N, int64_t K, const void *packed, const float *w_scales, const void *bias, void *out,
                              ql_dtype out_dtype, void *workspace, size_t workspace_bytes, void *stream);

@@ -220,14 +220,18 @@ def test_linear_exact(M, N, K):
     assert torch.equal(Q.linear_f8(x, xs, Q.pack_f8(w, ws), out_dtype=F32).to(D), ref)
 
 
-SCHEDULED = [(5, 300, 1184), (5, 9000, 288), (40, 3000, 416), (100, 2000, 672), (200, 4100, 544), (333, 5001, 544),
-             (1000, 5001, 288), (500, 4096, 288), (2048, 4096, 416), (600, 700, 4128), (70, 400, 8224), (4500, 2080, 160)]
+SCHEDULED = [(5, 300, 1184), (5, 9000, 288), (2048, 4096, 416), (2048, 4096, 1184), (1000, 4096, 1184), (333, 5001, 544),
+             (100, 5000, 4128), (200, 4100, 544), (40, 3000, 416), (35, 8297, 9408), (33, 4281, 9440), (1119, 66, 8160),
+             (33, 2301, 10304), (612, 67, 7424), (663, 68, 7776), (17, 73, 6592), (23, 112, 12320), (18, 69, 7520), (36, 4638, 28448),
+             (4500, 2080, 160)]
 
 
-def test_every_schedule_is_among_these():
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_every_schedule_is_among_these(dtype):
+    """All tiles, and all but the few-row kernels and the largest tiles also in splits."""
     Q = _Q()
-    seen = {(s.tile, s.splits > 1) for s in (Q.f8_default_schedule(*c) for c in SCHEDULED)}
-    assert {t for t, _ in seen} == set(range(7)), seen
+    seen = {(s.tile, s.splits > 1) for s in (Q.f8_default_schedule(*c, out_dtype=dtype) for c in SCHEDULED)}
+    assert seen == {(t, False) for t in range(8)} | {(t, True) for t in range(3, 8)}, sorted(seen)
 
 
 @pytest.mark.parametrize("M,N,K", SCHEDULED)

@@ -30,7 +30,10 @@ def test_packed_bytes(L):
 
 
 def test_workspaces(L):
-    for f in (L.qlinear_f8_workspace_bytes, L.qlinear_f8_backward_workspace_bytes):
+    def forward(dtype):
+        return lambda *a: L.qlinear_f8_workspace_bytes(*a[:-1], dtype, a[-1])
+    assert L.qlinear_f8_workspace_bytes(5, 1, 64, 64, 0, 2, ctypes.byref(ctypes.c_size_t())) == ARG
+    for f in (forward(BF16), forward(F32), L.qlinear_f8_backward_workspace_bytes):
         assert _bytes(f, 0, 1, 64, 64, 0) == (OK, 0)
         for bad in ((-1, 1, 64, 64, 0), (5, 1, 64, 100, 0), (5, 2, 64, 64, 0), (1 << 31, 1, 64, 64, 0), (5, 0, 64, 64, 1)):
             assert _bytes(f, *bad)[0] == SHAPE, bad
@@ -50,15 +53,15 @@ def test_workspaces(L):
 
 
 def test_default_schedule(L):
-    out = ctypes.create_string_buffer(8)
-    f = L.qlinear_f8_default_schedule
+    def f(M, E, N, K, grouped, backward, s, dtype=BF16):
+        return L.qlinear_f8_default_schedule(M, E, N, K, grouped, backward, dtype, s)
     import bit_weight_only_offline_amd as Q
     s = Q.Schedule()
     assert f(4, 1, 64, 64, 0, 0, ctypes.byref(s)) == OK and s.tile in (0, 1) and s.splits == 1
     assert f(0, 1, 64, 64, 0, 0, ctypes.byref(s)) == SHAPE
     assert f(4, 1, 64, 64, 0, 2, ctypes.byref(s)) == ARG and f(4, 1, 64, 64, 0, 0, None) == ARG
     assert f(4, 8, 64, 64, 0, 0, ctypes.byref(s)) == SHAPE and f(4, 8, 64, 64, 1, 1, ctypes.byref(s)) == OK
-    del out
+    assert f(4, 1, 64, 64, 0, 0, ctypes.byref(s), F32) == OK and f(4, 1, 64, 64, 0, 0, ctypes.byref(s), 2) == ARG
 
 
 def test_forward_refusals(L):
