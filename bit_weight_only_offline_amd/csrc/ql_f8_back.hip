@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_
                     if (q + P < 2 * MT) read_x(at, q + P);
                     else read_x(after, q + P - 2 * MT);
                     // the next step's operands, and behind a block's last products its sums in units of the next scale
-                    if (MT >= 4 ? i >= MT - 4 : true)
+                    if (MT >= 4 ? i >= MT - 4 : i == 0)
 #pragma unroll
                         for (int p = MT >= 4 ? i - (MT - 4) : 0; p < (MT >= 4 ? i - (MT - 4) + 1 : 4); ++p) decode(codes, p, s, op[1 - h]);
                     if (e == 1 && h == 1 && i > 0)
@@ -297,9 +297,19 @@ constexpr BackCfg CFGS[] = {
     {2, 4, 8},      // 256 x 256
     {2, 4, 4},      // 128 x 256
     {1, 4, 4},      // 64 x 256
+    {1, 4, 2},      // 32 x 256
     {1, 4, 1},      // 16 x 256
 };
-constexpr int NUM_CFGS = 4;
+constexpr int NUM_CFGS = 5, UNSPLIT = 1;    // 128 rows are never best in splits
+// Microseconds that a compute unit takes for a block of 128 channels, and for a tile besides (start, first loads, stores),
+// and what a round of 256 workgroups after the first takes of either, less where several share a unit.  Fitted to 60
+// sizes, 1 to 4096 x 4096 x 14336, 14336 x 4096, 4096 x 4096, 5000 x 4128, 2048 x 2048 and 1024 x 8192, every tile in
+// one to twelve splits; the choice was within 7% of the fastest at each.
+struct BackRate { float block, tile, tile_more, block_more; };
+constexpr BackRate RATES[NUM_CFGS] = {
+    {3.02f, 9.3f, 0.18f, 1.15f}, {1.91f, 6.0f, 0.22f, 1.07f}, {1.14f, 5.8f, 0.08f, 0.64f}, {0.97f, 3.6f, 0.24f, 0.53f}, {0.63f, 3.7f, 0.27f, 0.63f},
+};
+constexpr float JOIN_US = 4.6f, JOIN_BYTES_PER_US = 5.0e6f;
 
 template <int I, bool SPLIT>
 hipError_t launch_of(const F8BackArgs &a, hipStream_t st) {
@@ -317,8 +327,8 @@ hipError_t launch_of(const F8BackArgs &a, hipStream_t st) {
 
 template <int I>
 hipError_t launch(const F8BackArgs &a, hipStream_t st) {
-    if (a.ks == 1) return launch_of<I, false>(a, st);
-    const hipError_t e = launch_of<I, true>(a, st);
+    if (I == UNSPLIT || a.ks == 1) return launch_of<I, false>(a, st);
+    const hipError_t e = launch_of<I, I != UNSPLIT>(a, st);
     if (e != hipSuccess) return e;
     const int64_t n = int64_t(a.r.rows) * a.K;
     hipLaunchKernelGGL(f8_back_join_kernel, elementwise_grid(n / 4), dim3(256), 0, st, a.part, a.dx, n, a.ks);
@@ -327,33 +337,40 @@ hipError_t launch(const F8BackArgs &a, hipStream_t st) {
 
 }  // namespace
 
-// The tallest tiles that still give every compute unit one; fewer than that, and the channels are split.
+// The tile and the split of the channels whose time is least by the measured rates.  A grouped product's row
+// blocks are taken to be half a block an expert more than its rows fill; it is not split.
 F8BackPlan make_f8_back_plan(const F8Layout &L, int64_t M, bool grouped) {
     F8BackPlan p;
     p.ldy = ceil_div(L.N, 8) * 8;
-    p.bps = int(L.nblocks);
-    auto blocks = [&](int c, int64_t &mt, int64_t &nb) {
-        const BackCfg &t = CFGS[c];
-        mt = most_row_blocks(M, L.E, grouped, 16 * t.MT * t.WM);
-        nb = ceil_div(L.K, 64 * t.WN);
+    const int64_t used = grouped ? std::min(L.E, M) : 1;
+    auto columns = [&](const BackCfg &t) { return ceil_div(L.K, 64 * t.WN); };
+    auto threads = [&](const BackCfg &t) {
+        return ceil_div(most_row_blocks(M, L.E, grouped, 16 * t.MT * t.WM) * columns(t), 8) * 8 * 64 * t.WM * t.WN;
     };
-    const int64_t each = ceil_div(M, grouped ? std::min(L.E, M) : 1);
-    int64_t mt, nb;
-    p.cfg = NUM_CFGS - 1;
+    float best = 0.0f;
     for (int c = 0; c < NUM_CFGS; ++c) {
-        blocks(c, mt, nb);
-        if (each > 16 && mt * nb >= 256) { p.cfg = c; break; }
+        const BackCfg &t = CFGS[c];
+        const BackRate &rate = RATES[c];
+        if (c > 0 && threads(t) > LAUNCH_THREADS_MAX) continue;             // where the tallest do not fit, none does
+        const int64_t block = 16 * t.MT * t.WM, mt = grouped ? std::max(used, ceil_div(2 * M + used * block, 2 * block)) : ceil_div(M, block);
+        for (int ks : {1, 2, 3, 4, 6, 8, 12}) {
+            const int64_t bps = ceil_div(L.nblocks, ks);
+            if (ks > 1 && (grouped || c == UNSPLIT || bps < 2 || ceil_div(L.nblocks, bps) < ks)) break;
+            const float more = float(ceil_div(mt * columns(t) * ks, 256) - 1);
+            float us = (1.0f + more * rate.block_more) * float(bps) * rate.block + (1.0f + more * rate.tile_more) * rate.tile;
+            if (ks > 1) us += JOIN_US + float(ks) * float(M) * float(L.K) * 8.0f / JOIN_BYTES_PER_US;
+            if (best == 0.0f || us < best) {
+                best = us;
+                p.cfg = c;
+                p.ks = ks;
+                p.bps = int(bps);
+            }
+        }
     }
-    if (each > 16 && p.cfg == NUM_CFGS - 1) p.cfg = 2;
-    blocks(p.cfg, mt, nb);
-    if (!grouped && mt * nb < 256) {
-        const int64_t want = std::min<int64_t>(8, ceil_div(256, mt * nb));
-        p.bps = int(ceil_div(L.nblocks, std::min<int64_t>(want, ceil_div(L.nblocks, 4))));
-        p.ks = int(ceil_div(L.nblocks, p.bps));
-    }
-    p.mtiles = mt;
-    p.nblocks = nb;
-    p.threads = ceil_div(mt * nb, 8) * 8 * 64 * CFGS[p.cfg].WM * CFGS[p.cfg].WN;
+    const BackCfg &t = CFGS[p.cfg];
+    p.mtiles = most_row_blocks(M, L.E, grouped, 16 * t.MT * t.WM);
+    p.nblocks = columns(t);
+    p.threads = threads(t);
     p.operand_bytes = L.N % 8 != 0 ? round256(size_t(M) * size_t(p.ldy) * 2) : 0;
     p.ws_bytes = p.operand_bytes + (p.ks > 1 ? round256(size_t(p.ks) * size_t(M) * size_t(L.K) * 4) : 0);
     return p;
@@ -386,7 +403,8 @@ hipError_t launch_f8_backward(const F8Layout &L, const F8BackPlan &p, const F8Ba
         case 0: return launch<0>(a, st);
         case 1: return launch<1>(a, st);
         case 2: return launch<2>(a, st);
-        default: return launch<3>(a, st);
+        case 3: return launch<3>(a, st);
+        default: return launch<4>(a, st);
     }
 }
 

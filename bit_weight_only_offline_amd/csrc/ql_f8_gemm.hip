@@ -88,9 +88,10 @@ __device__ inline void emit(const F8Args &a, int expert, int m, int n, const f32
 // ---- few rows: the weight streams through registers ----------------------------------
 // One workgroup owns NT column tiles over the whole input dimension.  Its WK wavefronts take the
 // blocks in turn (block i goes to wavefront i mod WK), so together they read one contiguous run per
-// tile; U blocks are in flight while the U before them are multiplied.  The wavefronts' sums meet
-// in LDS and are added in a fixed order.
-template <int NT, int WK, int U>
+// tile; the next block is in flight while one is multiplied (two to four were slower: their registers leave room for
+// fewer wavefronts; 32 rows of 8 experts of 28672 x 4096: 149 us, 6.3 TB/s, 177 with two).  The wavefronts' sums
+// meet in LDS and are added in a fixed order.
+template <int NT, int WK>
 __global__ void __launch_bounds__(64 * WK) f8_rows_kernel(F8Args a) {
     extern __shared__ __attribute__((aligned(16))) f32x4 red[];      // [WK][NT][64]
     const int tid = threadIdx.x, lane = tid & 63;
@@ -120,39 +121,33 @@ __global__ void __launch_bounds__(64 * WK) f8_rows_kernel(F8Args a) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    struct Batch {
-        Operand w[U][NT], x[U];
-        uint32_t xs[U], ws[U];
+    struct Block {
+        Operand w[NT], x;
+        uint32_t xs, ws;
     };
-    auto load = [&](int it, Batch &b) {
+    auto load = [&](int it, Block &b) {
+        const int kb = it * WK + wv;
+        const uint32_t past = kb < a.kblocks ? 0u : OUT_OF_RANGE;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int kb = (it * U + u) * WK + wv;
-            const uint32_t past = kb < a.kblocks ? 0u : OUT_OF_RANGE;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                b.w[u][j].lo = ld128(wr, (w_off[j] + uint32_t(kb) * F8_TILE_BYTES) | past);
-                b.w[u][j].hi = ld128(wr, (w_off[j] + uint32_t(kb) * F8_TILE_BYTES + 1024u) | past);
-            }
-            // the next row's codes behind the last input might be NaN: they are not read
-            const int k = kb * F8_BLOCK + 16 * g;
-            b.x[u].lo = ld128(xr, k < a.K ? x_off + uint32_t(kb) * F8_BLOCK : OUT_OF_RANGE);
-            b.x[u].hi = ld128(xr, k + 64 < a.K ? x_off + uint32_t(kb) * F8_BLOCK + 64u : OUT_OF_RANGE);
-            b.xs[u] = ld32(sr, (s_off + uint32_t(kb) * 4u) | past);
-            b.ws[u] = ld32(vr, uint32_t(kb) * 4u | past);
+        for (int j = 0; j < NT; ++j) {
+            b.w[j].lo = ld128(wr, (w_off[j] + uint32_t(kb) * F8_TILE_BYTES) | past);
+            b.w[j].hi = ld128(wr, (w_off[j] + uint32_t(kb) * F8_TILE_BYTES + 1024u) | past);
         }
+        // the next row's codes behind the last input might be NaN: they are not read
+        const int k = kb * F8_BLOCK + 16 * g;
+        b.x.lo = ld128(xr, k < a.K ? x_off + uint32_t(kb) * F8_BLOCK : OUT_OF_RANGE);
+        b.x.hi = ld128(xr, k + 64 < a.K ? x_off + uint32_t(kb) * F8_BLOCK + 64u : OUT_OF_RANGE);
+        b.xs = ld32(sr, (s_off + uint32_t(kb) * 4u) | past);
+        b.ws = ld32(vr, uint32_t(kb) * 4u | past);
     };
-    auto multiply = [&](const Batch &b) {
+    auto multiply = [&](const Block &b) {
+        const float f = __uint_as_float(b.xs) * __uint_as_float(b.ws);
+        const Wide x = widen(b.x);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const float f = __uint_as_float(b.xs[u]) * __uint_as_float(b.ws[u]);
-            const Wide x = widen(b.x[u]);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) join(acc[j], block_product(widen(b.w[u][j]), x), f);
-        }
+        for (int j = 0; j < NT; ++j) join(acc[j], block_product(widen(b.w[j]), x), f);
     };
-    const int its = (a.kblocks + WK * U - 1) / (WK * U);
-    Batch b0, b1;
+    const int its = (a.kblocks + WK - 1) / WK;
+    Block b0, b1;
     load(0, b0);
     for (int it = 0; it < its; it += 2) {
         if (it + 1 < its) load(it + 1, b1);
@@ -537,7 +532,6 @@ constexpr F8Cfg CFGS[] = {
 #endif
 };
 constexpr int NUM_CFGS = 8, FIRST_TILE = 2;
-constexpr int ROWS_U = 2;
 // Microseconds that a compute unit takes for one block of a workgroup's tile, and for the tile besides (start, first
 // loads, stores); and what a round of 256 workgroups after the first takes of either, less where several share a unit,
 // more where the operands of more workgroups pass through the caches.  For results in bf16 and, through the bf16 cores,
@@ -556,7 +550,7 @@ template <int I>
 hipError_t launch_rows(const F8Args &a, hipStream_t st) {
     constexpr F8Cfg t = CFGS[I];
     constexpr size_t lds = size_t(t.WK) * t.NT * 1024;
-    hipLaunchKernelGGL((f8_rows_kernel<t.NT, t.WK, ROWS_U>), dim3(unsigned(a.nblocks), unsigned(a.mtiles)), dim3(64 * t.WK), lds, st, a);
+    hipLaunchKernelGGL((f8_rows_kernel<t.NT, t.WK>), dim3(unsigned(a.nblocks), unsigned(a.mtiles)), dim3(64 * t.WK), lds, st, a);
     return hipGetLastError();
 }
 
@@ -588,7 +582,9 @@ hipError_t launch_tiles(const F8Args &a, hipStream_t st) {
 
 }  // namespace
 
-// Up to 16 rows, an expert's on average, stream the weight through registers.  More take the schedule and the split of
+// Up to 16 rows, an expert's on average, stream the weight through registers, a workgroup one column tile as long as
+// that gives a compute unit at most one (4096 x 14336, one row: 11.4 us against 12.7 with two; 8192 x 8192, eight rows:
+// 13.4 against 12.9; 8 experts of 28672 x 4096, 32 rows: 156 against 149).  More take the schedule and the split of
 // the input dimension whose time is least by the measured rates.  A grouped product's row blocks are taken to
 // be half a block an expert more than its rows fill; it is not split.
 F8Plan make_f8_plan(const F8Layout &L, int64_t M, bool grouped, bool f32) {
@@ -603,7 +599,7 @@ F8Plan make_f8_plan(const F8Layout &L, int64_t M, bool grouped, bool f32) {
     };
     const bool rows_fit = most_row_blocks(M, L.E, grouped, 16) <= 65535;    // the grid dimension that holds them
     if (M <= 16 * used && rows_fit) {
-        p.cfg = L.ntiles <= 512 ? 0 : 1;
+        p.cfg = L.ntiles * used <= 256 ? 0 : 1;
     } else {
         float best = 0.0f;
         for (int c = M <= 64 * used && rows_fit ? 1 : FIRST_TILE; c < NUM_CFGS; ++c) {

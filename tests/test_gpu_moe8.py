@@ -364,14 +364,15 @@ def test_linear_backward(M, N, K):
     assert abs(float((got.to(D) * dx).sum()) - slope) <= float((tol * dx.abs()).sum())
 
 
-BACK_SCHEDULED = [(5, 300, 288), (20, 1000, 544), (100, 500, 4128), (1000, 300, 4160), (3000, 260, 4160), (2100, 133, 14336),
-                  (300, 2048, 1056), (9000, 40, 2080)]
+BACK_SCHEDULED = [(5, 300, 288), (1000, 300, 4160), (3000, 260, 4160), (240, 236, 24608), (1691, 1179, 8512), (6876, 4991, 544),
+                  (402, 5013, 3456), (387, 2658, 960), (17, 4746, 192), (9000, 40, 2080)]
 
 
 def test_every_backward_schedule_is_among_these():
+    """All tiles, and all but the one of 128 rows also in splits."""
     Q = _Q()
-    seen = {Q.f8_default_schedule(*c, backward=True).tile for c in BACK_SCHEDULED}
-    assert seen == set(range(4)), seen
+    seen = {(s.tile, s.splits > 1) for s in (Q.f8_default_schedule(*c, backward=True) for c in BACK_SCHEDULED)}
+    assert seen == {(t, False) for t in range(5)} | {(t, True) for t in (0, 2, 3, 4)}, sorted(seen)
 
 
 @pytest.mark.parametrize("M,N,K", BACK_SCHEDULED)
