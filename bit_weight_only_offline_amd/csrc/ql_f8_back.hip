@@ -295,21 +295,20 @@ __global__ void __launch_bounds__(256) f8_back_copy_kernel(const uint16_t *dy, u
 struct BackCfg { int WM, WN, MT; };
 constexpr BackCfg CFGS[] = {
     {2, 4, 8},      // 256 x 256
-    {2, 4, 4},      // 128 x 256
     {1, 4, 4},      // 64 x 256
     {1, 4, 2},      // 32 x 256
     {1, 4, 1},      // 16 x 256
 };
-constexpr int NUM_CFGS = 5, UNSPLIT = 1;    // 128 rows are never best in splits
+constexpr int NUM_CFGS = 4;
 // Microseconds that a compute unit takes for a block of 128 channels, and for a tile besides (start, first loads, stores),
-// and what a round of 256 workgroups after the first takes of either, less where several share a unit.  Fitted to 60
-// sizes, 1 to 4096 x 4096 x 14336, 14336 x 4096, 4096 x 4096, 5000 x 4128, 2048 x 2048 and 1024 x 8192, every tile in
-// one to twelve splits; the choice was within 7% of the fastest at each.
+// and what a round of 256 workgroups after the first takes of either, less where several share a unit.  Fitted to 84
+// sizes, 1 to 8192 x 4096 x 14336, 14336 x 4096, 4096 x 4096, 5000 x 4128, 2048 x 2048 and 1024 x 8192, every tile in
+// one to twelve splits; the choice was within 8% of the fastest at each.  Tiles of 128 rows were the fastest at none.
 struct BackRate { float block, tile, tile_more, block_more; };
 constexpr BackRate RATES[NUM_CFGS] = {
-    {3.02f, 9.3f, 0.18f, 1.15f}, {1.91f, 6.0f, 0.22f, 1.07f}, {1.14f, 5.8f, 0.08f, 0.64f}, {0.97f, 3.6f, 0.24f, 0.53f}, {0.63f, 3.7f, 0.27f, 0.63f},
+    {3.19f, 8.0f, 1.07f, 0.85f}, {1.19f, 5.2f, 0.05f, 0.74f}, {0.91f, 4.9f, 0.01f, 0.67f}, {0.69f, 4.4f, 0.19f, 0.4f},
 };
-constexpr float JOIN_US = 4.6f, JOIN_BYTES_PER_US = 5.0e6f;
+constexpr float JOIN_US = 4.1f, JOIN_BYTES_PER_US = 4.8e6f;
 
 template <int I, bool SPLIT>
 hipError_t launch_of(const F8BackArgs &a, hipStream_t st) {
@@ -327,8 +326,8 @@ hipError_t launch_of(const F8BackArgs &a, hipStream_t st) {
 
 template <int I>
 hipError_t launch(const F8BackArgs &a, hipStream_t st) {
-    if (I == UNSPLIT || a.ks == 1) return launch_of<I, false>(a, st);
-    const hipError_t e = launch_of<I, I != UNSPLIT>(a, st);
+    if (a.ks == 1) return launch_of<I, false>(a, st);
+    const hipError_t e = launch_of<I, true>(a, st);
     if (e != hipSuccess) return e;
     const int64_t n = int64_t(a.r.rows) * a.K;
     hipLaunchKernelGGL(f8_back_join_kernel, elementwise_grid(n / 4), dim3(256), 0, st, a.part, a.dx, n, a.ks);
@@ -355,7 +354,7 @@ F8BackPlan make_f8_back_plan(const F8Layout &L, int64_t M, bool grouped) {
         const int64_t block = 16 * t.MT * t.WM, mt = grouped ? std::max(used, ceil_div(2 * M + used * block, 2 * block)) : ceil_div(M, block);
         for (int ks : {1, 2, 3, 4, 6, 8, 12}) {
             const int64_t bps = ceil_div(L.nblocks, ks);
-            if (ks > 1 && (grouped || c == UNSPLIT || bps < 2 || ceil_div(L.nblocks, bps) < ks)) break;
+            if (ks > 1 && (grouped || bps < 2 || ceil_div(L.nblocks, bps) < ks)) break;
             const float more = float(ceil_div(mt * columns(t) * ks, 256) - 1);
             float us = (1.0f + more * rate.block_more) * float(bps) * rate.block + (1.0f + more * rate.tile_more) * rate.tile;
             if (ks > 1) us += JOIN_US + float(ks) * float(M) * float(L.K) * 8.0f / JOIN_BYTES_PER_US;
@@ -403,8 +402,7 @@ hipError_t launch_f8_backward(const F8Layout &L, const F8BackPlan &p, const F8Ba
         case 0: return launch<0>(a, st);
         case 1: return launch<1>(a, st);
         case 2: return launch<2>(a, st);
-        case 3: return launch<3>(a, st);
-        default: return launch<4>(a, st);
+        default: return launch<3>(a, st);
     }
 }
 

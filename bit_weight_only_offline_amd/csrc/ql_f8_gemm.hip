@@ -306,14 +306,13 @@ __global__ void __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_
         make_uniform_rsrc(a.ws + (int64_t(rb.expert) * a.nbs + nb0) * a.kblocks, uint32_t(nb_here) * uint32_t(a.kblocks) * 4u);
 
     const int k_first = kb0 + wk * BS;                     // first block of the wavefront's first stage
-    uint32_t x_off[XL], w_off[NT];
-    int x_left[XL];                                        // inputs from the piece to the row's end
-#pragma unroll
-    for (int q = 0; q < XL; ++q) {
-        const int row = (wn + WN * q) * 8 + (lane >> 3), piece = (lane & 7) ^ ((row >> 1) & 7);
-        x_off[q] = row < rb.count ? uint32_t(row) * uint32_t(a.K) + uint32_t(k_first) * F8_BLOCK + 16u * uint32_t(piece) : OUT_OF_RANGE;
-        x_left[q] = a.K - k_first * F8_BLOCK - 16 * piece;
-    }
+    // A wavefront's first rows of a block; the others lie a fixed distance on, those past the last past the range.
+    static_assert(WN % 2 == 0, "a wavefront's rows have one swizzle");
+    const int x_row = wn * 8 + (lane >> 3), x_piece = (lane & 7) ^ ((x_row >> 1) & 7);
+    const uint32_t x_off = uint32_t(x_row) * uint32_t(a.K) + uint32_t(k_first) * F8_BLOCK + 16u * uint32_t(x_piece);
+    const uint32_t x_far = uint32_t(WN * 8) * uint32_t(a.K);
+    const int x_left = a.K - k_first * F8_BLOCK - 16 * x_piece;   // inputs from the piece to the row's end
+    uint32_t w_off[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
         const int tile = wn * NT + j;
@@ -329,7 +328,7 @@ __global__ void __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_
             uint8_t *const to = ring + u * STAGE + b * BLOCK;
 #pragma unroll
             for (int q = 0; q < XL; ++q)
-                ld128_lds(xr, on * F8_BLOCK < x_left[q] ? (x_off[q] + uint32_t(on) * F8_BLOCK) | past(st, b) : OUT_OF_RANGE,
+                ld128_lds(xr, on * F8_BLOCK < x_left ? (x_off + uint32_t(q) * x_far + uint32_t(on) * F8_BLOCK) | past(st, b) : OUT_OF_RANGE,
                           to + (wn + WN * q) * 1024);
         }
     };
@@ -364,22 +363,20 @@ __global__ void __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_
         }
     };
     const uint8_t *const x_at[2] = {ring + c * 128 + ((g ^ (c >> 1)) * 16), ring + c * 128 + (((4 + g) ^ (c >> 1)) * 16)};
-    // token tile q of the stage in place u, those past its last from the next place
-    auto read_x = [&](Operand &o, int u, int q) {
-        const int at = (q < Q ? u : (u + 1) % S) * STAGE + q % Q / MT * BLOCK + q % MT * 2048;
-        o.lo = *reinterpret_cast<const u32x4 *>(x_at[0] + at);
-        o.hi = *reinterpret_cast<const u32x4 *>(x_at[1] + at);
-    };
-    float f[MT], v;                                        // the tokens' scales of a block, the weight's
+    // token tile q of the stage st in place u, those past its last from the next stage, with their scales
+    float f[XB], v;                                        // the tokens' scales, the weight's of a block
     const int v_row = (nt0 + wn * NT) * TILE_N / F8_BLOCK - nb0;
-    auto read_scales = [&](int st, int b) {
+    auto scale_at = [&](int st, int b, int row) {          // of rows with the same low bits as `row`
         const int block = (st * WK + wk) * BS + b, word = block & (PANEL_BLOCKS - 1);
-        const uint8_t *const panel = panels + (block / PANEL_BLOCKS & 1) * PANEL + (word & 3) * 4;
-        const uint8_t *const at = panel + c * 128 + (((word >> 2) ^ (c & 7)) * 16);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) f[i] = *reinterpret_cast<const float *>(at + i * 2048);
-        v = *reinterpret_cast<const float *>(panel + (MP + v_row) * 128 + (((word >> 2) ^ v_row) * 16));
+        return panels + (block / PANEL_BLOCKS & 1) * PANEL + (((word >> 2) ^ (row & 7)) * 16) + (word & 3) * 4;
     };
+    auto read_x = [&](int st, int u, int q) {
+        const int at = (q < Q ? u : (u + 1) % S) * STAGE + q % Q / MT * BLOCK + q % MT * 2048, to = (u * Q + q) % XB;
+        x[to].lo = *reinterpret_cast<const u32x4 *>(x_at[0] + at);
+        x[to].hi = *reinterpret_cast<const u32x4 *>(x_at[1] + at);
+        f[to] = *reinterpret_cast<const float *>(scale_at(q < Q ? st : st + 1, q % Q / MT, c) + c * 128 + q % MT * 2048);
+    };
+    auto read_v = [&](int st, int b) { v = *reinterpret_cast<const float *>(scale_at(st, b, v_row) + (MP + v_row) * 128); };
 
     f32x4 acc[NT][MT];
 #pragma unroll
@@ -400,21 +397,16 @@ __global__ void __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_
     wait_vmcnt<(S - 1) * PER_STAGE>();
     ring_barrier();
 #pragma unroll
-    for (int i = 0; i < P; ++i) read_x(x[i], 0, i);
-    read_scales(0, 0);
+    for (int i = 0; i < P; ++i) read_x(0, 0, i);
+    read_v(0, 0);
 
     // Stage st in place u.  A tile's sums are joined while the next tile's instructions run.
     auto stage = [&](int st, int u, bool more) {
         f32x4 sum[2][NT];
 #pragma unroll
         for (int b = 0; b < BS; ++b) {
-            float s[MT];
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                s[i] = f[i] * v;
-                // past the last block: weights that read as zero, but whatever scales lie there
-                if (BS * WK > 1 && past(st, b)) s[i] = 0.0f;
-            }
+            const float w_scale = v;
+            float s[2];
             Wide wide[EXACT ? NT : 1];
             if constexpr (EXACT)
 #pragma unroll
@@ -429,7 +421,10 @@ __global__ void __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_
                     if (more) load_x(st + S, u);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                if (i == MT - P) read_scales(b + 1 < BS ? st : st + 1, (b + 1) % BS);
+                if (i == MT - P) read_v(b + 1 < BS ? st : st + 1, (b + 1) % BS);
+                s[i & 1] = f[(u * Q + q) % XB] * w_scale;
+                // past the last block: weights that read as zero, but whatever scales lie there
+                if (BS * WK > 1 && past(st, b)) s[i & 1] = 0.0f;
                 if constexpr (EXACT) {
                     const Wide xw = widen(x[(u * Q + q) % XB]);
 #pragma unroll
@@ -438,17 +433,17 @@ __global__ void __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_
 #pragma unroll
                     for (int j = 0; j < NT; ++j) sum[i & 1][j] = block_product(w[u][b][j], x[(u * Q + q) % XB]);
                 }
-                read_x(x[(u * Q + q + P) % XB], u, q + P);
+                read_x(st, u, q + P);
                 __builtin_amdgcn_sched_barrier(0);         // joined first, the last sums would be waited for
                 if (i > 0)
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) join(acc[j][i - 1], sum[(i - 1) & 1][j], s[i - 1]);
+                    for (int j = 0; j < NT; ++j) join(acc[j][i - 1], sum[(i - 1) & 1][j], s[(i - 1) & 1]);
                 __builtin_amdgcn_sched_barrier(0);
             }
             if (more) load_w(st + S, u, b);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) join(acc[j][MT - 1], sum[(MT - 1) & 1][j], s[MT - 1]);
+            for (int j = 0; j < NT; ++j) join(acc[j][MT - 1], sum[(MT - 1) & 1][j], s[(MT - 1) & 1]);
         }
     };
     int st = 0, panel = 2;
