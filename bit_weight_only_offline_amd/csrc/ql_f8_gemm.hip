@@ -259,7 +259,7 @@ __device__ inline void store_tiles(const F8Args &a, const RowBlock &rb, int ct0,
 
 // EXACT: through the bf16 matrix cores.
 template <int WN, int WK, int MT, int NT, int BS, int S, bool SPLIT, bool EXACT>
-__global__ void __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_eu(2))) f8_tile_kernel(F8Args a) {
+__device__ inline void tile_product(const F8Args &a, const RowBlock &rb, const int nt0, uint8_t *const lds) {
     constexpr int MP = 16 * MT, NTT = NT * WN;
     constexpr int XL = MP / 8 / WN;                        // 1 KiB loads of a block's rows a wavefront
     constexpr int PER_STAGE = BS * (XL + 2 * NT);
@@ -269,28 +269,12 @@ __global__ void __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_
     static_assert((S * Q) % XB == 0 && P < XB && P < MT, "buffers come round");
     static_assert(F8_BLOCK % (16 * NT) == 0 && NTT * TILE_N <= 8 * F8_BLOCK, "one weight scale a wavefront and block, eight rows of them");
     static_assert(PANEL_BLOCKS % (BS * WK) == 0 && PANEL_BLOCKS / (BS * WK) > 2 * S, "a panel lasts longer than a load takes");
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wk = wv / WN, wn = wv % WN;
     const int g = lane >> 4, c = lane & 15;
-
-    // Block b runs on XCD b mod 8: give each XCD one contiguous run of the tile order, and order the
-    // tiles in bands of eight row blocks, so that the workgroups an XCD runs together share rows and
-    // columns in its L2.  A grouped product has at most a.mtiles row blocks; the counts say how many.
-    RowBlock rb;
-    int mtiles = a.mtiles;
-    if (a.r.counts) find_rows(a.r, MP, -1, lane, rb, mtiles);
-    const int tiles = mtiles * a.nblocks;
-    const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
-    const int q8 = tiles >> 3, r8 = tiles & 7;
-    if (idx >= q8 + (xcd < r8 ? 1 : 0)) return;
-    const int lin = xcd * q8 + min(xcd, r8) + idx;
-    const int band = lin / (8 * a.nblocks), in_band = lin - band * 8 * a.nblocks;
-    const int band_rows = min(8, mtiles - 8 * band);
-    find_rows(a.r, MP, 8 * band + in_band % band_rows, lane, rb, mtiles);
-    const int nt0 = in_band / band_rows * NTT, nt_here = min(NTT, a.ntiles - nt0);
+    const int nt_here = min(NTT, a.ntiles - nt0);
 
     const int kb0 = SPLIT ? int(blockIdx.y) * a.bps : 0;
     const int nkb = SPLIT ? min(a.kblocks - kb0, a.bps) : a.kblocks;
@@ -498,6 +482,73 @@ __global__ void __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_
     }
 }
 
+// Which tile a workgroup takes.  Block b runs on XCD b mod 8: each XCD takes one contiguous run of the tile order, and
+// the tiles are ordered in bands of eight row blocks, so that the workgroups an XCD runs together share rows and columns
+// in its L2.  A grouped product has at most a.mtiles row blocks; the counts say how many.
+struct Tiles {
+    int mtiles, first, run, at;                            // row blocks; this XCD's run; the workgroup's place on it
+    __device__ Tiles(const F8Args &a, int rows, int lane) {
+        mtiles = a.mtiles;
+        RowBlock none;
+        if (a.r.counts) find_rows(a.r, rows, -1, lane, none, mtiles);
+        const int tiles = mtiles * a.nblocks, xcd = blockIdx.x & 7, q8 = tiles >> 3, r8 = tiles & 7;
+        first = xcd * q8 + min(xcd, r8);
+        run = q8 + (xcd < r8 ? 1 : 0);
+        at = blockIdx.x >> 3;
+    }
+    // rows of the run's tile `place`; its block of columns
+    __device__ int open(const F8Args &a, int rows, int place, int lane, RowBlock &rb) {
+        const int lin = first + place, band = lin / (8 * a.nblocks), in_band = lin - band * 8 * a.nblocks;
+        const int band_rows = min(8, mtiles - 8 * band);
+        find_rows(a.r, rows, 8 * band + in_band % band_rows, lane, rb, mtiles);
+        return in_band / band_rows;
+    }
+};
+
+template <int WN, int WK, int MT, int NT, int BS, int S, bool SPLIT, bool EXACT>
+__global__ void __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_eu(2))) f8_tile_kernel(F8Args a) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int lane = threadIdx.x & 63;
+    Tiles t(a, 16 * MT, lane);
+    if (t.at >= t.run) return;
+    RowBlock rb;
+    const int column = t.open(a, 16 * MT, t.at, lane, rb);
+    tile_product<WN, WK, MT, NT, BS, S, SPLIT, EXACT>(a, rb, column * NT * WN, lds);
+}
+
+// 128 x 256.  A workgroup fills a compute unit, so an XCD's 32 take the tiles of its run in rounds, and a last round of few
+// tiles would leave most of them idle for as long as a whole one takes: its tiles are cut in two (64 x 256) where they are
+// at most 16, in four (64 x 128) where they are at most 8.  2176 x 4096 x 14336: 186 -> 143 us, 2900: 192 -> 170, 4500: 291 ->
+// 263; 8192 ragged rows over 8 experts 564 -> 521.
+constexpr int XCD_UNITS = 32;
+__host__ __device__ constexpr int last_parts(int tiles) { return tiles <= XCD_UNITS / 4 ? 4 : (tiles <= XCD_UNITS / 2 ? 2 : 1); }
+constexpr int LAST_MORE = 3 * XCD_UNITS / 4;               // workgroups that cutting adds to an XCD's, at most
+template <bool EXACT>
+__global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) f8_large_kernel(F8Args a) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int lane = threadIdx.x & 63;
+    Tiles t(a, 128, lane);
+    const int last = t.run % XCD_UNITS, whole = t.run - last, parts = last_parts(last);
+    if (t.at >= whole + last * parts) return;
+    const int part = t.at < whole ? 0 : (t.at - whole) % parts, place = t.at < whole ? t.at : whole + (t.at - whole) / parts;
+    RowBlock rb;
+    const int column = t.open(a, 128, place, lane, rb);
+    if (t.at < whole || parts == 1) {
+        tile_product<8, 1, 8, 2, 1, 3, false, EXACT>(a, rb, column * 16, lds);
+        return;
+    }
+    const int down = 64 * (part & 1), right = 8 * (part >> 1);
+    rb.first += down;
+    rb.count = min(64, rb.count - down);
+    if (rb.count <= 0 || column * 16 + right >= a.ntiles) return;
+    if (parts == 2) tile_product<8, 1, 4, 2, 1, 4, false, EXACT>(a, rb, column * 16, lds);
+    else tile_product<8, 1, 4, 1, 1, 6, false, EXACT>(a, rb, column * 16 + right, lds);
+}
+constexpr int large_lds() {
+    const int a = tile_lds<8, 1, 8, 2, 1, 3>(), b = tile_lds<8, 1, 4, 2, 1, 4>(), c = tile_lds<8, 1, 4, 1, 1, 6>();
+    return a > b ? (a > c ? a : c) : (b > c ? b : c);
+}
+
 // Adds the splits' sums in their order and finishes: a thread takes four channels of one token at a time.
 __global__ void __launch_bounds__(256) f8_join_kernel(F8Args a) {
     const int per_row = a.ntiles * 4;
@@ -564,12 +615,21 @@ hipError_t launch_tiles_of(const F8Args &a, hipStream_t st) {
     return hipGetLastError();
 }
 
+template <bool EXACT>
+hipError_t launch_large(const F8Args &a, hipStream_t st) {
+    static_assert(large_lds() <= LDS_BYTES_MAX, "fits");
+    static LdsLimit limit;
+    const hipError_t e = limit.raise((const void *)f8_large_kernel<EXACT>, large_lds());
+    if (e != hipSuccess) return e;
+    const unsigned grid = unsigned((ceil_div(int64_t(a.mtiles) * a.nblocks, 8) + LAST_MORE) * 8);
+    hipLaunchKernelGGL(f8_large_kernel<EXACT>, dim3(grid), dim3(512), large_lds(), st, a);
+    return hipGetLastError();
+}
+
 template <int I>
 hipError_t launch_tiles(const F8Args &a, hipStream_t st) {
-    // the largest tiles are not split
-    if (I == FIRST_TILE || a.ks == 1) return a.out_f32 ? launch_tiles_of<I, false, true>(a, st) : launch_tiles_of<I, false, false>(a, st);
-    constexpr bool SPLIT = I != FIRST_TILE;
-    const hipError_t e = a.out_f32 ? launch_tiles_of<I, SPLIT, true>(a, st) : launch_tiles_of<I, SPLIT, false>(a, st);
+    if (a.ks == 1) return a.out_f32 ? launch_tiles_of<I, false, true>(a, st) : launch_tiles_of<I, false, false>(a, st);
+    const hipError_t e = a.out_f32 ? launch_tiles_of<I, true, true>(a, st) : launch_tiles_of<I, true, false>(a, st);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(f8_join_kernel, elementwise_grid(int64_t(a.r.rows) * a.ntiles * 4), dim3(256), 0, st, a);
     return hipGetLastError();
@@ -590,7 +650,7 @@ F8Plan make_f8_plan(const F8Layout &L, int64_t M, bool grouped, bool f32) {
     auto threads = [&](int c) {
         const F8Cfg &t = CFGS[c];
         const int64_t mt = most_row_blocks(M, L.E, grouped, 16 * t.MT);
-        return (t.kind == 0 ? columns(t) : ceil_div(mt * columns(t), 8) * 8) * 64 * t.WK * t.WN;
+        return (t.kind == 0 ? columns(t) : (ceil_div(mt * columns(t), 8) + LAST_MORE) * 8) * 64 * t.WK * t.WN;
     };
     const bool rows_fit = most_row_blocks(M, L.E, grouped, 16) <= 65535;    // the grid dimension that holds them
     if (M <= 16 * used && rows_fit) {
@@ -605,8 +665,14 @@ F8Plan make_f8_plan(const F8Layout &L, int64_t M, bool grouped, bool f32) {
             for (int ks : {1, 2, 4, 8}) {
                 const int64_t step = t.WK * t.BS, bps = ks == 1 ? L.kblocks : ceil_div(ceil_div(L.kblocks, ks), step) * step;
                 if (ks > 1 && (c <= FIRST_TILE || grouped || bps < 4 * step || ceil_div(L.kblocks, bps) < ks)) break;
-                const float more = float(ceil_div(mt * columns(t) * ks, 256) - 1);
-                float us = (1.0f + more * rate.block_more) * float(bps) * rate.block + (1.0f + more * rate.tile_more) * rate.tile;
+                const int64_t tiles = mt * columns(t) * ks;
+                float more = float(ceil_div(tiles, 256) - 1), first = 1.0f;
+                if (c == FIRST_TILE && tiles % 256) {      // a last round of few tiles, cut: measured shares of a whole one
+                    const int parts = last_parts(int(ceil_div(tiles % 256, 8)));
+                    if (tiles < 256) first = parts == 4 ? 0.45f : (parts == 2 ? 0.62f : 1.0f);
+                    else more += parts == 4 ? -0.67f : (parts == 2 ? -0.5f : 0.0f);
+                }
+                float us = (first + more * rate.block_more) * float(bps) * rate.block + (1.0f + more * rate.tile_more) * rate.tile;
                 if (ks > 1) us += JOIN_US[f32] + float(ks) * float(M) * float(L.ntiles) * TILE_N * 8.0f / JOIN_BYTES_PER_US[f32];
                 if (best == 0.0f || us < best) {
                     best = us;
@@ -640,7 +706,7 @@ hipError_t launch_f8_forward(const F8Layout &L, const F8Plan &p, const F8Args &a
     switch (p.cfg) {
         case 0: return launch_rows<0>(a, st);
         case 1: return launch_rows<1>(a, st);
-        case 2: return launch_tiles<2>(a, st);
+        case 2: return a.out_f32 ? launch_large<true>(a, st) : launch_large<false>(a, st);    // never split
         case 3: return launch_tiles<3>(a, st);
         case 4: return launch_tiles<4>(a, st);
         case 5: return launch_tiles<5>(a, st);

@@ -246,6 +246,37 @@ def test_schedules_exact(M, N, K):
     assert torch.equal(Q.linear_f8(x, xs, pw, bias=b), ref.float().bfloat16())
 
 
+@pytest.mark.parametrize("M,N,K", [(2100, 4100, 1184), (2750, 4100, 1184), (4700, 4096, 288 * 4 + 32), (2100, 4097, 2080)])
+def test_last_rounds_exact(M, N, K):
+    """The largest tiles in rounds whose last is cut in two or in four, row and column ends inside the parts."""
+    Q, g = _Q(), _gen(M + N + K)
+    tiles = -(-M // 128) * -(-N // 256)
+    assert 0 < tiles // 8 % 32 <= 15 and all(Q.f8_default_schedule(M, N, K, out_dtype=t).tile == 2 for t in (BF, F32))
+    x, xs = R.activations(g, M, K, True)
+    w, ws = R.weights(g, (N, K), True)
+    ref = (x.to(D) * R.spread_rows(xs, K)) @ R.dense_weight(w, ws).t()
+    pw = Q.pack_f8(w, ws)
+    assert torch.equal(Q.linear_f8(x, xs, pw, out_dtype=F32).to(D), ref)
+    assert torch.equal(Q.linear_f8(x, xs, pw), ref.float().bfloat16())
+
+
+@pytest.mark.parametrize("counts", [[900, 13, 1200, 87], [1, 0, 1900, 300], [550, 550, 550, 550]])
+def test_grouped_last_rounds_exact(counts):
+    Q, N, K, T = _Q(), 4100, 1184, sum(counts)
+    g = _gen(T)
+    assert Q.f8_default_schedule(T, N, K, 4).tile == 2
+    x, xs = R.activations(g, T, K, True)
+    w, ws = R.weights(g, (4, N, K), True)
+    out = torch.full((T + 5, N), 7.0, device="cuda", dtype=BF)
+    y = Q.grouped_linear_f8(x, xs, Q.pack_f8(w, ws), torch.tensor(counts, dtype=torch.int32, device="cuda"), out=out[:T])
+    at = 0
+    for e, c in enumerate(counts):
+        ref = (x[at:at + c].to(D) * R.spread_rows(xs[at:at + c], K)) @ R.dense_weight(w[e], ws[e]).t()
+        assert torch.equal(y[at:at + c], ref.float().bfloat16()), e
+        at += c
+    assert bool((out[T:] == 7.0).all())
+
+
 def test_nan_stays_in_its_row_and_channel():
     """A NaN code, or scale, reaches its own row or channel alone: also where a row ends inside a block and the next
     row begins with NaN."""
