@@ -12,19 +12,21 @@
 namespace ql {
 
 // The largest magnitude of the 128 values of a block, eight in each of sixteen lanes; infinity if
-// one is NaN (a maximum would drop it).
+// one is NaN.  Magnitudes compare as integers do, and NaN lies above them all (a maximum of floats would drop it).  The
+// sixteen lanes are a row of the wavefront, whose rotations need no LDS.
+template <int BY>
+__device__ inline uint32_t row_rotate(uint32_t m) {
+    return uint32_t(__builtin_amdgcn_update_dpp(0, int(m), 0x120 + BY, 0xF, 0xF, true));
+}
 __device__ inline float block_amax(const float (&v)[8]) {
-    float m = 0.0f;
-    bool bad = false;
+    uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        m = fmaxf(m, fabsf(v[j]));
-        bad |= v[j] != v[j];
-    }
-    if (bad) m = INFINITY;
-#pragma unroll
-    for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
-    return m;
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    m = max(m, row_rotate<8>(m));
+    m = max(m, row_rotate<4>(m));
+    m = max(m, row_rotate<2>(m));
+    m = max(m, row_rotate<1>(m));
+    return __uint_as_float(min(m, 0x7F800000u));
 }
 
 // amax / 448; NaN for a block with NaN or infinity, whose codes are then 0.
@@ -35,11 +37,12 @@ __device__ inline float block_scale(float amax) {
 // Codes of v / s, each the e4m3 value nearest to the exact quotient (ties to even).
 //
 // A quotient rounded to float32 first may land on the border between two codes from either side;
-// bf16 values in particular often lie next to one.  So the quotient is formed with its remainder and
-// rounded to odd, that is to the neighbour toward zero with its last bit set where a remainder is
-// left: that keeps it off every border that it does not lie on.  The mantissa of s alone is divided
-// by: scales at the ends of float32's range stay exact.  Eleven operations a value, next to 15 that
-// a value's bytes leave time for.
+// bf16 values in particular often lie next to one.  So the quotient, taken by a reciprocal (off by one unit of its
+// last place itself) and off by at most four, is rounded to a multiple q of sixteen units, which every border is; the sign of the remainder
+// v - q s, which one fused operation gives whatever its size, says on which side of q the exact quotient lies, less
+// than sixteen units away, and q is moved by one unit to that side.  The mantissa of s alone is divided by:
+// scales at the ends of float32's range stay exact.  Nine operations a value; a value's three bytes leave time for about
+// twenty, which reading it, its maximum and its address take some of.
 struct BlockDivisor {
     float s, inv;
     int e;
@@ -49,17 +52,14 @@ struct BlockDivisor {
         int x = 0;
         s = some ? frexpf(scale, &x) : 1.0f;
         e = -x;
-        inv = __fdiv_rn(1.0f, s);
+        inv = __builtin_amdgcn_rcpf(s);
     }
     __device__ float quotient(float v) const {
-        const float a = ldexpf(v, e);
-        const float q0 = a * inv;
-        const float q = fmaf(fmaf(-q0, s, a), inv, q0);
-        const float r = fmaf(-q, s, a);
-        uint32_t b = __float_as_uint(q);
-        // below 2^-20 the code is 0 either way
-        if (r != 0.0f && fabsf(q) > 9.5367431640625e-7f) b = (b - (((__float_as_uint(r) ^ b) >> 31) & 1u)) | 1u;
-        return fminf(fmaxf(__uint_as_float(b), -F8_MAX), F8_MAX);   // a scale with few bits may leave more
+        const float a = ldexpf(fabsf(v), e);
+        const int q = (__float_as_int(a * inv) + 8) & ~15;
+        const int r = __float_as_int(fmaf(-__int_as_float(q), s, a));   // negative, zero or positive as an integer too
+        const int b = min(q + min(max(r, -1), 1), __float_as_int(F8_MAX));    // a scale with few bits may leave more
+        return copysignf(__int_as_float(b), v);
     }
     __device__ u32x2 codes(const float (&v)[8]) const {
         if (!some) return u32x2{0u, 0u};

