@@ -177,10 +177,14 @@ __global__ void __launch_bounds__(64 * WK) f8_rows_kernel(F8Args a) {
 // order it goes from memory to the registers it is multiplied from, S stages ahead, and LDS holds and
 // serves the activations and their scales.
 //
-// A stage is BS blocks of 128 inputs: 128-byte runs of the rows, whose 16-byte pieces are swizzled so
+// A stage is a block of 128 inputs: 128-byte runs of the rows, whose 16-byte pieces are swizzled so
 // that sixteen rows' pieces spread over all banks.  Operands are read P tiles ahead.  One barrier a stage, P
 // tiles before its end: by then every wavefront has read all of the stage's operands and the next stage has
 // arrived, so the rows of the stage S on go to this one's place.
+//
+// 2048 x 4096 x 14336 takes 112 to 129 us by the card, 2.0 PFLOP/s (a library's product with one scale for each tensor
+// 130).  Nothing bounds it alone: its loads by themselves take 100 us (48 KiB a stage and compute unit through the caches),
+// its matrix instructions 56 to 70; without the joins it takes 111, without the operand reads 103.
 //
 // Scales come in panels of 32 blocks, 128 bytes of a row (and of the weight's rows of scales), swizzled in the
 // same way, the next panel while one is in use.  Taken block by block instead, 64 lanes a load fetched 64 cache
@@ -194,9 +198,9 @@ template <int MT>
 constexpr int panel_bytes() { return (16 * MT + 8) * PANEL_BLOCKS * 4; }   // the tokens' rows, and eight of the weight's
 template <int NT>
 constexpr int out_stride() { return NT * 32 + 16; }
-template <int WN, int WK, int MT, int NT, int BS, int S>
+template <int WN, int WK, int MT, int NT, int S>
 constexpr int tile_lds() {
-    const int ring = S * WK * BS * x_bytes<MT>() + 2 * panel_bytes<MT>(), rows = (WK - 1) * WN * MT * NT * 1024 + WN * 16 * out_stride<NT>();
+    const int ring = S * WK * x_bytes<MT>() + 2 * panel_bytes<MT>(), rows = (WK - 1) * WN * MT * NT * 1024 + WN * 16 * out_stride<NT>();
     return ring > rows ? ring : rows;
 }
 
@@ -258,17 +262,16 @@ __device__ inline void store_tiles(const F8Args &a, const RowBlock &rb, int ct0,
 }
 
 // EXACT: through the bf16 matrix cores.
-template <int WN, int WK, int MT, int NT, int BS, int S, bool SPLIT, bool EXACT>
+template <int WN, int WK, int MT, int NT, int S, bool SPLIT, bool EXACT>
 __device__ inline void tile_product(const F8Args &a, const RowBlock &rb, const int nt0, uint8_t *const lds) {
     constexpr int MP = 16 * MT, NTT = NT * WN;
     constexpr int XL = MP / 8 / WN;                        // 1 KiB loads of a block's rows a wavefront
-    constexpr int PER_STAGE = BS * (XL + 2 * NT);
-    constexpr int Q = BS * MT;                             // token tiles of a stage's blocks, one after another
+    constexpr int PER_STAGE = XL + 2 * NT;
     constexpr int P = ahead<MT>(), XB = MT >= 4 ? 4 : 2;   // operands read ahead, and buffers for them
     static_assert(XL * WN * 8 == MP && XL >= 1, "loads divide evenly");
-    static_assert((S * Q) % XB == 0 && P < XB && P < MT, "buffers come round");
+    static_assert((S * MT) % XB == 0 && P < XB && P < MT, "buffers come round");
     static_assert(F8_BLOCK % (16 * NT) == 0 && NTT * TILE_N <= 8 * F8_BLOCK, "one weight scale a wavefront and block, eight rows of them");
-    static_assert(PANEL_BLOCKS % (BS * WK) == 0 && PANEL_BLOCKS / (BS * WK) > 2 * S, "a panel lasts longer than a load takes");
+    static_assert(PANEL_BLOCKS % WK == 0 && PANEL_BLOCKS / WK > 2 * S, "a panel lasts longer than a load takes");
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -278,7 +281,7 @@ __device__ inline void tile_product(const F8Args &a, const RowBlock &rb, const i
 
     const int kb0 = SPLIT ? int(blockIdx.y) * a.bps : 0;
     const int nkb = SPLIT ? min(a.kblocks - kb0, a.bps) : a.kblocks;
-    const int nst = (nkb + BS * WK - 1) / (BS * WK);
+    const int nst = (nkb + WK - 1) / WK;
 
     const __amdgpu_buffer_rsrc_t wr = make_uniform_rsrc(
         a.w + uint64_t(rb.expert) * a.w_stride + int64_t(nt0) * a.kblocks * F8_TILE_BYTES,
@@ -289,7 +292,7 @@ __device__ inline void tile_product(const F8Args &a, const RowBlock &rb, const i
     const __amdgpu_buffer_rsrc_t vr =
         make_uniform_rsrc(a.ws + (int64_t(rb.expert) * a.nbs + nb0) * a.kblocks, uint32_t(nb_here) * uint32_t(a.kblocks) * 4u);
 
-    const int k_first = kb0 + wk * BS;                     // first block of the wavefront's first stage
+    const int k_first = kb0 + wk;                          // the wavefront's first block
     // A wavefront's first rows of a block; the others lie a fixed distance on, those past the last past the range.
     static_assert(WN % 2 == 0, "a wavefront's rows have one swizzle");
     const int x_row = wn * 8 + (lane >> 3), x_piece = (lane & 7) ^ ((x_row >> 1) & 7);
@@ -302,19 +305,15 @@ __device__ inline void tile_product(const F8Args &a, const RowBlock &rb, const i
         const int tile = wn * NT + j;
         w_off[j] = tile < nt_here ? (uint32_t(tile) * uint32_t(a.kblocks) + uint32_t(k_first)) * F8_TILE_BYTES + 16u * lane : OUT_OF_RANGE;
     }
-    constexpr int BLOCK = x_bytes<MT>(), STAGE = BS * BLOCK;
+    constexpr int STAGE = x_bytes<MT>();
     uint8_t *const ring = lds + wk * (S * STAGE);
-    auto past = [&](int st, int b) { return (st * WK + wk) * BS + b < nkb ? 0u : OUT_OF_RANGE; };
+    auto past = [&](int st) { return st * WK + wk < nkb ? 0u : OUT_OF_RANGE; };
     auto load_x = [&](int st, int u) {
+        const int on = st * WK;                            // blocks after the first
 #pragma unroll
-        for (int b = 0; b < BS; ++b) {
-            const int on = st * WK * BS + b;               // blocks after the first
-            uint8_t *const to = ring + u * STAGE + b * BLOCK;
-#pragma unroll
-            for (int q = 0; q < XL; ++q)
-                ld128_lds(xr, on * F8_BLOCK < x_left ? (x_off + uint32_t(q) * x_far + uint32_t(on) * F8_BLOCK) | past(st, b) : OUT_OF_RANGE,
-                          to + (wn + WN * q) * 1024);
-        }
+        for (int q = 0; q < XL; ++q)
+            ld128_lds(xr, on * F8_BLOCK < x_left ? (x_off + uint32_t(q) * x_far + uint32_t(on) * F8_BLOCK) | past(st) : OUT_OF_RANGE,
+                      ring + u * STAGE + (wn + WN * q) * 1024);
     };
     uint8_t *const panels = lds + WK * S * STAGE;
     constexpr int PANEL = panel_bytes<MT>();
@@ -337,30 +336,30 @@ __device__ inline void tile_product(const F8Args &a, const RowBlock &rb, const i
             else if (unit == MP / 8) ld128_lds(vr, p_off[q] + uint32_t(at) * (PANEL_BLOCKS * 4), to);
         }
     };
-    Operand w[S][BS][NT], x[XB];
-    auto load_w = [&](int st, int u, int b) {
+    Operand w[S][NT], x[XB];
+    auto load_w = [&](int st, int u) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const uint32_t off = w_off[j] + uint32_t(st * WK * BS + b) * F8_TILE_BYTES;
-            w[u][b][j].lo = ld128(wr, off | past(st, b));
-            w[u][b][j].hi = ld128(wr, (off + 1024u) | past(st, b));
+            const uint32_t off = w_off[j] + uint32_t(st * WK) * F8_TILE_BYTES;
+            w[u][j].lo = ld128(wr, off | past(st));
+            w[u][j].hi = ld128(wr, (off + 1024u) | past(st));
         }
     };
     const uint8_t *const x_at[2] = {ring + c * 128 + ((g ^ (c >> 1)) * 16), ring + c * 128 + (((4 + g) ^ (c >> 1)) * 16)};
     // token tile q of the stage st in place u, those past its last from the next stage, with their scales
     float f[XB], v;                                        // the tokens' scales, the weight's of a block
     const int v_row = (nt0 + wn * NT) * TILE_N / F8_BLOCK - nb0;
-    auto scale_at = [&](int st, int b, int row) {          // of rows with the same low bits as `row`
-        const int block = (st * WK + wk) * BS + b, word = block & (PANEL_BLOCKS - 1);
+    auto scale_at = [&](int st, int row) {                 // of rows with the same low bits as `row`
+        const int block = st * WK + wk, word = block & (PANEL_BLOCKS - 1);
         return panels + (block / PANEL_BLOCKS & 1) * PANEL + (((word >> 2) ^ (row & 7)) * 16) + (word & 3) * 4;
     };
     auto read_x = [&](int st, int u, int q) {
-        const int at = (q < Q ? u : (u + 1) % S) * STAGE + q % Q / MT * BLOCK + q % MT * 2048, to = (u * Q + q) % XB;
+        const int at = (q < MT ? u : (u + 1) % S) * STAGE + q % MT * 2048, to = (u * MT + q) % XB;
         x[to].lo = *reinterpret_cast<const u32x4 *>(x_at[0] + at);
         x[to].hi = *reinterpret_cast<const u32x4 *>(x_at[1] + at);
-        f[to] = *reinterpret_cast<const float *>(scale_at(q < Q ? st : st + 1, q % Q / MT, c) + c * 128 + q % MT * 2048);
+        f[to] = *reinterpret_cast<const float *>(scale_at(q < MT ? st : st + 1, c) + c * 128 + q % MT * 2048);
     };
-    auto read_v = [&](int st, int b) { v = *reinterpret_cast<const float *>(scale_at(st, b, v_row) + (MP + v_row) * 128); };
+    auto read_v = [&](int st) { v = *reinterpret_cast<const float *>(scale_at(st, v_row) + (MP + v_row) * 128); };
 
     f32x4 acc[NT][MT];
 #pragma unroll
@@ -374,67 +373,62 @@ __device__ inline void tile_product(const F8Args &a, const RowBlock &rb, const i
     for (int u = 0; u < S; ++u) {
         load_x(u, u);
         __builtin_amdgcn_sched_barrier(0);                 // the waits count loads in this order
-#pragma unroll
-        for (int b = 0; b < BS; ++b) load_w(u, u, b);
+        load_w(u, u);
         __builtin_amdgcn_sched_barrier(0);
     }
     wait_vmcnt<(S - 1) * PER_STAGE>();
     ring_barrier();
 #pragma unroll
     for (int i = 0; i < P; ++i) read_x(0, 0, i);
-    read_v(0, 0);
+    read_v(0);
 
     // Stage st in place u.  A tile's sums are joined while the next tile's instructions run.
     auto stage = [&](int st, int u, bool more) {
         f32x4 sum[2][NT];
+        const float w_scale = v;
+        float s[2];
+        Wide wide[EXACT ? NT : 1];
+        if constexpr (EXACT)
 #pragma unroll
-        for (int b = 0; b < BS; ++b) {
-            const float w_scale = v;
-            float s[2];
-            Wide wide[EXACT ? NT : 1];
-            if constexpr (EXACT)
+            for (int j = 0; j < NT; ++j) wide[j] = widen(w[u][j]);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) wide[j] = widen(w[u][b][j]);
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const int q = b * MT + i;
-                if (q == Q - P) {
-                    // weights of the stage S on that are under way already
-                    if (more) wait_vmcnt<(S - 2) * PER_STAGE + (BS - 1) * 2 * NT>();
-                    ring_barrier();
-                    if (more) load_x(st + S, u);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-                if (i == MT - P) read_v(b + 1 < BS ? st : st + 1, (b + 1) % BS);
-                s[i & 1] = f[(u * Q + q) % XB] * w_scale;
-                // past the last block: weights that read as zero, but whatever scales lie there
-                if (BS * WK > 1 && past(st, b)) s[i & 1] = 0.0f;
-                if constexpr (EXACT) {
-                    const Wide xw = widen(x[(u * Q + q) % XB]);
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) sum[i & 1][j] = block_product(wide[j], xw);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) sum[i & 1][j] = block_product(w[u][b][j], x[(u * Q + q) % XB]);
-                }
-                read_x(st, u, q + P);
-                __builtin_amdgcn_sched_barrier(0);         // joined first, the last sums would be waited for
-                if (i > 0)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) join(acc[j][i - 1], sum[(i - 1) & 1][j], s[(i - 1) & 1]);
+        for (int i = 0; i < MT; ++i) {
+            if (i == MT - P) {
+                // the next stage has arrived, those after it may be under way
+                if (more) wait_vmcnt<(S - 2) * PER_STAGE>();
+                ring_barrier();
+                if (more) load_x(st + S, u);
                 __builtin_amdgcn_sched_barrier(0);
+                read_v(st + 1);
             }
-            if (more) load_w(st + S, u, b);
-            __builtin_amdgcn_sched_barrier(0);
+            s[i & 1] = f[(u * MT + i) % XB] * w_scale;
+            // past the last block: weights that read as zero, but whatever scales lie there
+            if (WK > 1 && past(st)) s[i & 1] = 0.0f;
+            if constexpr (EXACT) {
+                const Wide xw = widen(x[(u * MT + i) % XB]);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) join(acc[j][MT - 1], sum[(MT - 1) & 1][j], s[(MT - 1) & 1]);
+                for (int j = 0; j < NT; ++j) sum[i & 1][j] = block_product(wide[j], xw);
+            } else {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) sum[i & 1][j] = block_product(w[u][j], x[(u * MT + i) % XB]);
+            }
+            read_x(st, u, i + P);
+            __builtin_amdgcn_sched_barrier(0);             // joined first, the last sums would be waited for
+            if (i > 0)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) join(acc[j][i - 1], sum[(i - 1) & 1][j], s[(i - 1) & 1]);
+            __builtin_amdgcn_sched_barrier(0);
         }
+        if (more) load_w(st + S, u);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) join(acc[j][MT - 1], sum[(MT - 1) & 1][j], s[(MT - 1) & 1]);
     };
     int st = 0, panel = 2;
     for (; st + S <= nst; st += S) {
         // Every wavefront has read the scales of stage st - 1: the panel before its own is free.  The next is read C - S
         // stages on at the earliest, and the waits, which count its loads as a stage's, have seen to them by then.
-        constexpr int C = PANEL_BLOCKS / (BS * WK);
+        constexpr int C = PANEL_BLOCKS / WK;
         if (st > (panel - 1) * C) load_panel(panel++);
 #pragma unroll
         for (int u = 0; u < S; ++u) stage(st + u, u, true);
@@ -505,7 +499,7 @@ struct Tiles {
     }
 };
 
-template <int WN, int WK, int MT, int NT, int BS, int S, bool SPLIT, bool EXACT>
+template <int WN, int WK, int MT, int NT, int S, bool SPLIT, bool EXACT>
 __global__ void __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_eu(2))) f8_tile_kernel(F8Args a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int lane = threadIdx.x & 63;
@@ -513,7 +507,7 @@ __global__ void __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_
     if (t.at >= t.run) return;
     RowBlock rb;
     const int column = t.open(a, 16 * MT, t.at, lane, rb);
-    tile_product<WN, WK, MT, NT, BS, S, SPLIT, EXACT>(a, rb, column * NT * WN, lds);
+    tile_product<WN, WK, MT, NT, S, SPLIT, EXACT>(a, rb, column * NT * WN, lds);
 }
 
 // 128 x 256.  A workgroup fills a compute unit, so an XCD's 32 take the tiles of its run in rounds, and a last round of few
@@ -534,18 +528,18 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) f
     RowBlock rb;
     const int column = t.open(a, 128, place, lane, rb);
     if (t.at < whole || parts == 1) {
-        tile_product<8, 1, 8, 2, 1, 3, false, EXACT>(a, rb, column * 16, lds);
+        tile_product<8, 1, 8, 2, 3, false, EXACT>(a, rb, column * 16, lds);
         return;
     }
     const int down = 64 * (part & 1), right = 8 * (part >> 1);
     rb.first += down;
     rb.count = min(64, rb.count - down);
     if (rb.count <= 0 || column * 16 + right >= a.ntiles) return;
-    if (parts == 2) tile_product<8, 1, 4, 2, 1, 4, false, EXACT>(a, rb, column * 16, lds);
-    else tile_product<8, 1, 4, 1, 1, 6, false, EXACT>(a, rb, column * 16 + right, lds);
+    if (parts == 2) tile_product<8, 1, 4, 2, 4, false, EXACT>(a, rb, column * 16, lds);
+    else tile_product<8, 1, 4, 1, 6, false, EXACT>(a, rb, column * 16 + right, lds);
 }
 constexpr int large_lds() {
-    const int a = tile_lds<8, 1, 8, 2, 1, 3>(), b = tile_lds<8, 1, 4, 2, 1, 4>(), c = tile_lds<8, 1, 4, 1, 1, 6>();
+    const int a = tile_lds<8, 1, 8, 2, 3>(), b = tile_lds<8, 1, 4, 2, 4>(), c = tile_lds<8, 1, 4, 1, 6>();
     return a > b ? (a > c ? a : c) : (b > c ? b : c);
 }
 
@@ -563,19 +557,16 @@ __global__ void __launch_bounds__(256) f8_join_kernel(F8Args a) {
 }
 
 // Schedules.  kind 0 (few rows): NT column tiles a workgroup, WK wavefronts on alternate blocks; kind
-// 1 (tiles): WN wavefronts of MT x NT tiles, WK times on alternate stages of BS blocks, a ring of S stages.
-struct F8Cfg { int kind, MT, NT, WK, WN, BS, S; };
+// 1 (tiles): WN wavefronts of MT x NT tiles, WK times on alternate blocks, a ring of S stages.
+struct F8Cfg { int kind, MT, NT, WK, WN, S; };
 constexpr F8Cfg CFGS[] = {
-    {0, 1, 1, 8, 1, 1, 0}, {0, 1, 2, 8, 1, 1, 0},
-    {1, 8, 2, 1, 8, 1, 3},      // 128 x 256
-    {1, 4, 2, 1, 8, 1, 4},      // 64 x 256
-    {1, 4, 2, 1, 4, 1, 4},      // 64 x 128
-    {1, 4, 1, 2, 4, 1, 4},      // 64 x 64, two groups
-    {1, 2, 2, 1, 4, 1, 6},      // 32 x 128
-    {1, 2, 1, 2, 4, 1, 6},      // 32 x 64, two groups
-#ifdef EXTRA
-    EXTRA
-#endif
+    {0, 1, 1, 8, 1, 0}, {0, 1, 2, 8, 1, 0},
+    {1, 8, 2, 1, 8, 3},      // 128 x 256, for the schedule's choice: its kernel names its own
+    {1, 4, 2, 1, 8, 4},      // 64 x 256
+    {1, 4, 2, 1, 4, 4},      // 64 x 128
+    {1, 4, 1, 2, 4, 4},      // 64 x 64, two groups
+    {1, 2, 2, 1, 4, 6},      // 32 x 128
+    {1, 2, 1, 2, 4, 6},      // 32 x 64, two groups
 };
 constexpr int NUM_CFGS = 8, FIRST_TILE = 2;
 // Microseconds that a compute unit takes for one block of a workgroup's tile, and for the tile besides (start, first
@@ -603,9 +594,9 @@ hipError_t launch_rows(const F8Args &a, hipStream_t st) {
 template <int I, bool SPLIT, bool EXACT>
 hipError_t launch_tiles_of(const F8Args &a, hipStream_t st) {
     constexpr F8Cfg t = CFGS[I];
-    constexpr size_t lds = tile_lds<t.WN, t.WK, t.MT, t.NT, t.BS, t.S>();
+    constexpr size_t lds = tile_lds<t.WN, t.WK, t.MT, t.NT, t.S>();
     static_assert(lds <= LDS_BYTES_MAX, "fits");
-    auto kern = f8_tile_kernel<t.WN, t.WK, t.MT, t.NT, t.BS, t.S, SPLIT, EXACT>;
+    auto kern = f8_tile_kernel<t.WN, t.WK, t.MT, t.NT, t.S, SPLIT, EXACT>;
     static LdsLimit limit;
     const hipError_t e = limit.raise((const void *)kern, int(lds));
     if (e != hipSuccess) return e;
@@ -663,7 +654,7 @@ F8Plan make_f8_plan(const F8Layout &L, int64_t M, bool grouped, bool f32) {
             if (c > FIRST_TILE && threads(c) > LAUNCH_THREADS_MAX) continue;    // where the largest do not fit, none does
             const int64_t block = 16 * t.MT, mt = grouped ? std::max(used, ceil_div(2 * M + used * block, 2 * block)) : ceil_div(M, block);
             for (int ks : {1, 2, 4, 8}) {
-                const int64_t step = t.WK * t.BS, bps = ks == 1 ? L.kblocks : ceil_div(ceil_div(L.kblocks, ks), step) * step;
+                const int64_t step = t.WK, bps = ks == 1 ? L.kblocks : ceil_div(ceil_div(L.kblocks, ks), step) * step;
                 if (ks > 1 && (c <= FIRST_TILE || grouped || bps < 4 * step || ceil_div(L.kblocks, bps) < ks)) break;
                 const int64_t tiles = mt * columns(t) * ks;
                 float more = float(ceil_div(tiles, 256) - 1), first = 1.0f;

@@ -557,6 +557,8 @@ ql_status qlinear_f8_unpack(int64_t E, int64_t N, int64_t K, const void *packed,
  * 16-byte aligned.  Neither dy nor the codes are rounded.  Its workspace holds partial sums of split channels,
  * and a copy of dy where N is not a multiple of eight.
  *
+ * The product of two scales is formed in float32.
+ *
  * qlinear_f8_default_schedule: tile (rows x outputs of a workgroup) and splits of the summed dimension (out_dtype is
  * the forward product's, bf16 for the backward one):
  *   forward   0: 16 x 16, 1: 16 x 32, 2: 128 x 256, 3: 64 x 256, 4: 64 x 128, 5: 64 x 64, 6: 32 x 128, 7: 32 x 64
