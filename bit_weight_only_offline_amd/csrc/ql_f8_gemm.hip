@@ -510,36 +510,46 @@ __global__ void __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_
     tile_product<WN, WK, MT, NT, S, SPLIT, EXACT>(a, rb, column * NT * WN, lds);
 }
 
-// 128 x 256.  A workgroup fills a compute unit, so an XCD's 32 take the tiles of its run in rounds, and a last round of few
-// tiles would leave most of them idle for as long as a whole one takes: its tiles are cut in two (64 x 256) where they are
-// at most 16, in four (64 x 128) where they are at most 8.  2176 x 4096 x 14336: 186 -> 143 us, 2900: 192 -> 170, 4500: 291 ->
-// 263; 8192 ragged rows over 8 experts 564 -> 521.
+// Stages of the ring of eight wavefronts of MT x NT tiles.
+template <int MT, int NT>
+constexpr int large_ring() { return MT == 16 ? 2 : (MT == 8 ? (NT == 2 ? 3 : 4) : (NT == 2 ? 4 : 6)); }
+
+// 128 x 256 and 256 x 256 (TALL), which reads three quarters of the operand bytes and loses more to the ends of rounds and
+// experts: 8192 x 4096 x 14336 435 -> 406 us (2.4 PFLOP/s), 8192 x 14336 x 4096 475 -> 426, but 3000 x 4096 x 14336 174 -> 188.
+// Its blocks of at most half the rows take the tile of half the rows (1 to 3% of ragged grouped products).  A workgroup fills a compute unit, so an XCD's 32 take the tiles of its run in rounds, and
+// a last round of few tiles would leave most of them idle for as long as a whole one takes: its tiles are cut in two (half the
+// rows) where they are at most 16, in four (half the columns too) where they are at most 8.  2176 x 4096 x 14336: 186 -> 143
+// us, 2900: 192 -> 170, 4500: 291 -> 263; 8192 ragged rows over 8 experts 564 -> 521.
 constexpr int XCD_UNITS = 32;
 __host__ __device__ constexpr int last_parts(int tiles) { return tiles <= XCD_UNITS / 4 ? 4 : (tiles <= XCD_UNITS / 2 ? 2 : 1); }
 constexpr int LAST_MORE = 3 * XCD_UNITS / 4;               // workgroups that cutting adds to an XCD's, at most
-template <bool EXACT>
+template <bool TALL, bool EXACT>
 __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) f8_large_kernel(F8Args a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    constexpr int MT = TALL ? 16 : 8, HALF = 8 * MT;
     const int lane = threadIdx.x & 63;
-    Tiles t(a, 128, lane);
+    Tiles t(a, 2 * HALF, lane);
     const int last = t.run % XCD_UNITS, whole = t.run - last, parts = last_parts(last);
     if (t.at >= whole + last * parts) return;
     const int part = t.at < whole ? 0 : (t.at - whole) % parts, place = t.at < whole ? t.at : whole + (t.at - whole) / parts;
     RowBlock rb;
-    const int column = t.open(a, 128, place, lane, rb);
+    const int column = t.open(a, 2 * HALF, place, lane, rb);
     if (t.at < whole || parts == 1) {
-        tile_product<8, 1, 8, 2, 3, false, EXACT>(a, rb, column * 16, lds);
+        if (TALL && rb.count <= HALF) tile_product<8, 1, MT / 2, 2, large_ring<MT / 2, 2>(), false, EXACT>(a, rb, column * 16, lds);
+        else tile_product<8, 1, MT, 2, large_ring<MT, 2>(), false, EXACT>(a, rb, column * 16, lds);
         return;
     }
-    const int down = 64 * (part & 1), right = 8 * (part >> 1);
+    const int down = HALF * (part & 1), right = 8 * (part >> 1);
     rb.first += down;
-    rb.count = min(64, rb.count - down);
+    rb.count = min(HALF, rb.count - down);
     if (rb.count <= 0 || column * 16 + right >= a.ntiles) return;
-    if (parts == 2) tile_product<8, 1, 4, 2, 4, false, EXACT>(a, rb, column * 16, lds);
-    else tile_product<8, 1, 4, 1, 6, false, EXACT>(a, rb, column * 16 + right, lds);
+    if (parts == 2) tile_product<8, 1, MT / 2, 2, large_ring<MT / 2, 2>(), false, EXACT>(a, rb, column * 16, lds);
+    else tile_product<8, 1, MT / 2, 1, large_ring<MT / 2, 1>(), false, EXACT>(a, rb, column * 16 + right, lds);
 }
+template <int MT>
 constexpr int large_lds() {
-    const int a = tile_lds<8, 1, 8, 2, 3>(), b = tile_lds<8, 1, 4, 2, 4>(), c = tile_lds<8, 1, 4, 1, 6>();
+    const int a = tile_lds<8, 1, MT, 2, large_ring<MT, 2>()>(), b = tile_lds<8, 1, MT / 2, 2, large_ring<MT / 2, 2>()>(),
+              c = tile_lds<8, 1, MT / 2, 1, large_ring<MT / 2, 1>()>();
     return a > b ? (a > c ? a : c) : (b > c ? b : c);
 }
 
@@ -561,25 +571,29 @@ __global__ void __launch_bounds__(256) f8_join_kernel(F8Args a) {
 struct F8Cfg { int kind, MT, NT, WK, WN, S; };
 constexpr F8Cfg CFGS[] = {
     {0, 1, 1, 8, 1, 0}, {0, 1, 2, 8, 1, 0},
-    {1, 8, 2, 1, 8, 3},      // 128 x 256, for the schedule's choice: its kernel names its own
+    {1, 8, 2, 1, 8, 3},      // 128 x 256, with a kernel of its own
     {1, 4, 2, 1, 8, 4},      // 64 x 256
     {1, 4, 2, 1, 4, 4},      // 64 x 128
     {1, 4, 1, 2, 4, 4},      // 64 x 64, two groups
     {1, 2, 2, 1, 4, 6},      // 32 x 128
     {1, 2, 1, 2, 4, 6},      // 32 x 64, two groups
+    {1, 16, 2, 1, 8, 2},     // 256 x 256, with the same kernel as 2
 };
-constexpr int NUM_CFGS = 8, FIRST_TILE = 2;
+constexpr int NUM_CFGS = 9, FIRST_TILE = 2, TALL_TILE = 8;
 // Microseconds that a compute unit takes for one block of a workgroup's tile, and for the tile besides (start, first
 // loads, stores); and what a round of 256 workgroups after the first takes of either, less where several share a unit,
 // more where the operands of more workgroups pass through the caches.  For results in bf16 and, through the bf16 cores,
 // in float32.  Fitted to 60 sizes each, 20 to 8192 x 4096 x 14336, 14336 x 4096, 4096 x 4096, 5001 x 4128 and 2048 x
-// 2048, every schedule in one to eight splits; the choice was within 6% of the fastest at each.
+// 2048, every schedule in one to eight splits, and in bf16 the large tiles' to 64 of 300 to 32768 rows: the choice was within
+// 10% of the fastest at each, 1% at the median, and 14% where a grouped product's rows fill its blocks, which cannot be known.
 struct F8Rate { float block, tile, tile_more, block_more; };
 constexpr F8Rate RATES[2][NUM_CFGS] = {
-    {{0.105f, 5.1f, 0.18f, 1.11f}, {0.105f, 5.1f, 0.18f, 1.11f}, {0.80f, 6.6f, 0.24f, 1.31f}, {0.433f, 5.7f, 0.09f, 1.54f},
-     {0.296f, 5.6f, 0.0f, 1.05f}, {0.20f, 5.0f, 0.36f, 1.04f}, {0.20f, 5.0f, 0.0f, 1.09f}, {0.104f, 5.15f, 0.1f, 1.2f}},
+    {{0.105f, 5.1f, 0.18f, 1.11f}, {0.105f, 5.1f, 0.18f, 1.11f}, {0.87f, 6.6f, 0.8f, 1.05f}, {0.433f, 5.7f, 0.09f, 1.54f},
+     {0.296f, 5.6f, 0.12f, 1.05f}, {0.20f, 5.0f, 0.36f, 1.04f}, {0.20f, 5.0f, 0.0f, 1.09f}, {0.104f, 5.15f, 0.1f, 1.2f},
+     {1.77f, 7.2f, 1.0f, 0.97f}},
     {{0.086f, 6.3f, 0.01f, 1.49f}, {0.086f, 6.3f, 0.01f, 1.49f}, {1.195f, 18.1f, 0.84f, 1.2f}, {0.629f, 12.6f, 0.24f, 1.73f},
-     {0.421f, 7.3f, 0.63f, 0.79f}, {0.337f, 5.6f, 0.53f, 1.04f}, {0.312f, 6.5f, 0.17f, 0.93f}, {0.169f, 6.2f, 0.14f, 1.05f}},
+     {0.421f, 7.3f, 0.63f, 0.79f}, {0.337f, 5.6f, 0.53f, 1.04f}, {0.312f, 6.5f, 0.17f, 0.93f}, {0.169f, 6.2f, 0.14f, 1.05f},
+     {0.0f, 0.0f, 0.0f, 0.0f}},
 };
 constexpr float JOIN_US[2] = {4.0f, 3.1f}, JOIN_BYTES_PER_US[2] = {7.8e6f, 2.0e7f};
 
@@ -606,14 +620,16 @@ hipError_t launch_tiles_of(const F8Args &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <bool EXACT>
+template <bool TALL, bool EXACT>
 hipError_t launch_large(const F8Args &a, hipStream_t st) {
-    static_assert(large_lds() <= LDS_BYTES_MAX, "fits");
+    constexpr int lds = large_lds<TALL ? 16 : 8>();
+    static_assert(lds <= LDS_BYTES_MAX, "fits");
+    auto kern = f8_large_kernel<TALL, EXACT>;
     static LdsLimit limit;
-    const hipError_t e = limit.raise((const void *)f8_large_kernel<EXACT>, large_lds());
+    const hipError_t e = limit.raise((const void *)kern, lds);
     if (e != hipSuccess) return e;
     const unsigned grid = unsigned((ceil_div(int64_t(a.mtiles) * a.nblocks, 8) + LAST_MORE) * 8);
-    hipLaunchKernelGGL(f8_large_kernel<EXACT>, dim3(grid), dim3(512), large_lds(), st, a);
+    hipLaunchKernelGGL(kern, dim3(grid), dim3(512), lds, st, a);
     return hipGetLastError();
 }
 
@@ -651,14 +667,17 @@ F8Plan make_f8_plan(const F8Layout &L, int64_t M, bool grouped, bool f32) {
         for (int c = M <= 64 * used && rows_fit ? 1 : FIRST_TILE; c < NUM_CFGS; ++c) {
             const F8Cfg &t = CFGS[c];
             const F8Rate &rate = RATES[f32][c];
-            if (c > FIRST_TILE && threads(c) > LAUNCH_THREADS_MAX) continue;    // where the largest do not fit, none does
+            const bool large = c == FIRST_TILE || c == TALL_TILE;
+            const int largest = f32 ? FIRST_TILE : TALL_TILE;    // 256 x 256 has no registers for operands as bf16
+            if (f32 && c == TALL_TILE) continue;
+            if (c != largest && threads(c) > LAUNCH_THREADS_MAX) continue;    // where the largest do not fit, none does
             const int64_t block = 16 * t.MT, mt = grouped ? std::max(used, ceil_div(2 * M + used * block, 2 * block)) : ceil_div(M, block);
             for (int ks : {1, 2, 4, 8}) {
                 const int64_t step = t.WK, bps = ks == 1 ? L.kblocks : ceil_div(ceil_div(L.kblocks, ks), step) * step;
-                if (ks > 1 && (c <= FIRST_TILE || grouped || bps < 4 * step || ceil_div(L.kblocks, bps) < ks)) break;
+                if (ks > 1 && (c < FIRST_TILE || large || grouped || bps < 4 * step || ceil_div(L.kblocks, bps) < ks)) break;
                 const int64_t tiles = mt * columns(t) * ks;
                 float more = float(ceil_div(tiles, 256) - 1), first = 1.0f;
-                if (c == FIRST_TILE && tiles % 256) {      // a last round of few tiles, cut: measured shares of a whole one
+                if (large && tiles % 256) {      // a last round of few tiles, cut: measured shares of a whole one
                     const int parts = last_parts(int(ceil_div(tiles % 256, 8)));
                     if (tiles < 256) first = parts == 4 ? 0.45f : (parts == 2 ? 0.62f : 1.0f);
                     else more += parts == 4 ? -0.67f : (parts == 2 ? -0.5f : 0.0f);
@@ -697,12 +716,13 @@ hipError_t launch_f8_forward(const F8Layout &L, const F8Plan &p, const F8Args &a
     switch (p.cfg) {
         case 0: return launch_rows<0>(a, st);
         case 1: return launch_rows<1>(a, st);
-        case 2: return a.out_f32 ? launch_large<true>(a, st) : launch_large<false>(a, st);    // never split
+        case 2: return a.out_f32 ? launch_large<false, true>(a, st) : launch_large<false, false>(a, st);    // never split
         case 3: return launch_tiles<3>(a, st);
         case 4: return launch_tiles<4>(a, st);
         case 5: return launch_tiles<5>(a, st);
         case 6: return launch_tiles<6>(a, st);
-        default: return launch_tiles<7>(a, st);
+        case 7: return launch_tiles<7>(a, st);
+        default: return launch_large<true, false>(a, st);                  // bf16 alone
     }
 }
 

@@ -561,7 +561,8 @@ ql_status qlinear_f8_unpack(int64_t E, int64_t N, int64_t K, const void *packed,
  *
  * qlinear_f8_default_schedule: tile (rows x outputs of a workgroup) and splits of the summed dimension (out_dtype is
  * the forward product's, bf16 for the backward one):
- *   forward   0: 16 x 16, 1: 16 x 32, 2: 128 x 256, 3: 64 x 256, 4: 64 x 128, 5: 64 x 64, 6: 32 x 128, 7: 32 x 64
+ *   forward   0: 16 x 16, 1: 16 x 32, 2: 128 x 256, 3: 64 x 256, 4: 64 x 128, 5: 64 x 64, 6: 32 x 128, 7: 32 x 64,
+ *             8: 256 x 256 (bf16)
  *   backward  0: 256, 1: 64, 2: 32, 3: 16 rows, all x 256
  */
 ql_status qlinear_f8_default_schedule(int64_t M, int64_t E, int64_t N, int64_t K, int grouped, int backward,

@@ -246,9 +246,9 @@ def test_schedules_exact(M, N, K):
     assert torch.equal(Q.linear_f8(x, xs, pw, bias=b), ref.float().bfloat16())
 
 
-@pytest.mark.parametrize("M,N,K", [(2100, 4100, 1184), (2750, 4100, 1184), (4700, 4096, 288 * 4 + 32), (2100, 4097, 2080)])
+@pytest.mark.parametrize("M,N,K", [(2100, 4100, 1184), (2750, 4100, 1184), (4700, 4100, 1184), (2100, 4097, 2080)])
 def test_last_rounds_exact(M, N, K):
-    """The largest tiles in rounds whose last is cut in two or in four, row and column ends inside the parts."""
+    """Tiles of 128 x 256 in rounds whose last is cut in two or in four, row and column ends inside the parts."""
     Q, g = _Q(), _gen(M + N + K)
     tiles = -(-M // 128) * -(-N // 256)
     assert 0 < tiles // 8 % 32 <= 15 and all(Q.f8_default_schedule(M, N, K, out_dtype=t).tile == 2 for t in (BF, F32))
@@ -260,11 +260,37 @@ def test_last_rounds_exact(M, N, K):
     assert torch.equal(Q.linear_f8(x, xs, pw), ref.float().bfloat16())
 
 
-@pytest.mark.parametrize("counts", [[900, 13, 1200, 87], [1, 0, 1900, 300], [550, 550, 550, 550]])
-def test_grouped_last_rounds_exact(counts):
+@pytest.mark.parametrize("M,N,K", [(4096, 4090, 1184), (4500, 4100, 800), (5000, 4100, 1184), (8300, 2052, 1184), (4700, 4096, 1184)])
+def test_tall_tiles_exact(M, N, K):
+    """Tiles of 256 x 256: whole rounds, a last one cut in two or in four, a last block of at most half the rows."""
+    Q, g = _Q(), _gen(M + N + K)
+    assert Q.f8_default_schedule(M, N, K).tile == 8
+    x, xs = R.activations(g, M, K, True)
+    w, ws = R.weights(g, (N, K), True)
+    b = torch.randint(-4, 5, (N,), generator=g, device="cuda").bfloat16()
+    ref = (x.to(D) * R.spread_rows(xs, K)) @ R.dense_weight(w, ws).t() + b.to(D)
+    out = torch.full((M + 3, N), 7.0, device="cuda", dtype=BF)
+    assert torch.equal(Q.linear_f8(x, xs, Q.pack_f8(w, ws), bias=b, out=out[:M]), ref.float().bfloat16())
+    assert bool((out[M:] == 7.0).all())
+
+
+def test_tall_tiles_against_64_bits():
+    Q, M, N, K = _Q(), 4500, 4100, 1184
+    g = _gen(8)
+    assert Q.f8_default_schedule(M, N, K).tile == 8
+    x, xs = R.activations(g, M, K)
+    w, ws = R.weights(g, (N, K))
+    ref = (x.to(D) * R.spread_rows(xs, K)) @ R.dense_weight(w, ws).t()
+    tol = _product_tol(x, xs, w, ws) + _group_tol(x, xs, w, ws)
+    _close(Q.linear_f8(x, xs, Q.pack_f8(w, ws)), ref, tol * (1 + H) + H * ref.abs(), "tall")
+
+
+@pytest.mark.parametrize("counts,tile", [([900, 13, 1200, 87], 2), ([1, 0, 1900, 300], 2), ([550, 550, 550, 550], 2),
+                                         ([4000, 100, 300, 130], 8), ([2300, 0, 2300, 1], 8), ([1200, 1100, 1300, 1250], 8)])
+def test_grouped_last_rounds_exact(counts, tile):
     Q, N, K, T = _Q(), 4100, 1184, sum(counts)
     g = _gen(T)
-    assert Q.f8_default_schedule(T, N, K, 4).tile == 2
+    assert Q.f8_default_schedule(T, N, K, 4).tile == tile
     x, xs = R.activations(g, T, K, True)
     w, ws = R.weights(g, (4, N, K), True)
     out = torch.full((T + 5, N), 7.0, device="cuda", dtype=BF)
