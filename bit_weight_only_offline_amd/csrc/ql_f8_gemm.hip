@@ -584,11 +584,11 @@ constexpr int NUM_CFGS = 9, FIRST_TILE = 2, TALL_TILE = 8;
 // loads, stores); and what a round of 256 workgroups after the first takes of either, less where several share a unit,
 // more where the operands of more workgroups pass through the caches.  For results in bf16 and, through the bf16 cores,
 // in float32.  Fitted to 60 sizes each, 20 to 8192 x 4096 x 14336, 14336 x 4096, 4096 x 4096, 5001 x 4128 and 2048 x
-// 2048, every schedule in one to eight splits, and in bf16 the large tiles' to 64 of 300 to 32768 rows: the choice was within
-// 10% of the fastest at each, 1% at the median, and 14% where a grouped product's rows fill its blocks, which cannot be known.
+// 2048, every schedule in one to eight splits, and in bf16 the tiles of 256 columns again to 64 of 200 to 32768 rows: the
+// choice was within 6% of the fastest at each, 1% at the median.
 struct F8Rate { float block, tile, tile_more, block_more; };
 constexpr F8Rate RATES[2][NUM_CFGS] = {
-    {{0.105f, 5.1f, 0.18f, 1.11f}, {0.105f, 5.1f, 0.18f, 1.11f}, {0.87f, 6.6f, 0.8f, 1.05f}, {0.433f, 5.7f, 0.09f, 1.54f},
+    {{0.105f, 5.1f, 0.18f, 1.11f}, {0.105f, 5.1f, 0.18f, 1.11f}, {0.87f, 6.6f, 0.8f, 1.15f}, {0.433f, 5.7f, 1.1f, 1.45f},
      {0.296f, 5.6f, 0.12f, 1.05f}, {0.20f, 5.0f, 0.36f, 1.04f}, {0.20f, 5.0f, 0.0f, 1.09f}, {0.104f, 5.15f, 0.1f, 1.2f},
      {1.77f, 7.2f, 1.0f, 0.97f}},
     {{0.086f, 6.3f, 0.01f, 1.49f}, {0.086f, 6.3f, 0.01f, 1.49f}, {1.195f, 18.1f, 0.84f, 1.2f}, {0.629f, 12.6f, 0.24f, 1.73f},

