@@ -6,8 +6,10 @@
 // rounding either, and float32 holds the sums.  The scale of a block multiplies what 128 channels have summed
 // to.  Rather than a second set of sums, which registers have no room for, the running sums are kept in
 // units of the current block's scale: between two blocks they are multiplied by the ratio of the scales, and
-// at the end by the last.  Powers of two go into the codes' conversion, exactly, so the ratios lie
-// between 1/2 and 2 and cannot overflow.
+// at the end by the last.  Powers of two go into the codes' conversion, as far as that is exact: from 2^-124 to 2^119 a
+// code times the power is a bf16 number (2^-9 times the least is bf16's smallest, which the matrix cores keep; 448 times the
+// largest is finite).  So the unit left is between 1 and 2 for scales in that range, down to 2^-2 for other normal ones and
+// 2^-25 for subnormal ones, and below 2^9: sums up to 2^102 overflow at no scale.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -27,7 +29,7 @@ __device__ inline f32x4 mma(const u32x4 &a, const u32x4 &b, const f32x4 &c) {
 }
 
 // A block's scale as mantissa and power of two, the ratio of the sums' unit before to it, and how its codes are
-// taken apart.  Scales below float32's normal range keep the least power and a smaller mantissa; NaN and infinity are
+// taken apart.  Scales outside the powers' range have a smaller or larger mantissa; NaN and infinity are
 // mantissas.  A block with the scale 0 leaves the unit as it is, and its codes are taken as zeros.
 struct Scale {
     float mantissa, power, ratio;
@@ -35,14 +37,12 @@ struct Scale {
 };
 __device__ inline Scale split_scale(float s, float before) {
     asm("" : "+v"(s));                                     // selections, where a uniform value would make branches
-    const uint32_t b = __float_as_uint(s), e = (b >> 23) & 0xFFu;
-    const bool none = s == 0.0f, tiny = e == 0u, special = e == 0xFFu;
+    const uint32_t e = min(max((__float_as_uint(s) >> 23) & 0xFFu, 127u - 124u), 127u + 119u);
+    const bool none = s == 0.0f;
     Scale r;
-    r.mantissa = tiny ? s * 8.507059173023462e37f          // 2^126
-                      : special ? s : __uint_as_float((b & 0x807FFFFFu) | 0x3F800000u);
-    r.mantissa = none ? before : r.mantissa;
-    r.power = tiny ? 1.1754943508222875e-38f : special ? 1.0f : __uint_as_float(e << 23);   // 2^-126
-    r.ratio = before / r.mantissa;
+    r.power = __uint_as_float(e << 23);
+    r.mantissa = none ? before : s * __uint_as_float((254u - e) << 23);
+    r.ratio = none ? 1.0f : before / r.mantissa;           // an infinite unit by itself would be NaN
     r.lo = none ? 0x0C0C0C0Cu : 0x05010400u;
     r.hi = none ? 0x0C0C0C0Cu : 0x07030602u;
     return r;

@@ -557,7 +557,9 @@ ql_status qlinear_f8_unpack(int64_t E, int64_t N, int64_t K, const void *packed,
  * 16-byte aligned.  Neither dy nor the codes are rounded.  Its workspace holds partial sums of split channels,
  * and a copy of dy where N is not a multiple of eight.
  *
- * The product of two scales is formed in float32.
+ * The product of two scales is formed in float32, so it should be a normal float32 number or 0.  The backward pass takes
+ * weight scales of every size and sign; next to a subnormal one its sums may overflow from 2^102 on.  There a block
+ * with the scale 0 adds nothing, whatever its codes; a NaN or infinite scale leaves NaN or infinities in its columns.
  *
  * qlinear_f8_default_schedule: tile (rows x outputs of a workgroup) and splits of the summed dimension (out_dtype is
  * the forward product's, bf16 for the backward one):
