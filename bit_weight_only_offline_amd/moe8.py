@@ -229,6 +229,8 @@ def _forward(codes, scales, pw, counts, bias, out_dtype, out, workspace):
     _need(out_dtype in _DTYPES, "out_dtype must be bfloat16 or float32")
     lead, M, codes, scales = _rows(codes, scales, pw.K, pw.device)
     bias = _bias(bias, pw.E * pw.N, pw)
+    if bias is not None and counts is not None and bias.shape != (pw.E, pw.N):
+        _fail(f"bias must be {(pw.E, pw.N)}")
     out = _out(out, (*lead, pw.N), out_dtype, pw.device)
     need = f8_workspace_bytes(M, pw.N, pw.K, E, out_dtype)
     ws = _space(workspace, need, pw.device)
