@@ -68,7 +68,7 @@ __device__ inline uint32_t widen2(uint32_t codes, float power) {
 // Gradients.  128-byte runs of the rows, their 16-byte pieces swizzled; the B operand, read P tiles ahead.
 //
 // A stage is two steps of 32 channels.  During a step the next one's codes are read and turned into operands between
-// the matrix instructions (8192 x 4096 x 14336 over 8 equal experts: 817 us, 1.18 PFLOP/s, the matrix cores busy half of the
+// the matrix instructions (8192 x 4096 x 14336 over 8 equal experts: 812 us, 1.18 PFLOP/s, the matrix cores busy half of the
 // time; 934 while branches in the loop let the compiler move the decoding behind them, and 636 without the loads: they
 // are what the wavefronts wait for, a quarter of their time).  A barrier before each step: the first of a stage frees the stage before it, whose place
 // takes the loads of the stage after next; the second waits for the next stage.
@@ -305,7 +305,12 @@ constexpr int NUM_CFGS = 4;
 // Microseconds that a compute unit takes for a block of 128 channels, and for a tile besides (start, first loads, stores),
 // and what a round of 256 workgroups after the first takes of either, less where several share a unit.  Fitted to 84
 // sizes, 1 to 8192 x 4096 x 14336, 14336 x 4096, 4096 x 4096, 5000 x 4128, 2048 x 2048 and 1024 x 8192, every tile in
-// one to twelve splits; the choice was within 8% of the fastest at each.  Tiles of 128 rows were the fastest at none.
+// one to twelve splits.  Tiles of 128 rows were the fastest at none.  Of 66 sizes of the same layers, 1 to 4096 rows, the
+// choice is the fastest at the median and loses more than 9% at two: 333 x 4096 x 14336, where the 16-row tile's second
+// round is taken for too short (94 us against 60 with 64 rows), and 1400 x 5001 x 4128 (94 against 84).  Grouped products have no
+// sizes in the fit: over 8 experts of 4096 x 14336, 512 rows take 172 us (64-row tiles 98), 2048 rows 240 (256-row 220).  A
+// grouped product is not split, so that few rows leave most compute units idle: one row over 8 experts of 14336 x 4096
+// takes 97 us, where the plain product in splits takes 18.
 struct BackRate { float block, tile, tile_more, block_more; };
 constexpr BackRate RATES[NUM_CFGS] = {
     {3.19f, 8.0f, 1.07f, 0.85f}, {1.19f, 5.2f, 0.05f, 0.74f}, {0.91f, 4.9f, 0.01f, 0.67f}, {0.69f, 4.4f, 0.19f, 0.4f},

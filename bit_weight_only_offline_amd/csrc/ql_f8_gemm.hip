@@ -519,7 +519,7 @@ constexpr int large_ring() { return MT == 16 ? 2 : (MT == 8 ? (NT == 2 ? 3 : 4) 
 // Its blocks of at most half the rows take the tile of half the rows (1 to 3% of ragged grouped products).  A workgroup fills a compute unit, so an XCD's 32 take the tiles of its run in rounds, and
 // a last round of few tiles would leave most of them idle for as long as a whole one takes: its tiles are cut in two (half the
 // rows) where they are at most 16, in four (half the columns too) where they are at most 8.  2176 x 4096 x 14336: 186 -> 143
-// us, 2900: 192 -> 170, 4500: 291 -> 263; 8192 ragged rows over 8 experts 564 -> 521.
+// us, 2900: 192 -> 170, 4500: 291 -> 263; 8192 ragged rows over 8 experts 564 -> 525.
 constexpr int XCD_UNITS = 32;
 __host__ __device__ constexpr int last_parts(int tiles) { return tiles <= XCD_UNITS / 4 ? 4 : (tiles <= XCD_UNITS / 2 ? 2 : 1); }
 constexpr int LAST_MORE = 3 * XCD_UNITS / 4;               // workgroups that cutting adds to an XCD's, at most
@@ -584,14 +584,21 @@ constexpr int NUM_CFGS = 9, FIRST_TILE = 2, TALL_TILE = 8;
 // loads, stores); and what a round of 256 workgroups after the first takes of either, less where several share a unit,
 // more where the operands of more workgroups pass through the caches.  For results in bf16 and, through the bf16 cores,
 // in float32.  Fitted to 60 sizes each, 20 to 8192 x 4096 x 14336, 14336 x 4096, 4096 x 4096, 5001 x 4128 and 2048 x
-// 2048, every schedule in one to eight splits, and in bf16 the tiles of 256 columns again to 64 of 200 to 32768 rows: the
-// choice was within 6% of the fastest at each, 1% at the median.
-struct F8Rate { float block, tile, tile_more, block_more; };
+// 2048, every schedule in one to eight splits, and in bf16 the tiles of 256 columns again to 64 of 200 to 32768 rows.
+// The rates of float32 and of the small tiles were fitted before scales came in panels and last rounds were cut.
+//
+// How the choice compares with the fastest of all schedules, at 60 sizes of the same layers, 20 to 4096 rows: the median is
+// the fastest itself.  To bf16 it loses more than 6% at two, 48 x 4096 x 14336 (17.9 against 16.3 us) and 64 x 14336 x 4096
+// (13.7 against 12.7); to float32 at two, 33 x 4096 x 4096 (11.4 against 9.5) and 333 x 4096 x 14336 (61.5 against 55.5).
+// Grouped products have no sizes in the fit, and the model has no term for the bytes of the experts' weights: 512 equal
+// rows over 8 experts of 4096 x 14336 take 110 us, 64 x 128 tiles would 85 (to float32 123 and 91), 8192 rows to float32 960
+// against 846 with 128 x 256; 8192 rows to bf16, and 64 experts of 4096 x 7168, take the fastest.
+struct F8Rate { float block, tile, tile_more, block_more; };   // zeros: not compared
 constexpr F8Rate RATES[2][NUM_CFGS] = {
-    {{0.105f, 5.1f, 0.18f, 1.11f}, {0.105f, 5.1f, 0.18f, 1.11f}, {0.87f, 6.6f, 0.8f, 1.15f}, {0.433f, 5.7f, 1.1f, 1.45f},
+    {{0.0f, 0.0f, 0.0f, 0.0f}, {0.105f, 5.1f, 0.18f, 1.11f}, {0.87f, 6.6f, 0.8f, 1.15f}, {0.433f, 5.7f, 1.1f, 1.45f},
      {0.296f, 5.6f, 0.12f, 1.05f}, {0.20f, 5.0f, 0.36f, 1.04f}, {0.20f, 5.0f, 0.0f, 1.09f}, {0.104f, 5.15f, 0.1f, 1.2f},
      {1.77f, 7.2f, 1.0f, 0.97f}},
-    {{0.086f, 6.3f, 0.01f, 1.49f}, {0.086f, 6.3f, 0.01f, 1.49f}, {1.195f, 18.1f, 0.84f, 1.2f}, {0.629f, 12.6f, 0.24f, 1.73f},
+    {{0.0f, 0.0f, 0.0f, 0.0f}, {0.086f, 6.3f, 0.01f, 1.49f}, {1.195f, 18.1f, 0.84f, 1.2f}, {0.629f, 12.6f, 0.24f, 1.73f},
      {0.421f, 7.3f, 0.63f, 0.79f}, {0.337f, 5.6f, 0.53f, 1.04f}, {0.312f, 6.5f, 0.17f, 0.93f}, {0.169f, 6.2f, 0.14f, 1.05f},
      {0.0f, 0.0f, 0.0f, 0.0f}},
 };
@@ -646,7 +653,10 @@ hipError_t launch_tiles(const F8Args &a, hipStream_t st) {
 
 // Up to 16 rows, an expert's on average, stream the weight through registers, a workgroup one column tile as long as
 // that gives a compute unit at most one (4096 x 14336, one row: 11.4 us against 12.7 with two; 8192 x 8192, eight rows:
-// 13.4 against 12.9; 8 experts of 28672 x 4096, 32 rows: 156 against 149).  More take the schedule and the split of
+// 13.4 against 12.9; 8 experts of 28672 x 4096, 32 rows: 156 against 149).  An expert of more than 16 rows then has its
+// weight read again for each further 16, which costs where counts are uneven and the average is near 16: 8 ragged experts of
+// 28672 x 4096, 32, 64 and 128 rows, 134, 153 and 216 us (tiles of 32 x 64: 139, 142 and 148); 64 of 4096 x 7168, 256, 512 and
+// 1024 rows, 285, 297 and 373 (64 x 256: 289, 293 and 302).  More take the schedule and the split of
 // the input dimension whose time is least by the measured rates.  A grouped product's row blocks are taken to
 // be half a block an expert more than its rows fill; it is not split.
 F8Plan make_f8_plan(const F8Layout &L, int64_t M, bool grouped, bool f32) {

@@ -9,7 +9,8 @@
 // read once, in 16-byte pieces, and each result written once.  Sixteen lanes hold a block, eight
 // values each, so its maximum takes four exchanges inside a wavefront and no LDS.  4096 x 14336 in bf16: the gradient
 // 103 us (5.7 TB/s), the way back 31 (5.7), quantising 40 (4.5), with the SwiGLU 71 (4.2): there a value's operations
-// take nearly as long as its bytes (float32, with twice the bytes: 49 and 97, 6.0 and 5.4 TB/s).
+// take nearly as long as its bytes (float32, with twice the bytes: 49 and 97, 6.0 and 5.4 TB/s).  A weight of that size:
+// quantising 40 us from bf16 (4.5 TB/s) and 55 from float32 (5.4), packing and unpacking 20 each (5.8).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -259,7 +259,10 @@ def linear_f8(codes: torch.Tensor, scales: torch.Tensor, pw: BlockWeight, bias: 
               workspace: torch.Tensor | None = None) -> torch.Tensor:
     """y[..., N] = sum over blocks of 128 inputs of (codes . w^T) * scales * weight scales, plus bias.
 
-    codes float8_e4m3fn [..., K], scales float32 [..., ceil(K / 128)], bias bf16 [N]; out_dtype bf16 or float32."""
+    codes float8_e4m3fn [..., K], scales float32 [..., ceil(K / 128)], bias bf16 [N]; out_dtype bf16 or float32.  Sums are
+    float32 in an order that the number of rows sets.  To bf16, products of more than 16 rows may go through the 8-bit matrix
+    cores, which drop what lies below 2^-13 of the largest of eight products (1.5e-5 of a sum of normal values; its rounding
+    to bf16 is 1.7e-3); out_dtype=torch.float32, and fewer rows, keep it."""
     _weight(pw, False)
     return _forward(codes, scales, pw, None, bias, out_dtype, out, workspace)
 
@@ -267,7 +270,7 @@ def linear_f8(codes: torch.Tensor, scales: torch.Tensor, pw: BlockWeight, bias: 
 def linear_f8_backward(dy: torch.Tensor, pw: BlockWeight, out: torch.Tensor | None = None,
                        workspace: torch.Tensor | None = None) -> torch.Tensor:
     """dx bf16 [..., K] for dy bf16 [..., N]: the gradient of the dequantised activations.  The gradient of a
-    bias is dy summed over the tokens."""
+    bias is dy summed over the tokens.  A weight block with the scale 0 adds nothing, whatever its codes."""
     _weight(pw, False)
     return _backward(dy, pw, None, out, workspace)
 
@@ -277,7 +280,8 @@ def grouped_linear_f8(codes: torch.Tensor, scales: torch.Tensor, pw: BlockWeight
                       out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """linear_f8() of rows [T, K] in expert order, each with its own expert's weight: expert e owns the next
     tokens_per_expert[e] rows, an int32 device tensor [E]; bias bf16 [E, N].  Rows past the sum of the counts are left
-    as they are in `out` (uninitialised when allocated)."""
+    as they are in `out` (uninitialised when allocated).  The 8-bit matrix cores may be taken, as by linear_f8(),
+    where there are more than 16 rows to an expert on average."""
     _weight(pw, True)
     _tensor(codes, "codes", _CODES, pw.device)
     _need(codes.dim() == 2, f"codes must be [T, {pw.K}]")

@@ -597,6 +597,7 @@ ql_status qlinear_f8_backward(const void *dy, int64_t M, const int32_t *tokens_p
  * qlinear_combine_backward: dy[rows[t, j]] = weights[t, j] dout[t],
  *   dweights[t, j] = sum over d of dout[t, d] y[rows[t, j], d], 0 for a slot without a place
  * Rows outside 0 .. T k - 1 are skipped; rows of out, codes, scales and dy that no slot names are left as they are.
+ * Outputs overlap no input, but dy may be y.
  * bf16 or float32, k at most 256, D at most 2^24, T k below 2^31.  T = 0 is a no-op.
  */
 ql_status qlinear_expert_order_workspace_bytes(int64_t n, int64_t E, size_t *bytes);
